@@ -15,3 +15,7 @@ from .sparsepr import (  # noqa: F401
     host_workspace, test_fill, test_topk, test_partition_trace, load_library, workspace_size, row_errors, launch_count,
     kernel_timing, kernel_timing_read,
 )
+from .selected import (  # noqa: F401
+    ROTARY_HALF, ROTARY_INTERLEAVED, RotaryPlan, SelectConfig, block_attention, key_means, rotary, rotary_frequencies,
+    rotary_plan, select_blocks, selected_attn, selected_attn_backward, selected_workspace,
+)

@@ -1,0 +1,92 @@
+// Launch interface of the rotary and selected-block attention kernels (internal).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+#include "common.cuh"
+
+namespace spr {
+
+// A [batch, heads, rows, d] tensor with contiguous rows; strides in elements.
+struct View {
+  void* p;
+  long long sb, sh, sn;
+};
+
+struct RotaryArgs {
+  View x[2], y[2];  // q and k (h[1] = 0: no second tensor)
+  int h[2];
+  int Bt, n, d;
+  int first, rot;   // the rotated dims [first, first + rot)
+  bool half, f32, inverse;
+  int axes, pairs[4];
+  float factor;
+  const double* freqs;  // [rot / 2] radians per position
+  const int* positions;
+  long long pos_sb, pos_sn;
+  bool copy_rest;        // set by the launcher
+  int heads_per_thread;  // set by the launcher
+};
+cudaError_t launch_rotary(const RotaryArgs& a, cudaStream_t st);
+
+// Tokens of one sub-slice of the selection lists (one CTA's bit masks).
+constexpr int kSub = 512;
+// Blocks per head that the lists' shared-memory masks hold.
+constexpr int kMaxBlocks = 2048;
+
+// One work item of the attention kernels: rows [r0, r0 + rows) of the entries of key block g,
+// whose first entry is `off` of its region's list; row r is query head r % group of entry r / group.
+struct Unit {
+  int g, off, r0, rows;
+};
+
+struct SelArgs {
+  bool f32, causal;
+  int Bt, Hq, Hk, group, n, nk, d, block, nb, top;
+  int n_first, n_local;
+  int q_start0;          // position of query 0 where q_start is null
+  const int* kv_len;     // [Bt] or null (nk)
+  const int* q_start;    // [Bt] or null
+  float scale;
+  View q, k, v, o, go, gq, gk, gv;
+  const int* sel;        // [Bt, Hk, n, top]
+  float* lse;            // [Bt, Hq, n]
+  const float* means;    // [Bt, Hk, nb, d]
+  int* status;
+  // lists: per region (batch, key head, slice of `slice` tokens), `slices` regions per head
+  int slice, slices;
+  int subs;              // sub-slices of a slice
+  int* offs;             // [regions][nb][subs]: counts, then first entries
+  int* list;             // [regions][slice * top] tokens, block by block, ascending
+  int* inv;              // [Bt, Hk, n, top] entry of (token, slot) in its region, or -1
+  int unit_rows, unit_cap;
+  Unit* units;           // [regions][unit_cap]
+  int* n_units;          // [regions]
+  int2* blk;             // [regions][nb] {segments, first slot of the segment sums}
+  int* ticket;           // dynamic work counter of the persistent kernels
+  // partial rows of one chunk of regions
+  float* part;           // [chunk regions][slice * top * group][d]
+  float2* ml;            // forward: running maximum (log2 units) and sum of each partial row
+  float* delta;          // backward: sum of o * go per query row
+  float* seg;            // backward: [chunk regions][seg_cap][2][block][d] sums of split blocks
+  int seg_cap;
+};
+
+// Device limits of one batch element.
+__device__ __forceinline__ int kv_len_of(const SelArgs& a, int b) {
+  return a.kv_len == nullptr ? a.nk : min(max(a.kv_len[b], 0), a.nk);
+}
+__device__ __forceinline__ int q_start_of(const SelArgs& a, int b) {
+  return a.q_start == nullptr ? a.q_start0 : min(max(a.q_start[b], -(1 << 29)), 1 << 29);
+}
+
+cudaError_t launch_key_means(const SelArgs& a, const int* kv_start, int max_new, float* means, cudaStream_t st);
+cudaError_t launch_select(const SelArgs& a, int* sel, cudaStream_t st);
+cudaError_t launch_lists(const SelArgs& a, cudaStream_t st);
+// One chunk of `count` regions starting at region `first`.
+cudaError_t launch_selected_forward(const SelArgs& a, int first, int count, cudaStream_t st);
+cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cudaStream_t st);
+cudaError_t launch_delta(const SelArgs& a, cudaStream_t st);
+
+}  // namespace spr

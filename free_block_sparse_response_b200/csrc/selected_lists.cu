@@ -1,0 +1,194 @@
+// Selected-block attention: from each query's selected blocks to each block's queries.
+//
+// The attention kernels work block by block: one key block against 128 of the queries that
+// selected it, so that a key tile is read once for many queries although every query has its
+// own selection.  This file turns the selection [token][slot] -> block around.  Tokens are
+// cut into slices (regions: batch x key head x slice), slices into sub-slices of 512 tokens:
+//   count    one CTA per sub-slice sets one bit per (block, token) in shared memory and counts
+//            each block's bits;
+//   scan     one CTA per region turns the counts into first entries, block by block, and
+//            cuts every block's rows into work units;
+//   scatter  one CTA per sub-slice sets the bits again; an entry's place is the block's first
+//            entry plus the set bits before its token.
+// Bits make the order independent of the threads' timing: entries of a block ascend by token,
+// so every sum over a block's queries is formed in the same order in each run.  All three are
+// bound by latency (the selection is 4 bytes per query and slot, read twice).
+#include <cuda_runtime.h>
+
+#include "common.cuh"
+#include "selected.cuh"
+
+namespace spr {
+namespace {
+
+constexpr int kWords = kSub / 32;
+
+// The valid blocks of a token's row: ascending, in [0, nb), up to the first negative entry.
+// An entry out of range or not above all earlier ones is reported and skipped; a block with
+// no key that the token may attend to is skipped.
+template <typename F>
+__device__ __forceinline__ void each_selected(const SelArgs& a, const int* row, int limit_block, F f) {
+  int prev = -1;
+  bool bad = false;
+  for (int j = 0; j < a.top; ++j) {
+    const int g = __ldg(row + j);
+    if (g < 0) break;
+    if (g >= a.nb || g <= prev) {
+      bad = true;
+      continue;
+    }
+    prev = g;
+    if (g <= limit_block) f(j, g);
+  }
+  if (bad) record_error(a.status, kErrInvalidArg);
+}
+
+// Last block that holds a key token t may attend to (-1: none).
+__device__ __forceinline__ int limit_block(const SelArgs& a, int b, int t) {
+  int last = kv_len_of(a, b) - 1;
+  if (a.causal) last = min(last, q_start_of(a, b) + t);
+  return last < 0 ? -1 : last / a.block;
+}
+
+__device__ __forceinline__ void set_bits(const SelArgs& a, uint32_t* mask, int z, int t0) {
+  for (int i = threadIdx.x; i < a.nb * kWords; i += blockDim.x) mask[i] = 0;
+  __syncthreads();
+  const int b = z / a.Hk;
+  for (int i = threadIdx.x; i < kSub && t0 + i < a.n; i += blockDim.x) {
+    const int t = t0 + i;
+    each_selected(a, a.sel + (static_cast<size_t>(z) * a.n + t) * a.top, limit_block(a, b, t),
+                  [&](int, int g) { atomicOr(&mask[g * kWords + (i >> 5)], 1u << (i & 31)); });
+  }
+  __syncthreads();
+}
+
+__global__ void __launch_bounds__(256) count_kernel(const SelArgs a) {
+  extern __shared__ uint32_t mask[];  // [nb][kWords]
+  const int z = blockIdx.y, s = blockIdx.x;  // sub-slice s of the head's tokens
+  set_bits(a, mask, z, s * kSub);
+  const int region = z * a.slices + s / a.subs, ls = s % a.subs;
+  for (int g = threadIdx.x; g < a.nb; g += blockDim.x) {
+    int c = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) c += __popc(mask[g * kWords + w]);
+    a.offs[(static_cast<size_t>(region) * a.nb + g) * a.subs + ls] = c;
+  }
+}
+
+// Exclusive prefix sum of one value per thread over a block of 512 threads; total in `sum`.
+__device__ __forceinline__ int block_scan(int v, int& sum, int* s_warp) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int w = lane < 16 ? s_warp[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, w, o);
+      if (lane >= o) w += y;
+    }
+    if (lane < 16) s_warp[lane] = w;
+  }
+  __syncthreads();
+  const int before = warp > 0 ? s_warp[warp - 1] : 0;
+  sum = s_warp[15];
+  __syncthreads();
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
+  __shared__ int s_warp[16];
+  const int region = blockIdx.x;
+  const int s = region % a.slices;
+  // sub-slices of this region that hold tokens
+  const int live = min(a.subs, ceil_div(a.n - s * a.slice, kSub));
+  int entry0 = 0, unit0 = 0, slot0 = 0;
+  for (int g0 = 0; g0 < a.nb; g0 += 512) {
+    const int g = g0 + threadIdx.x;
+    int* c = a.offs + (static_cast<size_t>(region) * a.nb + g) * a.subs;
+    int cnt = 0;
+    if (g < a.nb)
+      for (int i = 0; i < live; ++i) cnt += c[i];
+    int sum;
+    int off = entry0 + block_scan(cnt, sum, s_warp);
+    entry0 += sum;
+    const int rows = cnt * a.group;
+    const int nu = ceil_div(rows, a.unit_rows);
+    const int u = unit0 + block_scan(nu, sum, s_warp);
+    unit0 += sum;
+    const int slots = nu > 1 ? nu : 0;
+    const int slot = slot0 + block_scan(slots, sum, s_warp);
+    slot0 += sum;
+    if (g < a.nb) {
+      for (int i = 0; i < nu; ++i)
+        a.units[static_cast<size_t>(region) * a.unit_cap + u + i] =
+            Unit{g, off, i * a.unit_rows, min(a.unit_rows, rows - i * a.unit_rows)};
+      a.blk[static_cast<size_t>(region) * a.nb + g] = make_int2(nu, slot);
+      for (int i = 0; i < live; ++i) {
+        const int x = c[i];
+        c[i] = off;
+        off += x;
+      }
+    }
+  }
+  if (threadIdx.x == 0) {
+    a.n_units[region] = unit0;
+    if (region == 0) *a.ticket = 0;
+  }
+}
+
+__global__ void __launch_bounds__(256) scatter_kernel(const SelArgs a) {
+  extern __shared__ uint32_t mask[];  // [nb][kWords], then the words' first entries [nb][kWords]
+  const int z = blockIdx.y, s = blockIdx.x, t0 = s * kSub;
+  set_bits(a, mask, z, t0);
+  uint16_t* before = reinterpret_cast<uint16_t*>(mask + a.nb * kWords);
+  for (int g = threadIdx.x; g < a.nb; g += blockDim.x) {
+    int c = 0;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      before[g * kWords + w] = static_cast<uint16_t>(c);
+      c += __popc(mask[g * kWords + w]);
+    }
+  }
+  __syncthreads();
+  const int region = z * a.slices + s / a.subs, ls = s % a.subs, b = z / a.Hk;
+  int* list = a.list + static_cast<size_t>(region) * a.slice * a.top;
+  for (int i = threadIdx.x; i < kSub && t0 + i < a.n; i += blockDim.x) {
+    const int t = t0 + i;
+    const size_t row = (static_cast<size_t>(z) * a.n + t) * a.top;
+    for (int j = 0; j < a.top; ++j) a.inv[row + j] = -1;
+    each_selected(a, a.sel + row, limit_block(a, b, t), [&](int j, int g) {
+      const int w = g * kWords + (i >> 5);
+      const int e = __ldg(a.offs + (static_cast<size_t>(region) * a.nb + g) * a.subs + ls) + before[w] +
+                    __popc(mask[w] & ((1u << (i & 31)) - 1u));
+      list[e] = t;
+      a.inv[row + j] = e;
+    });
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_lists(const SelArgs& a, cudaStream_t st) {
+  const int heads = a.Bt * a.Hk, subs = ceil_div(a.n, kSub);
+  if (heads > 65535) return cudaErrorInvalidValue;
+  const size_t mask = sizeof(uint32_t) * a.nb * kWords, both = mask + sizeof(uint16_t) * a.nb * kWords;
+  if (both > 227 * 1024) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e != cudaSuccess) return e;
+  count_kernel<<<dim3(subs, heads), 256, mask, st>>>(a);
+  if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
+  scan_kernel<<<heads * a.slices, 512, 0, st>>>(a);
+  if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
+  scatter_kernel<<<dim3(subs, heads), 256, both, st>>>(a);
+  return counted(cudaGetLastError(), 1);
+}
+
+}  // namespace spr

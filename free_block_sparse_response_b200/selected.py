@@ -1,0 +1,368 @@
+"""Rotary positions and attention over the key blocks that each query selects.
+
+Binding of the operators beside the SparsePR call (include/sparsepr.h): argument marshalling
+only, as in ``sparsepr.py``.  Tensors are [batch, heads, rows, d] CUDA tensors with
+contiguous rows and any strides of whole 16-byte units (a transposed [batch, rows, heads, d]
+buffer works); every call runs on the tensors' device and the current stream there.
+
+    plan = spr.rotary_plan(128, device, base=1e4)
+    q, k = spr.rotary(plan, positions, q, k)             # positions [batch, rows, 1] int32
+    cfg = spr.SelectConfig(block=128, top=16, causal=True)
+    out = spr.block_attention(q, k, v, cfg)              # means, selection and attention
+
+or, call by call, with a workspace that the caller keeps:
+
+    ws = spr.selected_workspace(q, k, cfg, backward=True)
+    means = spr.key_means(k, cfg.block)
+    sel = spr.select_blocks(q, means, k.shape[2], cfg, ws)
+    out, lse = spr.selected_attn(q, k, v, sel, cfg, ws)
+    dq, dk, dv = spr.selected_attn_backward(dout, q, k, v, out, lse, sel, cfg, ws)
+
+For a cache, ``kv_len`` [batch] holds each sequence's length and ``q_start`` [batch] the key
+position of its first query; after appending keys, ``key_means(..., kv_start=, max_new=,
+out=means)`` renews the touched blocks' means.
+"""
+from __future__ import annotations
+
+import ctypes
+import dataclasses
+import math
+from typing import NamedTuple, Optional, Sequence
+
+import torch
+
+from . import sparsepr as _s
+
+ROTARY_HALF, ROTARY_INTERLEAVED = 0, 1
+
+
+class _CView(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
+
+
+class _CRotary(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int32), ("first", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("axes", ctypes.c_int32), ("pairs", ctypes.c_int32 * 4), ("inverse", ctypes.c_int32),
+                ("factor", ctypes.c_float)]
+
+
+class _CSelected(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "Bt", "Hq", "Hkv", "Nq", "Nk", "d", "block", "top", "causal",
+                                              "n_first", "n_local")] + \
+               [("scale", ctypes.c_float), ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p)]
+
+
+def signatures():
+    """ctypes result and argument types of these entry points."""
+    vp, i32, i64, v = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(_CView)
+    p = ctypes.POINTER(_CSelected)
+    return {
+        "sparsepr_rotary": (ctypes.c_int, [ctypes.POINTER(_CRotary), vp, vp, i64, i64, ctypes.c_int, i32, i32, i32, i32, v,
+                                           v, i32, v, v, vp]),
+        "sparsepr_selected_workspace_size": (ctypes.c_size_t, [p, ctypes.c_int]),
+        "sparsepr_key_means": (ctypes.c_int, [p, v, vp, i32, vp, vp]),
+        "sparsepr_select_blocks": (ctypes.c_int, [p, v, vp, vp, vp, vp]),
+        "sparsepr_selected_attn": (ctypes.c_int, [p, v, v, v, vp, v, vp, vp, vp]),
+        "sparsepr_selected_attn_backward": (ctypes.c_int, [p, v, v, v, v, v, vp, vp, v, v, v, vp, vp]),
+    }
+
+
+def _view(t: Optional[torch.Tensor]):
+    if t is None:
+        return None
+    # a dimension of one row has no stride to speak of
+    return ctypes.byref(_CView(t.data_ptr(), *(s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride()))))
+
+
+def _need_rows(name: str, t: torch.Tensor, shape=None, like: Optional[torch.Tensor] = None) -> None:
+    """A [batch, heads, rows, d] CUDA tensor with contiguous rows (of the given shape, type and device)."""
+    if not t.is_cuda:
+        raise ValueError("SparsePR tensors must live on a CUDA device")
+    if t.dim() != 4 or t.stride(3) != 1:
+        raise ValueError(f"{name} must be [batch, heads, rows, d] with contiguous rows")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have the type and device of the other tensors")
+    _s._dtype_code(t)
+
+
+def _need_flat(name: str, t: Optional[torch.Tensor], shape, dtype, device) -> None:
+    """A contiguous CUDA tensor of the given shape, type and device, or None."""
+    if t is None:
+        return
+    if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _need_out(name: str, t: torch.Tensor) -> None:
+    """No two rows of an output in one place."""
+    if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+        raise ValueError(f"{name} must not be an expanded tensor")
+
+
+def _rows_like(t: torch.Tensor) -> torch.Tensor:
+    """Empty tensor of t's shape and, unless it is expanded, memory order."""
+    if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    return torch.empty_like(t)
+
+
+def _run(device, name: str, *args) -> None:
+    with torch.cuda.device(device):
+        _s._call(name, *args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream))
+
+
+# ------------------------------------------------------------------------------ rotary
+
+class RotaryPlan(NamedTuple):
+    """What a rotation needs besides the positions (made once by ``rotary_plan``)."""
+    freqs: torch.Tensor   # [rot_dim / 2] float64: radians per step of the position
+    d: int
+    rot_dim: int
+    first: int
+    layout: int
+    sections: tuple       # pairs of each position axis
+    factor: float
+
+
+def rotary_frequencies(sections: Sequence[int], base: float = 10000.0, scaling: str = "none", scaling_factor: float = 1.0,
+                       trained_length: int = 0, slow: float = 1.0, fast: float = 32.0):
+    """(frequencies, factor) of a rotation, in 64 bits on the host: for each axis with p pairs
+    f_i = base^(-i/p), i < p, and for contexts ``scaling_factor`` s times the trained length
+
+      "linear"  f_i / s (positions interpolated)
+      "base"    the ladder of the base  base * s^(2p / (2p - 2)): the lowest frequency is divided by s
+      "ramp"    by turns r_i = trained_length f_i / (2 pi) within the trained length: f_i / s where
+                r_i <= slow, f_i where r_i >= fast, linear in r_i between; factor 0.1 ln s + 1
+    """
+    if scaling not in ("none", "linear", "base", "ramp"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    if not (math.isfinite(base) and base > 0 and math.isfinite(scaling_factor) and scaling_factor > 0):
+        raise ValueError("base and scaling_factor must be positive")
+    if scaling == "ramp" and (trained_length < 1 or not fast > slow):
+        raise ValueError("ramp scaling needs trained_length >= 1 and fast > slow")
+    freqs = []
+    for p in sections:
+        if p < 0:
+            raise ValueError("an axis cannot have a negative number of pairs")
+        b = base
+        if scaling == "base" and p > 1:
+            b = base * scaling_factor ** (2 * p / (2 * p - 2))
+        f = [b ** (-i / p) for i in range(p)]
+        if scaling == "linear":
+            f = [x / scaling_factor for x in f]
+        elif scaling == "ramp":
+            keep = [min(1.0, max(0.0, (trained_length * x / (2 * math.pi) - slow) / (fast - slow))) for x in f]
+            f = [x * g + x / scaling_factor * (1.0 - g) for x, g in zip(f, keep)]
+        freqs += f
+    factor = 0.1 * math.log(scaling_factor) + 1.0 if scaling == "ramp" and scaling_factor > 1 else 1.0
+    return freqs, factor
+
+
+def rotary_plan(d: int, device, rot_dim: Optional[int] = None, first: int = 0, layout: int = ROTARY_HALF,
+                sections: Optional[Sequence[int]] = None, freqs: Optional[torch.Tensor] = None,
+                factor: Optional[float] = None, **ladder) -> RotaryPlan:
+    """Plan for heads of d dims whose dims [first, first + rot_dim) rotate (default: all).
+    ``sections``: pairs of each position axis, for example (24, 20, 20) for the t, y and x of a
+    video grid at d = 128 (default: one axis).  Frequencies come from ``rotary_frequencies``
+    (``ladder``: base, scaling, ...) or are given as ``freqs`` [rot_dim / 2], with ``factor``."""
+    rot_dim = d - first if rot_dim is None else rot_dim
+    if rot_dim < 2 or rot_dim % 2 or first < 0 or first + rot_dim > d:
+        raise ValueError("the rotated part must be an even number of dims inside the head")
+    if layout not in (ROTARY_HALF, ROTARY_INTERLEAVED):
+        raise ValueError(f"unknown rotary layout {layout}")
+    sections = (rot_dim // 2,) if sections is None else tuple(int(s) for s in sections)
+    if not 1 <= len(sections) <= 4 or min(sections) < 0 or sum(sections) != rot_dim // 2:
+        raise ValueError("sections: one to four axes whose pairs add up to rot_dim / 2")
+    if freqs is None:
+        f, scale = rotary_frequencies(sections, **ladder)
+        freqs = torch.tensor(f, dtype=torch.float64, device=device)
+    else:
+        if ladder:
+            raise ValueError("give frequencies or a ladder's parameters, not both")
+        freqs, scale = torch.as_tensor(freqs, dtype=torch.float64, device=device).contiguous(), 1.0
+        if tuple(freqs.shape) != (rot_dim // 2,):
+            raise ValueError("freqs must hold rot_dim / 2 values")
+    return RotaryPlan(freqs, d, rot_dim, first, layout, sections, float(scale if factor is None else factor))
+
+
+def rotary(plan: RotaryPlan, positions: torch.Tensor, q: torch.Tensor, k: Optional[torch.Tensor] = None,
+           inverse: bool = False, out=None):
+    """q and k rotated by their positions, in one launch: a tensor, or a pair where k is given.
+
+    positions: int32 [batch or 1, rows, axes] (axes may be left out where there is one), last
+    dimension contiguous.  ``inverse`` rotates back: the gradient of the rotation (the factor
+    is applied in both directions).  ``out``: the output tensor or pair, which may be the input
+    itself or a strided view such as the new rows of a key cache."""
+    outs = (None, None) if out is None else tuple(out) if k is not None else (out, None)
+    for name, t in (("q", q), ("k", k)):
+        if t is not None:
+            _need_rows(name, t, (q.shape[0], t.shape[1], q.shape[2], q.shape[3]), q)
+    bt, h, n, d = q.shape
+    if d != plan.d or plan.freqs.device != q.device:
+        raise ValueError("the plan was made for another head dim or device")
+    axes = len(plan.sections)
+    if positions.dim() == 2 and axes == 1:
+        positions = positions[..., None]
+    if positions.dtype != torch.int32 or positions.device != q.device or positions.dim() != 3 or \
+            positions.shape[0] not in (1, bt) or tuple(positions.shape[1:]) != (n, axes) or \
+            (axes > 1 and positions.stride(2) != 1):
+        raise ValueError(f"positions must be int32 [{bt} or 1, {n}, {axes}] on the tensors' device")
+    res = []
+    for name, t, o in (("out of q", q, outs[0]), ("out of k", k, outs[1])):
+        if t is None:
+            res.append(None)
+            continue
+        o = _rows_like(t) if o is None else o
+        _need_rows(name, o, t.shape, t)
+        _need_out(name, o)
+        res.append(o)
+    pairs = (ctypes.c_int32 * 4)(*(plan.sections + (0,) * (4 - axes)))
+    par = _CRotary(plan.rot_dim, plan.first, plan.layout, axes, pairs, 1 if inverse else 0, plan.factor)
+    _run(q.device, "sparsepr_rotary", ctypes.byref(par), _s._p(plan.freqs), _s._p(positions),
+         positions.stride(0) if positions.shape[0] > 1 else 0, positions.stride(1), _s._dtype_code(q), bt, n, d, h, _view(q),
+         _view(res[0]), 0 if k is None else k.shape[1], _view(k), _view(res[1]))
+    return res[0] if k is None else (res[0], res[1])
+
+
+# ------------------------------------------------------------- attention over selected blocks
+
+@dataclasses.dataclass(frozen=True)
+class SelectConfig:
+    """Attention over selected key blocks: keys per block (64 or 128), blocks per query, causal
+    masking, blocks that are always selected (the first ``n_first``; causal: the query's own
+    block and the ``n_local`` - 1 before it) and the softmax scale (<= 0: 1/sqrt(d))."""
+    block: int = 128
+    top: int = 16
+    causal: bool = False
+    n_first: int = 0
+    n_local: int = 0
+    scale: float = 0.0
+
+
+def _problem(dtype_of, bt, hq, hk, nq, nk, d, cfg: SelectConfig, kv_len, q_start) -> _CSelected:
+    return _CSelected(_s._dtype_code(dtype_of), bt, hq, hk, nq, nk, d, cfg.block, cfg.top, int(bool(cfg.causal)),
+                      cfg.n_first, cfg.n_local, cfg.scale, None if kv_len is None else kv_len.data_ptr(),
+                      None if q_start is None else q_start.data_ptr())
+
+
+def _lengths(bt: int, device, kv_len, q_start) -> None:
+    _need_flat("kv_len", kv_len, (bt,), torch.int32, device)
+    _need_flat("q_start", q_start, (bt,), torch.int32, device)
+
+
+def selected_workspace(q: torch.Tensor, k: torch.Tensor, cfg: SelectConfig, backward: bool = False) -> torch.Tensor:
+    """Workspace of the calls below for tensors of these shapes (status header zeroed)."""
+    _need_rows("q", q)
+    _need_rows("k", k, (q.shape[0], k.shape[1], k.shape[2], q.shape[3]), q)
+    p = _problem(q, q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3], cfg, None, None)
+    size = int(_s.lib().sparsepr_selected_workspace_size(ctypes.byref(p), 1 if backward else 0))
+    if size == 0:
+        raise _s.SparsePRError(_s.ERR_INVALID_ARG,
+                               f"selected_workspace: {_s.lib().sparsepr_last_error().decode(errors='replace')}")
+    ws = torch.empty(size, dtype=torch.uint8, device=q.device)
+    ws[:256].zero_()
+    return ws
+
+
+def _need_ws(ws: torch.Tensor, p: _CSelected, device, backward: bool) -> None:
+    size = int(_s.lib().sparsepr_selected_workspace_size(ctypes.byref(p), 1 if backward else 0))
+    if size and (ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < size or
+                 ws.data_ptr() % 256):
+        raise ValueError("the workspace is too small for these tensors, misaligned or on another device")
+
+
+def key_means(k: torch.Tensor, block: int, kv_len: Optional[torch.Tensor] = None,
+              kv_start: Optional[torch.Tensor] = None, max_new: int = 0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Mean key of every block of ``block`` keys: [batch, heads, ceil(rows / block), d] fp32.
+    With ``kv_start`` [batch] int32 only the blocks holding keys [kv_start, kv_len) are renewed
+    in ``out`` (at most ``max_new`` keys per sequence were appended)."""
+    _need_rows("k", k)
+    bt, h, n, d = k.shape
+    _lengths(bt, k.device, kv_len, kv_start)
+    if kv_start is not None and out is None:
+        raise ValueError("kv_start renews blocks of an existing tensor: give out")
+    shape = (bt, h, -(-n // block) if block > 0 else 0, d)
+    means = torch.empty(shape, dtype=torch.float32, device=k.device) if out is None else out
+    _need_flat("out", means, shape, torch.float32, k.device)
+    p = _problem(k, bt, h, h, 1, n, d, SelectConfig(block=block, top=1), kv_len, None)
+    _run(k.device, "sparsepr_key_means", ctypes.byref(p), _view(k), _s._p(kv_start), max_new, _s._p(means))
+    return means
+
+
+def select_blocks(q: torch.Tensor, means: torch.Tensor, keys: int, cfg: SelectConfig, ws: torch.Tensor,
+                  kv_len: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Blocks of the ``keys`` keys that each query attends to: [batch, key heads, rows, top]
+    int32, ascending, then -1 (ties to the lower block; the scores are compared in 64 bits)."""
+    _need_rows("q", q)
+    bt, hq, n, d = q.shape
+    hk = means.shape[1] if means.dim() == 4 else 0
+    _need_flat("means", means, (bt, hk, -(-keys // cfg.block) if cfg.block > 0 else 0, d), torch.float32, q.device)
+    _lengths(bt, q.device, kv_len, q_start)
+    p = _problem(q, bt, hq, hk, n, keys, d, cfg, kv_len, q_start)
+    _need_ws(ws, p, q.device, False)
+    sel = torch.empty(bt, hk, n, cfg.top, dtype=torch.int32, device=q.device) if out is None else out
+    _need_flat("out", sel, (bt, hk, n, cfg.top), torch.int32, q.device)
+    _run(q.device, "sparsepr_select_blocks", ctypes.byref(p), _view(q), _s._p(means), _s._p(sel), _s._p(ws))
+    return sel
+
+
+def _attention_problem(q, k, v, sel, cfg, ws, kv_len, q_start, backward) -> _CSelected:
+    _need_rows("q", q)
+    bt, hq, n, d = q.shape
+    _need_rows("k", k, (bt, k.shape[1], k.shape[2], d), q)
+    _need_rows("v", v, k.shape, q)
+    _need_flat("sel", sel, (bt, k.shape[1], n, cfg.top), torch.int32, q.device)
+    _lengths(bt, q.device, kv_len, q_start)
+    p = _problem(q, bt, hq, k.shape[1], n, k.shape[2], d, cfg, kv_len, q_start)
+    _need_ws(ws, p, q.device, backward)
+    return p
+
+
+def selected_attn(q, k, v, sel: torch.Tensor, cfg: SelectConfig, ws: torch.Tensor,
+                  kv_len: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """Softmax attention of every query over the keys of its selected blocks: (out, lse), out
+    like q and lse [batch, heads, rows] fp32 (natural log; -inf and a zero row without keys)."""
+    p = _attention_problem(q, k, v, sel, cfg, ws, kv_len, q_start, False)
+    o = _rows_like(q) if out is None else out
+    _need_rows("out", o, q.shape, q)
+    _need_out("out", o)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if lse is None else lse
+    _need_flat("lse", lse, q.shape[:3], torch.float32, q.device)
+    _run(q.device, "sparsepr_selected_attn", ctypes.byref(p), _view(q), _view(k), _view(v), _s._p(sel), _view(o), _s._p(lse),
+         _s._p(ws))
+    return o, lse
+
+
+def selected_attn_backward(dout, q, k, v, out, lse, sel: torch.Tensor, cfg: SelectConfig, ws: torch.Tensor,
+                           kv_len: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None, dq=None,
+                           dk=None, dv=None):
+    """(dq, dk, dv) of ``selected_attn`` for the gradient of its output; the selection is fixed.
+    ``ws`` was made with ``backward=True``."""
+    p = _attention_problem(q, k, v, sel, cfg, ws, kv_len, q_start, True)
+    _need_rows("dout", dout, q.shape, q)
+    _need_rows("out", out, q.shape, q)
+    _need_flat("lse", lse, q.shape[:3], torch.float32, q.device)
+    res = []
+    for name, g, t in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        g = _rows_like(t) if g is None else g
+        _need_rows(name, g, t.shape, q)
+        _need_out(name, g)
+        res.append(g)
+    _run(q.device, "sparsepr_selected_attn_backward", ctypes.byref(p), _view(dout), _view(q), _view(k), _view(v), _view(out),
+         _s._p(lse), _s._p(sel), *(_view(g) for g in res), _s._p(ws))
+    return tuple(res)
+
+
+def block_attention(q, k, v, cfg: SelectConfig, ws: Optional[torch.Tensor] = None,
+                    kv_len: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
+                    out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Mean keys, selection and attention in one call: out like q."""
+    ws = selected_workspace(q, k, cfg) if ws is None else ws
+    means = key_means(k, cfg.block, kv_len=kv_len)
+    sel = select_blocks(q, means, k.shape[2], cfg, ws, kv_len=kv_len, q_start=q_start)
+    return selected_attn(q, k, v, sel, cfg, ws, kv_len=kv_len, q_start=q_start, out=out)[0]

@@ -33,6 +33,8 @@ EXPORTED_SYMBOLS = (
     "sparsepr_kernel_timing", "sparsepr_kernel_timing_read",
     "sparsepr_sparse_attn_apply", "sparsepr_reset_workspace", "sparsepr_call_workspace_size", "sparsepr_attention",
     "sparsepr_host_workspace_size", "sparsepr_attention_host", "sparsepr_test_partition_trace",
+    "sparsepr_rotary", "sparsepr_selected_workspace_size", "sparsepr_key_means", "sparsepr_select_blocks",
+    "sparsepr_selected_attn", "sparsepr_selected_attn_backward",
 )
 
 
@@ -139,6 +141,8 @@ def load_library(path: str) -> ctypes.CDLL:
         "sparsepr_test_partition_trace": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _i32, _i32, _i32, _i32, P, _vp,
                                                          _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
     }
+    from .selected import signatures
+    sig.update(signatures())
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
         fn.restype = res
@@ -352,17 +356,29 @@ def apply_residual(s_out, m, beta, probe_idx, probe_out, out_dtype=torch.bfloat1
 
 # --------------------------------------------------------------------------- the call
 
+def _rotated(q, k, rotary):
+    """q and k rotated by (plan, positions), or as they are where there is none."""
+    if rotary is None:
+        return q, k
+    from . import selected
+    plan, positions = rotary
+    return selected.rotary(plan, positions, q, k)
+
+
 def attention(q, k, v, cfg: SparsePRConfig, ws: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
-              return_parts: bool = False, fused: Optional[bool] = None):
+              return_parts: bool = False, fused: Optional[bool] = None, rotary=None):
     """One SparsePR attention call.  Returns O [Bt,H,N,d] in q's dtype (and the
     intermediates if asked).  Asynchronous on the current stream; ``check(ws)`` surfaces
     device-side errors.
+
+    rotary: (plan, positions) of ``rotary`` -- q and k are rotated first (into new tensors).
 
     fused (default: when built for the shape and no intermediates are asked for):
     partition, route, probe rows, fit, then the sparse attention with the correction in
     its epilogue (S never leaves the SM).  Otherwise: partition, route, sparse attention
     (S fp32), probe rows, fit, apply."""
     _need_cuda(q, k, v)
+    q, k = _rotated(q, k, rotary)
     bt, h, n, d = q.shape
     if ws is None:
         ws = new_workspace(bt, h, n, d, cfg, q.device)
@@ -493,10 +509,12 @@ def call_workspace(q: torch.Tensor, cfg: SparsePRConfig) -> torch.Tensor:
 
 
 def attention_call(q, k, v, cfg: SparsePRConfig, ws: Optional[torch.Tensor] = None,
-                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                   out: Optional[torch.Tensor] = None, rotary=None) -> torch.Tensor:
     """The whole call as one native entry point (``sparsepr_attention``): the same stages
-    and order as ``attention``, every intermediate in ``ws``."""
+    and order as ``attention``, every intermediate in ``ws``.  rotary: (plan, positions) that
+    q and k are rotated by first, as in ``attention``."""
     _need_cuda(q, k, v)
+    q, k = _rotated(q, k, rotary)
     bt, h, n, d = q.shape
     ws = call_workspace(q, cfg) if ws is None else ws
     o = torch.empty_like(q) if out is None else out

@@ -308,6 +308,109 @@ SPARSEPR_API int sparsepr_apply_residual(const float* S_out, const float* M, con
                             int32_t Bt, int32_t H, int32_t N, int32_t d, int32_t P,
                             void* O, int out_dtype, sparsepr_stream_t stream);
 
+/* ---- rotary positions, and attention over blocks that each query selects -----------
+ * Operators beside the SparsePR call: the rotation that q and k get before any attention,
+ * and a trainable block-sparse attention in which a cheap score (query . mean key of a
+ * block) selects key blocks for every single query instead of for a block of queries.
+ *
+ * Tensors here are views: [Bt, heads, rows, d] with contiguous rows of d elements and any
+ * strides of whole 16-byte units (a [Bt, rows, heads, d] buffer is such a view), starting on
+ * a 16-byte boundary, else INVALID_ARG.  Outputs must not overlap each other or inputs,
+ * except for the rotation in place.  Calls launch on the current device, which must be the
+ * tensors'; they may be captured into graphs.  Two calls that can overlap on the GPU need
+ * workspaces of their own; calls in sequence (replays of two graphs too) may share one:
+ * each writes what it reads of it, but for the status word, which stays until
+ * sparsepr_reset_workspace. */
+typedef struct sparsepr_view {
+  void* data;                          /* device */
+  int64_t stride_b, stride_h, stride_n; /* elements; 0 repeats (inputs only) */
+} sparsepr_view;
+
+/* Layout of a pair in the R = rot_dim rotated dims: HALF pairs dim i with i + R/2,
+ * INTERLEAVED pairs 2i with 2i + 1. */
+enum { SPARSEPR_ROTARY_HALF = 0, SPARSEPR_ROTARY_INTERLEAVED = 1 };
+
+typedef struct sparsepr_rotary_params {
+  int32_t rot_dim;  /* R: rotated dims, even, 2 .. d                                   */
+  int32_t first;    /* first rotated dim; dims outside [first, first + R) are copied   */
+  int32_t layout;   /* SPARSEPR_ROTARY_*                                               */
+  int32_t axes;     /* position streams, 1 .. 4 (a video grid: t, y, x)                */
+  int32_t pairs[4]; /* pairs of each axis, in order; sum R/2                           */
+  int32_t inverse;  /* 1: rotate by the negative angle (the backward pass)             */
+  float factor;     /* multiplies the rotated part (1 unless a context scaling sets it)*/
+} sparsepr_rotary_params;
+
+/* Rotary positions of X1 (and, H2 > 0, X2 with its own head count) into Y1 (Y2):
+ * pair (a, b) with frequency f_i at position p: factor * (a cos(p f_i) - b sin(p f_i),
+ * b cos(p f_i) + a sin(p f_i)), rounded once.  Angles are formed and reduced in 64 bits.
+ *   freqs      [R/2] double, device: radians per step of the position
+ *   positions  [Bt, N, axes] int32, device, axes contiguous, the other strides in elements
+ *              (0: one row of positions for every batch element)
+ * Y may be X (same strides): in place.  Rows off 16-byte boundaries and odd parts work, by
+ * a slower kernel.  The gradient of the rotation is the rotation with inverse = 1. */
+SPARSEPR_API int sparsepr_rotary(const sparsepr_rotary_params* p, const double* freqs, const int32_t* positions,
+                                 int64_t pos_stride_b, int64_t pos_stride_n, int dtype, int32_t Bt, int32_t N,
+                                 int32_t d, int32_t H1, const sparsepr_view* X1, const sparsepr_view* Y1, int32_t H2,
+                                 const sparsepr_view* X2, const sparsepr_view* Y2, sparsepr_stream_t stream);
+
+/* One selected-attention problem.  Query heads h, h + 1, .. of a group of Hq / Hkv share a
+ * key head and one selection.  Keys at or past kv_len[b] do not exist: their K and V rows
+ * are not read (they may hold anything).  causal: query i sits at key position
+ * q_start[b] + i and sees keys up to it; q_start NULL: Nk - Nq (the queries are the last
+ * ones).  A NaN or infinity in a key or value row that exists reaches every query that
+ * selected its block, causally hidden rows of the query's own block included. */
+typedef struct sparsepr_selected {
+  int32_t dtype;                     /* of Q, K, V and the results                      */
+  int32_t Bt, Hq, Hkv, Nq, Nk, d;    /* d 64 or 128                                     */
+  int32_t block;                     /* keys per block: 64 or 128; at most 2048 blocks  */
+  int32_t top;                       /* blocks per query (row length of sel), 1 .. 1024 */
+  int32_t causal;
+  int32_t n_first;                   /* the first n_first blocks are always selected    */
+  int32_t n_local;                   /* causal: so are the query's own block and the
+                                        n_local - 1 before it; n_first + n_local <= top */
+  float scale;                       /* softmax scale; <= 0 selects 1/sqrt(d)           */
+  const int32_t* kv_len;             /* [Bt] device, or NULL (Nk); clamped to [0, Nk]   */
+  const int32_t* q_start;            /* [Bt] device, or NULL                            */
+} sparsepr_selected;
+
+/* Bytes of workspace of the calls below on this problem (0 on invalid sizes); `backward`
+ * adds what the backward call needs.  The first 256 bytes must be zero before first use. */
+SPARSEPR_API size_t sparsepr_selected_workspace_size(const sparsepr_selected* p, int backward);
+
+/* Mean key of every block, means [Bt, Hkv, ceil(Nk/block), d] fp32: the mean of the block's
+ * keys below kv_len (summed in 64 bits, rounded once), zero for a block without keys.  With
+ * kv_start [Bt] (device), only the blocks that hold keys [kv_start, kv_len) are written --
+ * after appending at most max_new keys per sequence to a cache -- from all of their keys;
+ * the others keep their means. */
+SPARSEPR_API int sparsepr_key_means(const sparsepr_selected* p, const sparsepr_view* K, const int32_t* kv_start,
+                                    int32_t max_new, float* means, sparsepr_stream_t stream);
+
+/* Selected blocks of every query, sel [Bt, Hkv, Nq, top] int32: of the blocks that hold a
+ * key the query sees, the forced ones (n_first, n_local), then those with the largest
+ * (sum of the group's queries) . mean, ties to the lower block; ascending, then -1.  The
+ * scores are compared as exact 64-bit values.  A NaN score ranks lowest and records
+ * SPARSEPR_ERR_NONFINITE in the status word. */
+SPARSEPR_API int sparsepr_select_blocks(const sparsepr_selected* p, const sparsepr_view* Q, const float* means,
+                                        int32_t* sel, void* ws, sparsepr_stream_t stream);
+
+/* Softmax attention of every query over the keys of its selected blocks that it sees:
+ * O [Bt,Hq,Nq,d] in dtype, lse [Bt,Hq,Nq] fp32 natural log-sum-exp; a query without keys
+ * gets a zero row and -inf.  sel rows ascend and end at their first negative entry; an entry
+ * that does not ascend or is past the last block is skipped and records
+ * SPARSEPR_ERR_INVALID_ARG in the status word. */
+SPARSEPR_API int sparsepr_selected_attn(const sparsepr_selected* p, const sparsepr_view* Q, const sparsepr_view* K,
+                                        const sparsepr_view* V, const int32_t* sel, const sparsepr_view* O, float* lse,
+                                        void* ws, sparsepr_stream_t stream);
+
+/* Its backward pass for a fixed selection: dQ, dK, dV (all rows written, zero where nothing
+ * contributes) from dO and the forward call's inputs, O and lse.  Sums over a block's
+ * queries run in token order: the result is the same in every run. */
+SPARSEPR_API int sparsepr_selected_attn_backward(const sparsepr_selected* p, const sparsepr_view* dO,
+                                                 const sparsepr_view* Q, const sparsepr_view* K, const sparsepr_view* V,
+                                                 const sparsepr_view* O, const float* lse, const int32_t* sel,
+                                                 const sparsepr_view* dQ, const sparsepr_view* dK,
+                                                 const sparsepr_view* dV, void* ws, sparsepr_stream_t stream);
+
 /* Measurement: per-row relative L2 error against a reference output (the metric the
  * abstract reports, averaged there over unprobed queries):
  *   err[b,h,i] = |O_i - O_ref_i|_2 / |O_ref_i|_2, and NaN for the P probe rows listed in
