@@ -37,8 +37,9 @@ constexpr int kMaxBlocks = 2048;
 
 // One work item of the attention kernels: rows [r0, r0 + rows) of the entries of key block g,
 // whose first entry is `off` of its region's list; row r is query head r % group of entry r / group.
-struct Unit {
-  int g, off, r0, rows;
+// rows = 0: none.  live, qs: the length and the position of query 0, both from the block's first key on.
+struct __align__(32) Unit {
+  int g, off, r0, rows, live, qs, b, kh;
 };
 
 struct SelArgs {
@@ -61,12 +62,13 @@ struct SelArgs {
   int* list;             // [regions][slice * top] tokens, block by block, ascending
   int* inv;              // [Bt, Hk, n, top] entry of (token, slot) in its region, or -1
   int unit_rows, unit_cap;
-  Unit* units;           // [regions][unit_cap]
+  Unit* units;           // [regions][unit_cap], the last ones empty
   int* n_units;          // [regions]
   int2* blk;             // [regions][nb] {segments, first slot of the segment sums}
-  int* ticket;           // dynamic work counter of the persistent kernels
-  // partial rows of one chunk of regions
-  float* part;           // [chunk regions][slice * top * group][d]
+  // partial rows of one chunk of regions: fp32 [chunk regions][slice * top * group][d], or fp16
+  // in planes of 64 columns (selected_tc.cu)
+  float* part;
+  long long plane;       // rows of a plane
   float2* ml;            // forward: running maximum (log2 units) and sum of each partial row
   float* delta;          // backward: sum of o * go per query row
   float* seg;            // backward: [chunk regions][seg_cap][2][block][d] sums of split blocks

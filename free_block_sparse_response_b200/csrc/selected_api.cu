@@ -80,19 +80,21 @@ SelArgs base_args(const sparsepr_selected* p) {
 }
 
 // Bytes of partial rows that one chunk of regions may take.
-constexpr size_t kPartialBytes = 256u << 20;
+constexpr size_t kPartialBytes = 1ull << 30;
 
 // Slices, chunks and scratch regions of one call (the workspace's first 256 bytes are its
 // status header).
 struct Plan {
   int regions, chunk;  // chunk: regions per launch
-  size_t offs, list, inv, units, n_units, blk, ticket, part, ml, delta, seg, total;
+  size_t offs, list, inv, units, n_units, blk, part, ml, delta, seg, total;
 };
 
 Plan make_plan(SelArgs& a, bool backward) {
   Plan L{};
   const long long subs = spr::ceil_div(a.n, spr::kSub);
-  const size_t row = sizeof(float) * a.d + sizeof(float2);
+  // the tensor-core forward pass keeps its partial rows in fp16
+  const size_t val = backward || a.f32 ? sizeof(float) : 2;
+  const size_t row = val * a.d + sizeof(float2);
   const size_t sub_bytes = row * spr::kSub * a.top * a.group;
   // A backward region is a head's whole token range, so that a key block's gradient is
   // formed by one region; a forward region is cut where its partial rows pass the chunk.
@@ -106,7 +108,8 @@ Plan make_plan(SelArgs& a, bool backward) {
   L.regions = a.Bt * a.Hk * a.slices;
   const long long entries = static_cast<long long>(a.slice) * a.top, rows = entries * a.group;
   L.chunk = static_cast<int>(std::min<long long>(L.regions, std::max<long long>(1, kPartialBytes / (row * rows))));
-  a.unit_rows = backward ? 2048 : 512;
+  a.plane = rows * L.chunk;
+  a.unit_rows = backward ? 2048 : a.f32 ? 512 : 128;  // the tensor-core forward pass works tile by tile
   a.unit_cap = a.nb + static_cast<int>(rows / a.unit_rows);
   a.seg_cap = backward ? static_cast<int>(2 * (rows / a.unit_rows)) + 2 : 0;
   size_t off = 256;
@@ -122,8 +125,7 @@ Plan make_plan(SelArgs& a, bool backward) {
   L.units = take(sizeof(spr::Unit) * R * a.unit_cap);
   L.n_units = take(sizeof(int) * R);
   L.blk = take(sizeof(int2) * R * a.nb);
-  L.ticket = take(sizeof(int));
-  L.part = take(sizeof(float) * a.d * rows * L.chunk);
+  L.part = take(val * a.d * rows * L.chunk);
   L.ml = take(backward ? 0 : sizeof(float2) * rows * L.chunk);
   L.delta = take(backward ? sizeof(float) * static_cast<size_t>(a.Bt) * a.Hq * a.n : 0);
   L.seg = take(sizeof(float) * 2 * a.block * a.d * static_cast<size_t>(a.seg_cap) * L.chunk);
@@ -144,7 +146,6 @@ void bind(SelArgs& a, const Plan& L, void* ws) {
   a.units = at<spr::Unit>(ws, L.units);
   a.n_units = at<int>(ws, L.n_units);
   a.blk = at<int2>(ws, L.blk);
-  a.ticket = at<int>(ws, L.ticket);
   a.part = at<float>(ws, L.part);
   a.ml = at<float2>(ws, L.ml);
   a.delta = at<float>(ws, L.delta);

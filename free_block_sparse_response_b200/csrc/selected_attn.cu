@@ -15,6 +15,7 @@
 
 #include "common.cuh"
 #include "selected.cuh"
+#include "selected_tc.cuh"
 
 namespace spr {
 namespace {
@@ -85,8 +86,8 @@ template <typename T, int D, int B>
 __global__ void __launch_bounds__(kFwdThreads) forward_kernel(const SelArgs a, int first, int count) {
   extern __shared__ __align__(16) float smem[];
   const int ci = blockIdx.x % count, u = blockIdx.x / count, region = first + ci;
-  if (u >= a.n_units[region]) return;
   const Unit un = a.units[static_cast<size_t>(region) * a.unit_cap + u];
+  if (un.rows == 0) return;
   float *sq = smem, *sk = sq + kFwdRows * (D + 4), *sv = sk + B * (D + 4), *sp = sv + B * (D + 4);
   const int z = region / a.slices, b = z / a.Hk, kh = z % a.Hk;
   const int len = kv_len_of(a, b), j0 = un.g * B;
@@ -274,8 +275,8 @@ template <typename T, int D, int B>
 __global__ void __launch_bounds__(kBwdThreads) backward_kernel(const SelArgs a, int first, int count) {
   extern __shared__ __align__(16) float smem[];
   const int ci = blockIdx.x % count, u = blockIdx.x / count, region = first + ci;
-  if (u >= a.n_units[region]) return;
   const Unit un = a.units[static_cast<size_t>(region) * a.unit_cap + u];
+  if (un.rows == 0) return;
   float *sk = smem, *sv = sk + B * (D + 4), *sq = sv + B * (D + 4), *sg = sq + kBwdRows * (D + 4),
         *sp = sg + kBwdRows * (D + 4), *sd = sp + kBwdRows * (B + 4);
   const int z = region / a.slices, b = z / a.Hk, kh = z % a.Hk;
@@ -507,7 +508,10 @@ cudaError_t delta(const SelArgs& a, cudaStream_t st) {
                 : (a.block == 128 ? fn<__nv_bfloat16, 64, 128>(__VA_ARGS__) : fn<__nv_bfloat16, 64, 64>(__VA_ARGS__))))
 
 cudaError_t launch_selected_forward(const SelArgs& a, int first, int count, cudaStream_t st) {
-  return SPR_SHAPES(forward, a, first, count, st);
+  if (!a.f32) return launch_selected_forward_tc(a, first, count, st);
+  if (a.d == 128)
+    return a.block == 128 ? forward<float, 128, 128>(a, first, count, st) : forward<float, 128, 64>(a, first, count, st);
+  return a.block == 128 ? forward<float, 64, 128>(a, first, count, st) : forward<float, 64, 64>(a, first, count, st);
 }
 
 cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cudaStream_t st) {

@@ -23,42 +23,58 @@ namespace {
 
 constexpr int kWords = kSub / 32;
 
-// The valid blocks of a token's row: ascending, in [0, nb), up to the first negative entry.
-// An entry out of range or not above all earlier ones is reported and skipped; a block with
-// no key that the token may attend to is skipped.
+// The valid entries of the sub-slice's rows: ascending, in [0, nb), up to the first negative
+// one.  An entry out of range or not above all earlier ones is reported and skipped; a block with
+// no key that the token may attend to is skipped (f gets -1).  The lanes of a warp take the slots
+// of one or more rows (a power of two of at least 4 lanes a row), a prefix maximum over them
+// finds the entries that ascend.
 template <typename F>
-__device__ __forceinline__ void each_selected(const SelArgs& a, const int* row, int limit_block, F f) {
-  int prev = -1;
+__device__ __forceinline__ void each_selected(const SelArgs& a, int z, int t0, F f) {
+  const int b = z / a.Hk, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  int width = 4;
+  while (width < 32 && width < a.top) width *= 2;
+  const int per = 32 / width, slot = lane & (width - 1), sub = lane / width;
+  const int len = kv_len_of(a, b), qs = q_start_of(a, b);
   bool bad = false;
-  for (int j = 0; j < a.top; ++j) {
-    const int g = __ldg(row + j);
-    if (g < 0) break;
-    if (g >= a.nb || g <= prev) {
-      bad = true;
-      continue;
+  for (int i0 = warp * per; i0 < kSub && t0 + i0 < a.n; i0 += warps * per) {
+    const int i = i0 + sub, t = t0 + i;
+    const bool live = t < a.n;
+    // last block that holds a key the token may attend to (-1: none)
+    int last = a.causal ? min(len - 1, qs + t) : len - 1;
+    last = last < 0 ? -1 : last / a.block;
+    const size_t row = (static_cast<size_t>(z) * a.n + t) * a.top;
+    int above = -1;  // largest valid-range entry of the slots before this chunk
+    bool ended = false;
+    for (int j0 = 0; j0 < a.top; j0 += width) {
+      const int j = j0 + slot;
+      int g = live && j < a.top ? __ldg(a.sel + row + j) : -1;
+      // entries from the row's first negative one on do not count
+      const unsigned neg = __ballot_sync(0xffffffffu, g < 0) >> (sub * width);
+      const unsigned before = width == 32 ? (slot == 31 ? 0x7fffffffu : (1u << slot) - 1u) : (1u << slot) - 1u;
+      const bool past = ended || g < 0 || (neg & before) != 0;
+      const int v = past || g >= a.nb ? -1 : g;
+      int mx = v;  // inclusive prefix maximum over the row's lanes
+      for (int o = 1; o < width; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, mx, o, width);
+        if (slot >= o) mx = max(mx, y);
+      }
+      int prev = __shfl_up_sync(0xffffffffu, mx, 1, width);
+      prev = max(above, slot > 0 ? prev : -1);
+      if (!past && (g >= a.nb || g <= prev)) bad = true;
+      if (live && j < a.top) f(i, row + j, v >= 0 && v > prev && v <= last ? v : -1);
+      above = max(above, __shfl_sync(0xffffffffu, mx, width - 1, width));
+      ended = ended || (neg & (width == 32 ? 0xffffffffu : (1u << width) - 1u)) != 0;
     }
-    prev = g;
-    if (g <= limit_block) f(j, g);
   }
   if (bad) record_error(a.status, kErrInvalidArg);
-}
-
-// Last block that holds a key token t may attend to (-1: none).
-__device__ __forceinline__ int limit_block(const SelArgs& a, int b, int t) {
-  int last = kv_len_of(a, b) - 1;
-  if (a.causal) last = min(last, q_start_of(a, b) + t);
-  return last < 0 ? -1 : last / a.block;
 }
 
 __device__ __forceinline__ void set_bits(const SelArgs& a, uint32_t* mask, int z, int t0) {
   for (int i = threadIdx.x; i < a.nb * kWords; i += blockDim.x) mask[i] = 0;
   __syncthreads();
-  const int b = z / a.Hk;
-  for (int i = threadIdx.x; i < kSub && t0 + i < a.n; i += blockDim.x) {
-    const int t = t0 + i;
-    each_selected(a, a.sel + (static_cast<size_t>(z) * a.n + t) * a.top, limit_block(a, b, t),
-                  [&](int, int g) { atomicOr(&mask[g * kWords + (i >> 5)], 1u << (i & 31)); });
-  }
+  each_selected(a, z, t0, [&](int i, size_t, int g) {
+    if (g >= 0) atomicOr(&mask[g * kWords + (i >> 5)], 1u << (i & 31));
+  });
   __syncthreads();
 }
 
@@ -105,7 +121,8 @@ __device__ __forceinline__ int block_scan(int v, int& sum, int* s_warp) {
 __global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
   __shared__ int s_warp[16];
   const int region = blockIdx.x;
-  const int s = region % a.slices;
+  const int s = region % a.slices, z = region / a.slices, b = z / a.Hk;
+  const int len = kv_len_of(a, b), qs = q_start_of(a, b);
   // sub-slices of this region that hold tokens
   const int live = min(a.subs, ceil_div(a.n - s * a.slice, kSub));
   int entry0 = 0, unit0 = 0, slot0 = 0;
@@ -128,7 +145,8 @@ __global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
     if (g < a.nb) {
       for (int i = 0; i < nu; ++i)
         a.units[static_cast<size_t>(region) * a.unit_cap + u + i] =
-            Unit{g, off, i * a.unit_rows, min(a.unit_rows, rows - i * a.unit_rows)};
+            Unit{g, off, i * a.unit_rows, min(a.unit_rows, rows - i * a.unit_rows), len - g * a.block, qs - g * a.block, b,
+                 z % a.Hk};
       a.blk[static_cast<size_t>(region) * a.nb + g] = make_int2(nu, slot);
       for (int i = 0; i < live; ++i) {
         const int x = c[i];
@@ -137,10 +155,9 @@ __global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
       }
     }
   }
-  if (threadIdx.x == 0) {
-    a.n_units[region] = unit0;
-    if (region == 0) *a.ticket = 0;
-  }
+  if (threadIdx.x == 0) a.n_units[region] = unit0;
+  for (int u = unit0 + threadIdx.x; u < a.unit_cap; u += 512)
+    a.units[static_cast<size_t>(region) * a.unit_cap + u] = Unit{};
 }
 
 __global__ void __launch_bounds__(256) scatter_kernel(const SelArgs a) {
@@ -157,20 +174,18 @@ __global__ void __launch_bounds__(256) scatter_kernel(const SelArgs a) {
     }
   }
   __syncthreads();
-  const int region = z * a.slices + s / a.subs, ls = s % a.subs, b = z / a.Hk;
+  const int region = z * a.slices + s / a.subs, ls = s % a.subs;
   int* list = a.list + static_cast<size_t>(region) * a.slice * a.top;
-  for (int i = threadIdx.x; i < kSub && t0 + i < a.n; i += blockDim.x) {
-    const int t = t0 + i;
-    const size_t row = (static_cast<size_t>(z) * a.n + t) * a.top;
-    for (int j = 0; j < a.top; ++j) a.inv[row + j] = -1;
-    each_selected(a, a.sel + row, limit_block(a, b, t), [&](int j, int g) {
+  const int* offs = a.offs + static_cast<size_t>(region) * a.nb * a.subs + ls;
+  each_selected(a, z, t0, [&](int i, size_t at, int g) {
+    int e = -1;
+    if (g >= 0) {
       const int w = g * kWords + (i >> 5);
-      const int e = __ldg(a.offs + (static_cast<size_t>(region) * a.nb + g) * a.subs + ls) + before[w] +
-                    __popc(mask[w] & ((1u << (i & 31)) - 1u));
-      list[e] = t;
-      a.inv[row + j] = e;
-    });
-  }
+      e = __ldg(offs + static_cast<size_t>(g) * a.subs) + before[w] + __popc(mask[w] & ((1u << (i & 31)) - 1u));
+      list[e] = t0 + i;
+    }
+    a.inv[at] = e;
+  });
 }
 
 }  // namespace

@@ -1,0 +1,599 @@
+// Selected-block attention on the 5th-generation tensor cores (bf16).
+//
+// Mathematics as in selected_attn.cu: a work unit is one key block and up to unit_rows of the
+// query rows that selected it.  K and V of the block stay in shared memory; 128 rows at a time
+//   S = Q K^T (128 x B),  P = exp(S - row max),  O = P V (128 x D)
+// need no running maximum, since one tile holds all the keys of the row's part.  The part goes
+// out as O / l in fp16 times a power of two per row (the row's largest magnitude scaled to
+// 1/2 .. 1), with its log-sum-exp; join_half_kernel adds a row's parts.  fp16 with its own scale
+// rounds a part by 2^-12 of the row's largest element, 16 times finer than the result's bf16;
+// fp32 parts would double the traffic that bounds the pass.
+//
+// Work of a tile (B = D = 128): 8.4 MFLOP, 16K exponentials, 32 KB of Q gathered, 32 KB written.
+// A tile passes through five stages of ~1 us (gather, S, softmax, O, output), so one persistent
+// CTA per SM keeps five tiles in a ring of slots, each slot holding Q and then P of its tile, and
+// gives each stage warps of its own; tiles alternate between two streams (S and O in TMEM each):
+//   warps 0-7    softmax, one warpgroup a stream, one thread a row: maximum, then exponentials,
+//                reading S twice (a second read costs ~100 cycles, 128 held values spill);
+//   warps 8-11   output: O / l of each tile to memory;
+//   warps 12-15  gather Q rows through the block's list (16-byte asynchronous copies, 16 lanes a
+//                row, into the 128-byte swizzle), slots ahead of the products;
+//   warps 16-17  issue the products of one stream each: S of the stream's next tile as soon as
+//                the softmax has read the last one, O when P is written;
+//   warp 18      TMA boxes of the units' K and V, and zeros over V rows at or past the length
+//                (their P is 0, but 0 times what a cache holds there need not be).
+// All waits are bounded; on a timeout every role leaves, products and copies in flight drained.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cudaTypedefs.h>
+
+#include "common.cuh"
+#include "selected.cuh"
+#include "selected_tc.cuh"
+#include "tcgen05.cuh"
+#include "warp_mma.cuh"
+
+namespace spr {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kInf = __builtin_huge_valf();
+
+constexpr int kThreads = 640, kLoaders = 128;
+constexpr int kRegSoftmax = 112, kRegOut = 136, kRegRest = 56;
+constexpr int kOutWarp = 8, kLoadWarp = 12, kMmaWarp = 16, kKvWarp = 18;
+
+template <int D, int B>
+struct Fwd {
+  static constexpr uint32_t kSlot = 128 * (D > B ? D : B) * 2, kKV = B * D * 2;
+  static constexpr uint32_t kTail = 2 * 128 * sizeof(float2) + 512;  // row statistics, barriers
+  static constexpr int kFit = (227 * 1024 - 2 * kKV - kTail) / kSlot;
+  static constexpr int kSlots = kFit < 8 ? kFit : 8;
+  static constexpr uint32_t kSmem = kSlots * kSlot + 2 * kKV + kTail;
+};
+
+// Per unit: K landed, V landed, V ready (zeros in place), K and V read by every product; per
+// stream: S ready, P written (and S read), O ready, O read, drain; per slot: Q in place, free.
+enum : int {
+  kK = 0, kVLand, kV, kKFree, kVFree, kS, kP = kS + 2, kO = kP + 2, kOFree = kO + 2, kDrain = kOFree + 2,
+  kQ = kDrain + 2, kFree = kQ + 8, kNumBars = kFree + 8
+};
+static_assert(8 * kNumBars + 32 <= 512, "barriers fit their room");
+
+// Row maximum over 32 values, four chains of 3-input maxima; masking of columns from n on.
+__device__ __forceinline__ void max_into(float (&mx)[4], const uint32_t (&s)[32]) {
+#pragma unroll
+  for (int c = 0; c < 32; c += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      mx[i] = fmax3(mx[i], __uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
+}
+__device__ __forceinline__ void mask_from(uint32_t (&s)[32], int n) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c)
+    if (c >= n) s[c] = __float_as_uint(-kInf);
+}
+
+template <int D, int B>
+__global__ void __launch_bounds__(kThreads, 1)
+    selected_forward_tc_kernel(const __grid_constant__ BlockMap mk, const __grid_constant__ BlockMap mv, const SelArgs a,
+                               int first, int count) {
+  using F = Fwd<D, B>;
+  constexpr int R = F::kSlots;
+  extern __shared__ __align__(1024) uint8_t dsmem[];
+  uint8_t* const tail = dsmem + R * F::kSlot + 2 * F::kKV;
+  float2* const s_stat = reinterpret_cast<float2*>(tail);  // [stream][row] log-sum-exp (log2 units), 1 / sum
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(tail + 2 * 128 * sizeof(float2));
+  uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(bars + kNumBars);
+  int& abort_flag = *reinterpret_cast<int*>(bars + kNumBars + 1);
+  int* const s_first = reinterpret_cast<int*>(bars + kNumBars + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sSlot = tc::saddr(dsmem), sK = sSlot + R * F::kSlot, sV = sK + F::kKV;
+  if ((sSlot & 1023u) != 0) {  // the tiles' swizzle counts from 1024-byte lines
+    if (tid == 0) record_error(a.status, kErrCuda);
+    return;
+  }
+  auto bar = [&](int i) { return tc::saddr(&bars[i]); };
+  if (tid == 0) {
+    tc::mbar_init(bar(kK), 1);
+    tc::mbar_init(bar(kVLand), 1);
+    tc::mbar_init(bar(kV), 32);
+    tc::mbar_init(bar(kKFree), 2);
+    tc::mbar_init(bar(kVFree), 2);
+    for (int x = 0; x < 2; ++x) {
+      tc::mbar_init(bar(kS + x), 1);
+      tc::mbar_init(bar(kP + x), 128);
+      tc::mbar_init(bar(kO + x), 1);
+      tc::mbar_init(bar(kOFree + x), 128);
+      tc::mbar_init(bar(kDrain + x), 1);
+    }
+    for (int i = 0; i < 8; ++i) {
+      tc::mbar_init(bar(kQ + i), kLoaders);
+      tc::mbar_init(bar(kFree + i), 1);
+    }
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tc::saddr(&tmem_slot), 512);
+    tc::tmem_relinquish();
+  }
+  if (warp == kOutWarp) {  // this CTA's first tile (region, tile of it) and number of tiles
+    int sum = 0;
+    for (int i = lane; i < count; i += 32) sum += __ldg(a.n_units + first + i);
+    sum = __reduce_add_sync(0xffffffffu, sum);
+    const int lo = static_cast<int>(static_cast<long long>(sum) * blockIdx.x / gridDim.x);
+    const int hi = static_cast<int>(static_cast<long long>(sum) * (blockIdx.x + 1) / gridDim.x);
+    if (lane == 0) {
+      int ci = 0, before = 0, n = 0;
+      while (ci < count && before + (n = __ldg(a.n_units + first + ci)) <= lo) before += n, ++ci;
+      s_first[0] = ci, s_first[1] = lo - before, s_first[2] = hi - lo;
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tbase = tmem_slot;  // S of stream x at 128 x, O at 256 + 128 x
+  volatile int* abort_v = &abort_flag;
+  const size_t cap = static_cast<size_t>(a.slice) * a.top;
+  // This CTA's tiles: an equal share of the chunk's, contiguous in the order region, block, row,
+  // so that K and V change seldom.  Every role walks them in this order (a stream's warps every
+  // second one), the records of the next two in flight.
+  // f(record, region of the chunk, tile, unit = run of tiles of one block, opens it, closes it);
+  // the last three only at step 1.
+  auto each_tile = [&](int from, int step, auto f) {
+    int ci = s_first[0], idx = s_first[1] + from;
+    const int tiles = s_first[2];
+    int n = tiles > 0 ? __ldg(a.n_units + first + ci) : 0;
+    struct Rec {
+      Unit un;
+      int ci;
+    };
+    auto fetch = [&](int t) {  // record of tile t, called in order
+      Rec r{};
+      if (t < tiles) {
+        while (idx >= n) idx -= n, n = __ldg(a.n_units + first + ++ci);
+        r.un = a.units[static_cast<size_t>(first + ci) * a.unit_cap + idx];
+        r.ci = ci;
+        idx += step;
+      }
+      return r;
+    };
+    Rec now = fetch(from), next = fetch(from + step);
+    int u = 0;
+    bool opens = true;
+    for (int t = from; t < tiles; t += step) {
+      const Rec ahead = fetch(t + 2 * step);
+      const bool closes = t + 1 == tiles || next.ci != now.ci || next.un.g != now.un.g;
+      if (!f(now.un, now.ci, t, u, opens, closes)) return false;
+      opens = closes;
+      u += closes;
+      now = next, next = ahead;
+    }
+    return true;
+  };
+  auto wait1 = [&](int i, int phase) { return wait_bar(bar(i), phase & 1, abort_v, a.status); };
+  auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, wait1(i, phase)); };
+
+  // registers: 96 a thread at launch, 480 x 128 in all; 2 x 112 + 136 + 2 x 56 of them are used
+  if (warp < kOutWarp) {
+    // ---------------------------------------------------------------- softmax
+    tc::setmaxnreg_inc<kRegSoftmax>();
+    const int x = warp >> 2, row = tid & 127;
+    const uint32_t tS = tbase + 128 * x + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+    const float scale2 = a.scale * kLog2e;
+    each_tile(x, 2, [&](const Unit& un, int ci, int t, int, bool, bool) {
+        int nv = un.live;  // visible keys of this row in the block
+        if (a.causal && row < un.rows)
+          nv = min(nv, un.qs + __ldg(a.list + (first + ci) * cap + un.off + (un.r0 + row) / a.group) + 1);
+        if (!wait(kS + x, t >> 1)) return false;
+        tc::fence_after_sync();
+        const bool cut = __any_sync(0xffffffffu, nv < B);
+        float mx[4] = {-kInf, -kInf, -kInf, -kInf};
+#pragma unroll 1
+        for (int c0 = 0; c0 < B; c0 += 32) {
+          uint32_t s[32];
+          tc::tmem_ld32(tS + c0, s);
+          tc::tmem_wait_ld();
+          if (cut) mask_from(s, nv - c0);
+          max_into(mx, s);
+        }
+        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
+        const float ms = m == -kInf ? 0.f : m;
+        const uint64_t sc2 = f32x2(scale2, scale2), nm2 = f32x2(-ms, -ms);
+        uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+        const uint32_t sP = sSlot + (t % R) * F::kSlot;  // over Q, which S has read
+#pragma unroll 1
+        for (int c0 = 0; c0 < B; c0 += 32) {
+          uint32_t s[32], pk[16];
+          tc::tmem_ld32(tS + c0, s);
+          tc::tmem_wait_ld();
+          if (cut) mask_from(s, nv - c0);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float y0, y1;
+            f32x2_split(ffma2(f32x2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), sc2, nm2), y0, y1);
+            const float p0 = ex2(y0), p1 = ex2(y1);
+            sum[i & 1] = fadd2(sum[i & 1], f32x2(p0, p1));
+            pk[i] = pack_bf16x2(p0, p1);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            st_shared_16(sP + tc::sw128_offset(row, c0 / 8 + c), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
+        }
+        tc::fence_proxy_async();
+        float l0, l1, l2, l3;
+        f32x2_split(sum[0], l0, l1);
+        f32x2_split(sum[1], l2, l3);
+        // the output warps have taken the statistics of the stream's tile before
+        if (t > 1 && !wait(kOFree + x, (t >> 1) - 1)) return false;
+        const float l = (l0 + l1) + (l2 + l3);  // not above 0: no visible key (or a NaN, which stays one)
+        s_stat[x * 128 + row] = make_float2(l > 0.f || l != l ? m + __log2f(l) : -kInf,
+                                            l > 0.f ? __fdividef(1.f, l) : l != l ? l : 0.f);
+        tc::fence_before_sync();
+        tc::mbar_arrive(bar(kP + x));
+        return true;
+    });
+  } else if (warp < kLoadWarp) {
+    // ---------------------------------------------------------------- output
+    tc::setmaxnreg_inc<kRegOut>();
+    // A quad of lanes holds rows q and q + 8 of 16 TMEM lanes, lane i of it columns 8 j + 2 i
+    // and + 1; each lane's 16 columns of a 64-column plane go out as 32 contiguous bytes, a
+    // row's quad as one 128-byte line (part_column() is the order inside the line).
+    const int w4 = warp & 3, q = lane >> 2, i = lane & 3;
+    uint8_t* const part = static_cast<uint8_t*>(static_cast<void*>(a.part));
+    each_tile(0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
+        const int x = t & 1;
+        const long long out0 = static_cast<long long>((ci * cap + un.off) * a.group + un.r0);
+        if (!wait(kP + x, t >> 1) || !wait(kO + x, t >> 1)) return false;  // the statistics, O
+        tc::fence_after_sync();
+        const uint32_t tO = tbase + 256 + 128 * x;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int lane0 = 32 * w4 + 16 * half;
+          uint32_t o[D / 2];
+#pragma unroll
+          for (int c = 0; c < D; c += 64)
+            tmem_ld_16x64(tO + (static_cast<uint32_t>(lane0) << 16) + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c / 2]));
+          tc::tmem_wait_ld();
+          // rows lane0 + q and lane0 + q + 8, side by side: this stage is bound by its latencies
+          const float2 st[2] = {s_stat[x * 128 + lane0 + q], s_stat[x * 128 + lane0 + q + 8]};
+          float big[2][2] = {};
+#pragma unroll
+          for (int c = 0; c < D / 2; c += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              big[k & 1][k >> 1] = fmax3(big[k & 1][k >> 1], fabsf(__uint_as_float(o[c + 2 * k])),
+                                         fabsf(__uint_as_float(o[c + 2 * k + 1])));
+          float mx[2] = {fmaxf(big[0][0], big[0][1]), fmaxf(big[1][0], big[1][1])}, up[2], f[2];
+#pragma unroll
+          for (int m = 1; m < 4; m <<= 1)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], m));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            float down;
+            pow2_scale(mx[k] * st[k].y, up[k], down);
+            f[k] = st[k].y * down;
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int r = lane0 + q + 8 * k;
+            if (r < un.rows) {
+#pragma unroll
+              for (int c = 0; c < D; c += 64) {
+                uint32_t h[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                  const __half2 v = __floats2half2_rn(__uint_as_float(o[c / 2 + 4 * j + 2 * k]) * f[k],
+                                                      __uint_as_float(o[c / 2 + 4 * j + 2 * k + 1]) * f[k]);
+                  h[j] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+                st_global_32(part + ((c / 64) * a.plane + out0 + r) * 128 + 32 * i, h);
+              }
+              if (i == 0) a.ml[out0 + r] = make_float2(st[k].x, up[k]);
+            }
+          }
+        }
+        tc::fence_before_sync();
+        tc::mbar_arrive(bar(kOFree + x));
+        return true;
+    });
+  } else if (warp < kMmaWarp) {
+    // ---------------------------------------------------------------- Q rows, 32 a warp
+    tc::setmaxnreg_dec<kRegRest>();
+    constexpr int kPer = D / 8, kStep = 32 / kPer;  // lanes per row, rows per instruction
+    const int lw = warp - kLoadWarp, ch = lane % kPer;
+    // tile t - 1 has landed once at most one group of copies is in flight
+    auto landed = [&](int tile) {
+      tc::fence_proxy_async();
+      tc::mbar_arrive(bar(kQ + tile % R));
+    };
+    // The copies of a tile are issued when the walk is at the next one, so that the list entry
+    // read here has arrived.
+    Unit last{};
+    int entry = 0;
+    auto copy = [&](int t) {
+      const __nv_bfloat16* q =
+          static_cast<const __nv_bfloat16*>(a.q.p) + last.b * a.q.sb + last.kh * a.group * a.q.sh + ch * 8;
+      const int row = last.r0 + 32 * lw + lane;
+      const long long off =
+          32 * lw + lane < last.rows ? entry * a.q.sn + (row % a.group) * a.q.sh : -1;
+      if (t >= R && !wait(kFree + t % R, t / R - 1)) return false;
+      const uint32_t sQ = sSlot + (t % R) * F::kSlot;
+#pragma unroll
+      for (int s = 0; s < 32; s += kStep) {
+        const int src = s + lane / kPer;
+        const long long o = __shfl_sync(0xffffffffu, off, src);
+        cp_async_16(sQ + tc::sw128_offset(32 * lw + src, ch), o < 0 ? q : q + o, o < 0 ? 0 : 16);
+      }
+      cp_async_commit();
+      if (t > 0) {
+        cp_async_wait<1>();
+        landed(t - 1);
+      }
+      return true;
+    };
+    bool ok = each_tile(0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
+      int e = 0;
+      if (32 * lw + lane < un.rows)
+        e = __ldg(a.list + (first + ci) * cap + un.off + (un.r0 + 32 * lw + lane) / a.group);
+      if (t > 0 && !copy(t - 1)) return false;
+      last = un, entry = e;
+      return true;
+    });
+    const int tiles = s_first[2];
+    ok = ok && tiles > 0 && copy(tiles - 1);
+    cp_async_wait<0>();
+    if (ok) landed(tiles - 1);
+  } else {
+    tc::setmaxnreg_dec<kRegRest>();
+  if (warp < kKvWarp) {
+    // ---------------------------------------------------------------- products of one stream
+    constexpr uint32_t kIdS = tc::idesc_bf16(128, B, false, false), kIdO = tc::idesc_bf16(128, D, false, true);
+    const int x = warp - kMmaWarp;
+    const uint32_t tS = tbase + 128 * x, tO = tbase + 256 + 128 * x;
+    if (lane == 0) {
+      int held = -1;           // tile whose O is still to be issued, of the unit held_u
+      int held_u = 0;
+      bool held_last = false;  // ... and the stream's last of that unit
+      int of_unit = 0;         // the stream's tiles of the current unit
+      auto issue_s = [&](int tile) {
+        uint64_t dq = tc::sdesc_sw128(sSlot + (tile % R) * F::kSlot, 16, 1024), dk = tc::sdesc_sw128(sK, 16, 1024);
+        keep_here(dq, dk);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc::mma_ss(tS, dq + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
+                     dk + ((kk >> 2) * (B * 128) + (kk & 3) * 32) / 16, kIdS, kk > 0 ? 1u : 0u);
+        tc::mma_commit(bar(kS + x));
+      };
+      auto issue_o = [&]() {  // of the held tile, whose P is written
+        if (!wait1(kV, held_u)) return false;
+        if (held > 1 && !wait1(kOFree + x, (held >> 1) - 1)) return false;
+        tc::fence_after_sync();
+        uint64_t dp = tc::sdesc_sw128(sSlot + (held % R) * F::kSlot, 16, 1024), dv = tc::sdesc_sw128(sV, B * 128, 1024);
+        keep_here(dp, dv);
+#pragma unroll
+        for (int kk = 0; kk < B / 16; ++kk)
+          tc::mma_ss(tO, dp + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16, dv + kk * (2048 / 16), kIdO, kk > 0 ? 1u : 0u);
+        tc::mma_commit(bar(kO + x));
+        tc::mma_commit(bar(kFree + held % R));
+        if (held_last) tc::mma_commit(bar(kVFree));
+        held = -1;
+        return true;
+      };
+      auto flush = [&]() { return held < 0 || (wait1(kP + x, held >> 1) && issue_o()); };
+      const bool ok = each_tile(0, 1, [&](const Unit&, int, int t, int u, bool opens, bool closes) {
+        if (opens) of_unit = 0;
+        if ((t & 1) == x) {
+          if (held >= 0) {
+            if (!wait1(kP + x, held >> 1)) return false;  // P written, S read
+            tc::fence_after_sync();
+            // S first where its operands are there, so that the softmax goes on at once
+            if (!(bar_done(bar(kK), u & 1) && bar_done(bar(kQ + t % R), (t / R) & 1)) && !issue_o()) return false;
+          }
+          if (!wait1(kK, u) || !wait1(kQ + t % R, t / R)) return false;
+          tc::fence_after_sync();
+          issue_s(t);
+          if (held >= 0 && !issue_o()) return false;
+          held = t, held_u = u, held_last = false;
+          ++of_unit;
+        }
+        if (!closes) return true;
+        // this stream's share of the unit's releases: K behind its last S, V behind its last O.
+        // Without a tile in the unit, once the unit before is released (two arrivals of one
+        // stream in a phase would stand for the other stream's).
+        if (of_unit > 0) {
+          tc::mma_commit(bar(kKFree));
+          held_last = true;
+        } else {
+          if (!flush() || !wait1(kK, u) || !wait1(kV, u)) return false;
+          tc::mbar_arrive(bar(kKFree));
+          tc::mbar_arrive(bar(kVFree));
+        }
+        return true;
+      });
+      if (ok) flush();
+      tc::mma_commit(bar(kDrain + x));  // every product has finished before TMEM goes back
+      tc::mbar_wait_quiet(bar(kDrain + x), 0);
+    }
+    __syncwarp();
+  } else if (warp == kKvWarp) {
+    // ---------------------------------------------------------------- K and V of each unit
+    int issued = 0;
+    const bool ok = each_tile(0, 1, [&](const Unit& un, int, int, int u, bool opens, bool) {
+      if (!opens) return true;
+      if (u > 0 && !wait(kKFree, u - 1)) return false;
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(bar(kK), F::kKV);
+#pragma unroll
+        for (int c = 0; c < D; c += 64) load_box(sK + c * (B * 2), mk, c, un.g * B, un.kh, un.b, bar(kK));
+      }
+      issued = 2 * u + 1;
+      if (u > 0 && !wait(kVFree, u - 1)) return false;
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(bar(kVLand), F::kKV);
+#pragma unroll
+        for (int c = 0; c < D; c += 64) load_box(sV + c * (B * 2), mv, c, un.g * B, un.kh, un.b, bar(kVLand));
+      }
+      __syncwarp();
+      issued = 2 * u + 2;
+      if (!wait(kVLand, u)) return false;
+      for (int i = lane; i < (B - un.live) * (D / 8); i += 32)  // V rows of the block from the length on
+        st_shared_zero(sV + sw128_rows<B>(un.live + i / (D / 8), i % (D / 8)));
+      tc::fence_proxy_async();
+      tc::mbar_arrive(bar(kV));
+      return true;
+    });
+    // boxes still in flight after an abort land before the CTA exits
+    if (!ok && lane == 0 && issued > 0) {
+      tc::mbar_wait_quiet(bar(kK), (issued - 1) / 2 & 1);
+      if (issued % 2 == 0) tc::mbar_wait_quiet(bar(kVLand), (issued / 2 - 1) & 1);
+    }
+    __syncwarp();
+  }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tbase, 512);
+  }
+}
+
+// Joins a query row's parts: D / 8 lanes cover a row with 16-byte loads, the groups of lanes
+// take slots in turn, four parts in flight each.
+template <int D>
+__global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int first, int count) {
+  constexpr int kPer = D / 8, kGroups = 32 / kPer;
+  const int lane = threadIdx.x & 31, sub = lane / kPer, ch = lane % kPer;
+  const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int per = a.slice * a.group;
+  const int ci = static_cast<int>(w / per);
+  if (ci >= count) return;
+  const int region = first + ci, z = region / a.slices, s = region % a.slices;
+  const int lr = static_cast<int>(w % per), t = s * a.slice + lr / a.group, h = lr % a.group;
+  if (t >= a.n) return;
+  const int b = z / a.Hk, kh = z % a.Hk;
+  const int* inv = a.inv + (static_cast<size_t>(z) * a.n + t) * a.top;
+  const size_t row0 = ci * static_cast<size_t>(a.slice) * a.top * a.group + h;
+  // the lane's 16 bytes of a part: chunk ch % 8 of a line in plane ch / 8
+  const uint8_t* part =
+      static_cast<const uint8_t*>(static_cast<const void*>(a.part)) + (ch / 8) * a.plane * 128 + (ch % 8) * 16;
+  float m = -kInf;
+  for (int j = lane; j < a.top; j += 32) {
+    const int e = inv[j];
+    if (e >= 0) m = fmaxf(m, a.ml[row0 + static_cast<size_t>(e) * a.group].x);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float ms = m == -kInf ? 0.f : m;
+  float l = 0.f, acc[8] = {};
+  for (int j0 = 0; j0 < a.top; j0 += 32) {
+    const int e = j0 + lane < a.top ? inv[j0 + lane] : -1;
+    float f = 0.f;
+    if (e >= 0) {
+      const float2 st = a.ml[row0 + static_cast<size_t>(e) * a.group];
+      const float wt = exp2f(st.x - ms);
+      l += wt;
+      f = wt * st.y;
+    }
+    const int lim = min(32, a.top - j0);
+    for (int j = 0; j < lim; j += 4 * kGroups) {
+      uint4 v[4];
+      float fj[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int src = j + i * kGroups + sub;
+        const int ej = __shfl_sync(0xffffffffu, e, src & 31);
+        fj[i] = __shfl_sync(0xffffffffu, f, src & 31);
+        v[i] = make_uint4(0, 0, 0, 0);
+        const size_t row = row0 + static_cast<size_t>(ej) * a.group;
+        if (src < lim && ej >= 0)
+          v[i] = __ldcs(reinterpret_cast<const uint4*>(part + row * 128));
+        else
+          fj[i] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[c]));
+          acc[2 * c] = fmaf(fj[i], y.x, acc[2 * c]);
+          acc[2 * c + 1] = fmaf(fj[i], y.y, acc[2 * c + 1]);
+        }
+      }
+    }
+  }
+  l = warp_sum(l);
+#pragma unroll
+  for (int o = kPer; o < 32; o <<= 1)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], o);
+  const float inv_l = l > 0.f ? 1.f / l : l != l ? l : 0.f;
+  if (sub == 0) {
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o.p) + b * a.o.sb + (kh * a.group + h) * a.o.sh + t * a.o.sn;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      *reinterpret_cast<uint32_t*>(o + part_column(ch, c)) = pack_bf16x2(acc[2 * c] * inv_l, acc[2 * c + 1] * inv_l);
+  }
+  if (lane == 0)
+    a.lse[(static_cast<size_t>(b) * a.Hq + kh * a.group + h) * a.n + t] =
+        l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -kInf;
+}
+
+template <int D, int B>
+cudaError_t forward(const SelArgs& a, int first, int count, cudaStream_t st) {
+  BlockMap mk, mv;
+  if (!block_map(&mk, a.k, a, B) || !block_map(&mv, a.v, a, B)) return cudaErrorInvalidValue;
+  auto kern = selected_forward_tc_kernel<D, B>;
+  constexpr int smem = static_cast<int>(Fwd<D, B>::kSmem);
+  // the register split must fit in what a block is launched with, or its increase would wait for good
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (128 * (2 * kRegSoftmax + kRegOut + 2 * kRegRest) > fa.numRegs * kThreads) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const long long grid = std::min<long long>(148, static_cast<long long>(count) * a.unit_cap);
+  kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(mk, mv, a, first, count);
+  if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(count) * a.slice * a.group;
+  join_half_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(a, first, count);
+  return counted(cudaGetLastError(), 1);
+}
+
+}  // namespace
+
+bool block_map(BlockMap* m, const View& v, const SelArgs& a, int rows) {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool ok = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                        cudaSuccess && q == cudaDriverEntryPointSuccess;
+    return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+  }();
+  if (fn == nullptr) return false;
+  // a repeated (stride 0) dimension is one of size 1, always read at 0
+  m->h = v.sh != 0 ? 1 : 0;
+  m->b = v.sb != 0 ? 1 : 0;
+  const long long row = static_cast<long long>(a.d) * 2;
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(a.d), static_cast<cuuint64_t>(a.nk), static_cast<cuuint64_t>(m->h ? a.Hk : 1),
+                        static_cast<cuuint64_t>(m->b ? a.Bt : 1)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(v.sn ? v.sn * 2 : row), static_cast<cuuint64_t>(v.sh ? v.sh * 2 : row),
+                           static_cast<cuuint64_t>(v.sb ? v.sb * 2 : row)};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rows), 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(&m->map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_selected_forward_tc(const SelArgs& a, int first, int count, cudaStream_t st) {
+  if (a.d == 128) return a.block == 128 ? forward<128, 128>(a, first, count, st) : forward<128, 64>(a, first, count, st);
+  return a.block == 128 ? forward<64, 128>(a, first, count, st) : forward<64, 64>(a, first, count, st);
+}
+
+}  // namespace spr

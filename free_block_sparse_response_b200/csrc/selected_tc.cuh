@@ -1,0 +1,149 @@
+// Device helpers shared by the tensor-core kernels of selected-block attention.
+#pragma once
+
+#include <cuda.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "selected.cuh"
+#include "tcgen05.cuh"
+
+namespace spr {
+
+// TMA map over a K or V view as (d, rows, heads, batch), boxes of 64 columns x one key block;
+// h and b are 0 where the view repeats one head or batch element.
+struct BlockMap {
+  CUtensorMap map;
+  int h, b;
+};
+bool block_map(BlockMap* m, const View& v, const SelArgs& a, int rows);
+
+// The box at (column, row, head, batch) into `dst`; column is a multiple of 64 and rows past
+// the tensor's end arrive as zeros.
+__device__ __forceinline__ void load_box(uint32_t dst, const BlockMap& m, int col, int row, int h, int b, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(&m.map)), "r"(col), "r"(row), "r"(m.h ? h : 0), "r"(m.b ? b : 0), "r"(bar)
+      : "memory");
+}
+
+// Byte offset of 16-byte chunk `ch` of row `r` in a 128-byte-swizzled tile of `ROWS` rows.
+template <int ROWS>
+__device__ __forceinline__ uint32_t sw128_rows(int r, int ch) {
+  return static_cast<uint32_t>((ch >> 3) * (ROWS * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4));
+}
+
+// tc::mbar_wait with the bound counted in SM cycles (4e9: about two seconds) and looked at only
+// every 64th try: a wait here is a microsecond in a chain of five per tile, and reading the
+// global timer takes as long.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (tc::mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (tc::mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > 4000000000ll) {
+      record_error(status, kErrTimeout);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+
+// Keeps what is computed from x and y inside the loop around it: a matrix descriptor of every
+// step of a product, formed ahead of the loop, would hold registers until they spill.
+__device__ __forceinline__ void keep_here(uint64_t& x, uint64_t& y) { asm volatile("" : "+l"(x), "+l"(y)); }
+
+__device__ __forceinline__ void st_shared_zero(uint32_t addr) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(addr), "r"(0) : "memory");
+}
+
+__device__ __forceinline__ void st_shared_16(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// 32 bytes in one store: a whole sector per thread.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]),
+               "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// 16 TMEM lanes x 64 columns: lane 4 q + i of the warp gets row q (registers 4 j, 4 j + 1) and
+// row q + 8 (4 j + 2, 4 j + 3) of columns 8 j + 2 i and 8 j + 2 i + 1, j < 8.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// Partial rows: planes of 64 columns, rows of 128 bytes.  First column of the c-th pair of
+// 16-byte chunk `ch` of a row (8 chunks a plane): the four lanes of a quad, which hold columns
+// 2 i, 2 i + 1 of every eight, write 32 bytes each.
+__device__ __forceinline__ int part_column(int ch, int c) {
+  return (ch >> 3) * 64 + ((ch & 1) * 4 + c) * 8 + ((ch & 7) >> 1) * 2;
+}
+
+// Whether the phase with this parity has completed, without waiting.
+__device__ __forceinline__ bool bar_done(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void f32x2_split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Powers of two with big * down in [1/2, 1) and up * down = 1 (0 and non-finite values: as
+// the nearest exponent that has both).
+__device__ __forceinline__ void pow2_scale(float big, float& up, float& down) {
+  int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) + 1;
+  e = min(max(e, 1), 253);
+  up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+  down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+}
+
+cudaError_t launch_selected_forward_tc(const SelArgs& a, int first, int count, cudaStream_t st);
+
+}  // namespace spr
