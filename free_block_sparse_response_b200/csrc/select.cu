@@ -1,12 +1,27 @@
 // Mean key of every key block, and the blocks that each query selects.
 //
 // A block's mean key is summed in 64 bits (exact for bf16 keys) and rounded once to 32.  The
-// score of a query and a block is (sum of the group's queries) . mean; the selection is
-// decided on scores in 64 bits, so it is the definition's whatever the types.
+// score of a query and a block is (sum of the group's queries) . mean, and the selection is the
+// one that scores in 64 bits give.  Prompts (select_tile_kernel) do not compute them all:
+//
+//   1. Scores s~ of a tile of queries from bf16 hi + lo parts on the tensor cores.  With
+//      x = hi + lo + r, |lo| <= 2^-9 |x| and |r| <= 2^-18 |x|, the products hi hi + hi lo + lo hi
+//      leave out at most 3 * 2^-18 sum |q||m|, and eight chained fp32 accumulations add at most
+//      2^-18 of it: |s~ - s| <= e = 2^-16 |q| max |m_g| (Cauchy-Schwarz; for a group, |q| is the
+//      norm of the sum of magnitudes, which also covers the fp32 sum over the heads).
+//   2. The k-th and (k+1)-th largest s~, a and b.  Scores above b + 2e are in and scores below
+//      a - 2e are out whatever the rounding; with a - b > 2e nothing is left between.
+//   3. The few blocks between are compared by their scores in 64 bits.
+//
+// Rows that leave more than 32 blocks open (equal keys, zero or non-finite queries) go to a
+// list that select_row_kernel works off, one CTA a row, all scores in 64 bits; it also takes
+// the calls of a few tokens, where there is no tile to fill.  A tile's time goes to the
+// selection of step 2 (a warp per row over shared memory), then to the products.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
 #include "selected.cuh"
+#include "warp_mma.cuh"
 
 namespace spr {
 namespace {
@@ -56,52 +71,34 @@ __device__ __forceinline__ unsigned long long score_key(double s) {
   return (u >> 63) ? ~u : (u | (1ull << 63));
 }
 
-// One warp per (batch, key head, token): every block's score in 64 bits, then the `top`
-// largest keys by binary search over the key's bits, ties to the lower block.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) select_exact_kernel(const SelArgs a, int* __restrict__ sel) {
-  extern __shared__ unsigned long long keys_smem[];
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long w = static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + warp;
-  if (w >= static_cast<long long>(a.Bt) * a.Hk * a.n) return;
-  unsigned long long* keys = keys_smem + static_cast<size_t>(warp) * a.nb;
-  const int t = static_cast<int>(w % a.n), z = static_cast<int>(w / a.n), b = z / a.Hk, kh = z % a.Hk;
-  int* out = sel + w * a.top;
-  double q[C] = {};
-  for (int h = 0; h < a.group; ++h) {
-    const T* p = static_cast<const T*>(a.q.p) + b * a.q.sb + (kh * a.group + h) * a.q.sh + t * a.q.sn + lane * C;
-#pragma unroll
-    for (int c = 0; c < C; ++c) q[c] += static_cast<double>(to_f32<T>(p[c]));
-  }
-  const int len = kv_len_of(a, b), pos = q_start_of(a, b) + t;
-  int last = len - 1;
+// What a token may select from: blocks [0, cand), of which the forced ones come first.
+struct Scope {
+  int cand, mine;
+};
+__device__ __forceinline__ Scope scope_of(const SelArgs& a, int b, int t) {
+  const int pos = q_start_of(a, b) + t;
+  int last = kv_len_of(a, b) - 1;
   if (a.causal) last = min(last, pos);
-  const int cand = last < 0 ? 0 : last / a.block + 1;  // candidates are blocks [0, cand)
-  const int mine = a.causal && pos >= 0 ? pos / a.block : -1;
-  const float* m = a.means + (static_cast<size_t>(z) * a.nb) * D + lane * C;
-  for (int g = 0; g < cand; ++g) {
-    double s = 0.0;
-#pragma unroll
-    for (int c = 0; c < C; ++c) s = fma(q[c], static_cast<double>(m[static_cast<size_t>(g) * D + c]), s);
-    s = warp_sum_d(s);
-    const bool forced = g < a.n_first || (a.causal && g <= mine && g > mine - a.n_local);
-    if (lane == 0) {
-      if (!forced && s != s) record_error(a.status, kErrNonFinite);
-      keys[g] = forced ? ~0ull : score_key(s);
-    }
-  }
-  __syncwarp();
-  const int want = min(a.top, cand);
+  return Scope{last < 0 ? 0 : last / a.block + 1, a.causal && pos >= 0 ? pos / a.block : -1};
+}
+__device__ __forceinline__ bool is_forced(const SelArgs& a, const Scope& s, int g) {
+  return g < a.n_first || (a.causal && g <= s.mine && g > s.mine - a.n_local);
+}
+
+// Writes the `want` largest of the keys of blocks [0, cand), ties to the lower block, ascending,
+// then -1.  One warp; the threshold by binary search over the key's bits.
+__device__ __forceinline__ void pick(const unsigned long long* keys, int cand, int top, int* out) {
+  const int lane = threadIdx.x & 31;
+  const int want = min(top, cand);
   // largest key value v with at least `want` keys >= v
   unsigned long long v = 0;
-  if (want < cand) {
-    for (int bit = 63; bit >= 0; --bit) {
-      const unsigned long long tryv = v | (1ull << bit);
-      int c = 0;
-      for (int g = lane; g < cand; g += 32) c += keys[g] >= tryv;
-      if (__reduce_add_sync(0xffffffffu, c) >= want) v = tryv;
-    }
+  int have = cand;
+  for (int bit = 63; bit >= 0 && have != want; --bit) {
+    const unsigned long long tryv = v | (1ull << bit);
+    int c = 0;
+    for (int g = lane; g < cand; g += 32) c += keys[g] >= tryv;
+    c = __reduce_add_sync(0xffffffffu, c);
+    if (c >= want) v = tryv, have = c;
   }
   int above = 0;
   for (int g = lane; g < cand; g += 32) above += keys[g] > v;
@@ -117,21 +114,311 @@ __global__ void __launch_bounds__(256) select_exact_kernel(const SelArgs a, int*
     n_out += __popc(tm);
     ties -= min(ties, __popc(eqm));
   }
-  for (int j = n_out + lane; j < a.top; j += 32) out[j] = -1;
+  for (int j = n_out + lane; j < top; j += 32) out[j] = -1;
+}
+
+// One CTA per row (batch, key head, token): eight lanes per block form its score in 64 bits,
+// then one warp picks.  Rows [0, rows), or those of `list` (its length at list[-1]).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) select_row_kernel(const SelArgs a, int* __restrict__ sel, const int* __restrict__ list,
+                                                         long long rows) {
+  extern __shared__ unsigned long long keys[];  // [nb]
+  constexpr int C = D / 8;
+  const int part = threadIdx.x & 7, grp = threadIdx.x >> 3;
+  if (list != nullptr) rows = __ldg(list - 1);
+  for (long long i = blockIdx.x; i < rows; i += gridDim.x) {
+    const long long w = list != nullptr ? list[i] : i;
+    const int t = static_cast<int>(w % a.n), z = static_cast<int>(w / a.n), b = z / a.Hk, kh = z % a.Hk;
+    const Scope sc = scope_of(a, b, t);
+    double q[C] = {};
+    for (int h = 0; h < a.group; ++h) {
+      const T* p = static_cast<const T*>(a.q.p) + b * a.q.sb + (kh * a.group + h) * a.q.sh + t * a.q.sn;
+#pragma unroll
+      for (int c = 0; c < C; ++c) q[c] += static_cast<double>(to_f32<T>(p[(c / 4) * 32 + part * 4 + c % 4]));
+    }
+    const float* m = a.means + static_cast<size_t>(z) * a.nb * D + part * 4;
+    for (int g0 = 0; g0 < sc.cand; g0 += 32) {
+      const int g = g0 + grp;
+      double s = 0.0;
+      if (g < sc.cand) {
+#pragma unroll
+        for (int c = 0; c < C; c += 4) {
+          const float4 x = __ldg(reinterpret_cast<const float4*>(m + static_cast<size_t>(g) * D + c * 8));
+          s = fma(q[c], static_cast<double>(x.x), s);
+          s = fma(q[c + 1], static_cast<double>(x.y), s);
+          s = fma(q[c + 2], static_cast<double>(x.z), s);
+          s = fma(q[c + 3], static_cast<double>(x.w), s);
+        }
+      }
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (part == 0 && g < sc.cand) {
+        const bool forced = is_forced(a, sc, g);
+        if (!forced && s != s) record_error(a.status, kErrNonFinite);
+        keys[g] = forced ? ~0ull : score_key(s);
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) pick(keys, sc.cand, a.top, sel + w * a.top);
+    __syncthreads();
+  }
+}
+
+// Tiles of ROWS tokens of one (batch, key head) against 64 blocks at a time.
+constexpr int kChunk = 64;
+
+template <int D, int ROWS>
+size_t tile_smem(int nb) {
+  const int ld = (nb + kChunk - 1) / kChunk * kChunk + 4;
+  return 2 * 2 * static_cast<size_t>(D) * (ROWS + kChunk) + sizeof(float) * ld * ROWS + sizeof(float) * ROWS +
+         8 * 32 * sizeof(int) + 16;
+}
+
+template <typename T, int D, int ROWS>
+__global__ void __launch_bounds__(256) select_tile_kernel(const SelArgs a, int* __restrict__ sel, int* __restrict__ list) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int kTileQ = ROWS * D * 2, kTileM = kChunk * D * 2;
+  constexpr int RG = ROWS / 16, CG = 8 / RG, NT = kChunk / CG / 8;  // warps over rows, columns; column tiles a warp
+  const int ld = ceil_div(a.nb, kChunk) * kChunk + 4;
+  const uint32_t sqh = smem_u32(smem), sql = sqh + kTileQ, smh = sql + kTileQ, sml = smh + kTileM;
+  float* score = reinterpret_cast<float*>(smem + 2 * kTileQ + 2 * kTileM);  // [ROWS][ld]
+  float* qn = score + static_cast<size_t>(ROWS) * ld;
+  int* open = reinterpret_cast<int*>(qn + ROWS);                            // [warp][32]
+  int* mmax = open + 8 * 32;                                                // bits of the largest mean norm squared
+  const int z = blockIdx.y, b = z / a.Hk, kh = z % a.Hk, t0 = blockIdx.x * ROWS;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the tile's last token sees the most
+  const int most = scope_of(a, b, min(t0 + ROWS, a.n) - 1).cand;
+  if (tid == 0) *mmax = 0;
+  auto put = [&](uint32_t hi_tile, uint32_t lo_tile, int r, int c, const float (&x)[8]) {  // 8 values at column c
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split_bf16x2(x[2 * i], x[2 * i + 1], h[i], l[i]);
+    const uint32_t at = swz<D>(r, c / 8);
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(hi_tile + at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(lo_tile + at), "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3]) : "memory");
+  };
+  // the group's query sums and the norms of their sums of magnitudes: D / 8 threads a row
+  for (int i = tid; i < ROWS * (D / 8); i += 256) {
+    const int r = i / (D / 8), c = i % (D / 8) * 8;
+    float x[8] = {}, y = 0.f, mag[8] = {};
+    if (t0 + r < a.n) {
+      for (int h = 0; h < a.group; ++h) {
+        const T* p = static_cast<const T*>(a.q.p) + b * a.q.sb + (kh * a.group + h) * a.q.sh + (t0 + r) * a.q.sn + c;
+        uint4 v[sizeof(T) / 2];
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) v[k] = reinterpret_cast<const uint4*>(p)[k];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float f = to_f32<T>(reinterpret_cast<const T*>(v)[k]);
+          x[k] += f;
+          mag[k] += fabsf(f);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y = fmaf(mag[k], mag[k], y);
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+    if (c == 0) qn[r] = sqrtf(y);
+    put(sqh, sql, r, c, x);
+  }
+  const int rg = warp % RG, cg = warp / RG;
+  for (int g0 = 0; g0 < most; g0 += kChunk) {
+    __syncthreads();  // the chunk before is read
+    for (int i = tid; i < kChunk * (D / 8); i += 256) {
+      const int r = i / (D / 8), c = i % (D / 8) * 8, g = g0 + r;
+      float x[8] = {}, y = 0.f;
+      if (g < most) {
+        const float4* p = reinterpret_cast<const float4*>(a.means + (static_cast<size_t>(z) * a.nb + g) * D + c);
+        const float4 u = __ldg(p), v = __ldg(p + 1);
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y = fmaf(x[k], x[k], y);
+#pragma unroll
+      for (int o = D / 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+      if (c == 0) atomicMax(mmax, __float_as_int(y != y ? __builtin_huge_valf() : y));  // order of nonnegative floats
+      put(smh, sml, r, c, x);
+    }
+    __syncthreads();
+    float hh[NT][4], rest[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) hh[n][k] = rest[n][k] = 0.f;
+#pragma unroll
+    for (int k2 = 0; k2 < D / 32; ++k2) {  // two 16-column steps
+      uint32_t ah[2][4], al[2][4];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const uint32_t at = swz<D>(rg * 16 + (lane & 15), (2 * k2 + s) * 2 + (lane >> 4));
+        ldmatrix_x4(ah[s], sqh + at);
+        ldmatrix_x4(al[s], sql + at);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint32_t bh[4], bl[4];
+        const uint32_t at = swz<D>((cg * NT + n) * 8 + (lane & 7), 4 * k2 + (lane >> 3));
+        ldmatrix_x4(bh, smh + at);
+        ldmatrix_x4(bl, sml + at);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          mma_bf16_16816(hh[n], ah[s], bh + 2 * s);
+          mma_bf16_16816(rest[n], ah[s], bl + 2 * s);
+          mma_bf16_16816(rest[n], al[s], bh + 2 * s);
+        }
+      }
+    }
+    float* out = score + static_cast<size_t>(rg * 16 + (lane >> 2)) * ld + g0 + cg * NT * 8 + (lane & 3) * 2;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      *reinterpret_cast<float2*>(out + n * 8) = make_float2(hh[n][0] + rest[n][0], hh[n][1] + rest[n][1]);
+      *reinterpret_cast<float2*>(out + 8 * ld + n * 8) = make_float2(hh[n][2] + rest[n][2], hh[n][3] + rest[n][3]);
+    }
+  }
+  __syncthreads();
+  const float mnorm = sqrtf(__int_as_float(*mmax));
+  int* my_open = open + warp * 32;
+  for (int r = warp; r < ROWS && t0 + r < a.n; r += 8) {
+    const long long w = static_cast<long long>(z) * a.n + t0 + r;
+    int* out = sel + w * a.top;
+    const Scope sc = scope_of(a, b, t0 + r);
+    const float* sr = score + static_cast<size_t>(r) * ld;
+    const float e2 = 2.f * 0x1p-16f * qn[r] * mnorm;  // 2e
+    int forced = 0;
+    if (sc.cand > 0) {
+      const int f0 = min(a.n_first, sc.cand);  // [0, f0) and [l0, l1)
+      const int l1 = a.causal ? min(sc.mine + 1, sc.cand) : 0, l0 = max(f0, sc.mine - a.n_local + 1);
+      forced = f0 + (a.causal ? max(0, l1 - l0) : 0);
+    }
+    const int want = min(a.top, sc.cand) - forced;  // of the blocks that are not forced
+    const int pool = sc.cand - forced;
+    const bool split = want > 0 && want < pool;  // some of them, not all
+    // scores above hi are in, scores in [lo, hi] open; bit j of `chosen`: the j-th open block is in
+    float lo = __builtin_huge_valf(), hi = __builtin_huge_valf();
+    unsigned chosen = 0;
+    bool slow = split && !(e2 < 0x1p100f);  // not finite
+    if (split && !slow) {
+      uint32_t v = 0;
+      int have = pool;
+      for (int bit = 31; bit >= 0 && have != want; --bit) {
+        const uint32_t tryv = v | (1u << bit);
+        int c = 0;
+        for (int g = lane; g < sc.cand; g += 32) c += float_order_key(sr[g]) >= tryv && !is_forced(a, sc, g);
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (c >= want) v = tryv, have = c;
+      }
+      // the want-th largest, and the one after it
+      uint32_t ka = 0xffffffffu, kb = 0;
+      for (int g = lane; g < sc.cand; g += 32) {
+        const uint32_t key = float_order_key(sr[g]);
+        if (is_forced(a, sc, g)) continue;
+        if (key >= v)
+          ka = min(ka, key);
+        else
+          kb = max(kb, key);
+      }
+      const float fa = float_from_order_key(__reduce_min_sync(0xffffffffu, ka));
+      const float fb = have > want ? fa : float_from_order_key(__reduce_max_sync(0xffffffffu, kb));
+      if (fa - fb > e2) {
+        hi = fb;
+      } else {
+        lo = fa - e2, hi = fb + e2;
+        int in = 0, mid = 0;
+        for (int g0 = 0; g0 < sc.cand; g0 += 32) {
+          const int g = g0 + lane;
+          const bool live = g < sc.cand && !is_forced(a, sc, g);
+          const float s = live ? sr[g] : 0.f;
+          in += __popc(__ballot_sync(0xffffffffu, live && s > hi));
+          const bool o = live && s >= lo && s <= hi;
+          const unsigned om = __ballot_sync(0xffffffffu, o);
+          const int at = mid + __popc(om & ((1u << lane) - 1u));
+          if (o && at < 32) my_open[at] = g;
+          mid += __popc(om);
+        }
+        __syncwarp();
+        slow = mid > 32;
+        if (!slow) {  // the open blocks' scores in 64 bits: lane j keeps the j-th's
+          constexpr int C = D / 32;
+          double q[C] = {};
+          for (int h = 0; h < a.group; ++h) {
+            const T* p = static_cast<const T*>(a.q.p) + b * a.q.sb + (kh * a.group + h) * a.q.sh + (t0 + r) * a.q.sn + lane * C;
+#pragma unroll
+            for (int c = 0; c < C; ++c) q[c] += static_cast<double>(to_f32<T>(p[c]));
+          }
+          double mine = 0.0;
+          for (int j = 0; j < mid; ++j) {
+            const float* m = a.means + (static_cast<size_t>(z) * a.nb + my_open[j]) * D + lane * C;
+            double s = 0.0;
+#pragma unroll
+            for (int c = 0; c < C; ++c) s = fma(q[c], static_cast<double>(__ldg(m + c)), s);
+            s = warp_sum_d(s);
+            if (lane == j) mine = s;
+          }
+          int before = 0;  // open blocks that come before this lane's
+          for (int j = 0; j < mid; ++j) {
+            const double s = __shfl_sync(0xffffffffu, mine, j);
+            before += s > mine || (s == mine && j < lane);
+          }
+          chosen = __ballot_sync(0xffffffffu, lane < mid && before < want - in);
+        }
+        __syncwarp();
+      }
+    }
+    if (slow) {
+      if (lane == 0) list[atomicAdd(list - 1, 1)] = static_cast<int>(w);
+      continue;
+    }
+    int n_out = 0, n_open = 0;
+    for (int g0 = 0; g0 < sc.cand; g0 += 32) {
+      const int g = g0 + lane;
+      const bool live = g < sc.cand, f = live && is_forced(a, sc, g);
+      const float s = live ? sr[g] : 0.f;
+      const bool o = split && live && !f && s >= lo && s <= hi;
+      const unsigned om = __ballot_sync(0xffffffffu, o);
+      bool take = f || (live && want >= pool);
+      if (split && live && !f) take = o ? (chosen >> (n_open + __popc(om & ((1u << lane) - 1u)))) & 1u : s > hi;
+      n_open += __popc(om);
+      const unsigned tm = __ballot_sync(0xffffffffu, take);
+      if (take) out[n_out + __popc(tm & ((1u << lane) - 1u))] = g;
+      n_out += __popc(tm);
+    }
+    for (int j = n_out + lane; j < a.top; j += 32) out[j] = -1;
+  }
 }
 
 template <typename T, int D>
-cudaError_t select_blocks(const SelArgs& a, int* sel, cudaStream_t st) {
-  // eight warps' keys in shared memory while they fit, fewer warps past that
-  int warps = 8;
-  while (warps > 1 && sizeof(unsigned long long) * a.nb * warps > 96 * 1024) warps /= 2;
-  const size_t smem = sizeof(unsigned long long) * a.nb * warps;
-  cudaError_t e = cudaFuncSetAttribute(select_exact_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
+cudaError_t row_select(const SelArgs& a, int* sel, const int* list, cudaStream_t st) {
+  const size_t smem = sizeof(unsigned long long) * a.nb;
   const long long rows = static_cast<long long>(a.Bt) * a.Hk * a.n;
-  select_exact_kernel<T, D><<<static_cast<unsigned>((rows + warps - 1) / warps), 32 * warps, smem, st>>>(a, sel);
+  const unsigned grid = static_cast<unsigned>(list != nullptr ? 2 * 148 : rows < 8 * 148 ? rows : 8 * 148);
+  select_row_kernel<T, D><<<grid, 256, smem, st>>>(a, sel, list, rows);
   return counted(cudaGetLastError(), 1);
+}
+
+template <typename T, int D, int ROWS>
+cudaError_t tile_select(const SelArgs& a, int* sel, cudaStream_t st) {
+  cudaError_t e = cudaMemsetAsync(a.slow, 0, sizeof(int), st);
+  if (e != cudaSuccess) return e;
+  const size_t smem = tile_smem<D, ROWS>(a.nb);
+  e = cudaFuncSetAttribute(select_tile_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  select_tile_kernel<T, D, ROWS><<<dim3(ceil_div(a.n, ROWS), a.Bt * a.Hk), 256, smem, st>>>(a, sel, a.slow + 1);
+  if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
+  return row_select<T, D>(a, sel, a.slow + 1, st);
+}
+
+// Up to eight tokens a head leave a tile of 16 half empty: one CTA a row.  Otherwise the tallest
+// tile whose scores fit in shared memory (a mean is read once per tile).
+template <typename T, int D>
+cudaError_t select_blocks(const SelArgs& a, int* sel, cudaStream_t st) {
+  if (a.n <= 8) return row_select<T, D>(a, sel, nullptr, st);
+  constexpr size_t kMost = 227 * 1024;
+  if (tile_smem<D, 64>(a.nb) <= kMost) return tile_select<T, D, 64>(a, sel, st);
+  if (tile_smem<D, 32>(a.nb) <= kMost) return tile_select<T, D, 32>(a, sel, st);
+  return tile_select<T, D, 16>(a, sel, st);
 }
 
 }  // namespace

@@ -55,6 +55,7 @@ struct SelArgs {
   float* lse;            // [Bt, Hq, n]
   const float* means;    // [Bt, Hk, nb, d]
   int* status;
+  int* slow;             // select: number of rows left to select_row_kernel, then the rows
   // lists: per region (batch, key head, slice of `slice` tokens), `slices` regions per head
   int slice, slices;
   int subs;              // sub-slices of a slice
@@ -89,6 +90,9 @@ cudaError_t launch_lists(const SelArgs& a, cudaStream_t st);
 // One chunk of `count` regions starting at region `first`.
 cudaError_t launch_selected_forward(const SelArgs& a, int first, int count, cudaStream_t st);
 cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cudaStream_t st);
+// The single-token form: whether it takes this call, and the whole of it in one launch.
+bool use_decode(const SelArgs& a);
+cudaError_t launch_decode(const SelArgs& a, cudaStream_t st);
 cudaError_t launch_delta(const SelArgs& a, cudaStream_t st);
 
 }  // namespace spr

@@ -86,7 +86,7 @@ constexpr size_t kPartialBytes = 1ull << 30;
 // status header).
 struct Plan {
   int regions, chunk;  // chunk: regions per launch
-  size_t offs, list, inv, units, n_units, blk, part, ml, delta, seg, total;
+  size_t slow, offs, list, inv, units, n_units, blk, part, ml, delta, seg, total;
 };
 
 Plan make_plan(SelArgs& a, bool backward) {
@@ -119,6 +119,8 @@ Plan make_plan(SelArgs& a, bool backward) {
     return at;
   };
   const size_t R = L.regions;
+  // the selection's list comes first: its place depends on nothing else
+  L.slow = take(sizeof(int) * (static_cast<size_t>(a.Bt) * a.Hk * a.n + 1));
   L.offs = take(sizeof(int) * R * a.nb * a.subs);
   L.list = take(sizeof(int) * R * entries);
   L.inv = take(sizeof(int) * static_cast<size_t>(a.Bt) * a.Hk * a.n * a.top);
@@ -140,6 +142,7 @@ T* at(void* ws, size_t off) {
 
 void bind(SelArgs& a, const Plan& L, void* ws) {
   a.status = at<int>(ws, 0);
+  a.slow = at<int>(ws, L.slow);
   a.offs = at<int>(ws, L.offs);
   a.list = at<int>(ws, L.list);
   a.inv = at<int>(ws, L.inv);
@@ -229,7 +232,8 @@ int sparsepr_select_blocks(const sparsepr_selected* p, const sparsepr_view* Q, c
   if (means == nullptr || sel == nullptr || ws == nullptr) return bad("null pointer argument");
   if ((reinterpret_cast<uintptr_t>(means) & 15u) != 0) return bad("means must start on a 16-byte boundary");
   SelArgs a = base_args(p);
-  a.q = view(Q), a.means = means, a.status = at<int>(ws, 0);
+  bind(a, make_plan(a, false), ws);
+  a.q = view(Q), a.means = means;
   return cuda_status(spr::launch_select(a, sel, reinterpret_cast<cudaStream_t>(stream)), "select blocks");
 }
 
@@ -247,6 +251,7 @@ int sparsepr_selected_attn(const sparsepr_selected* p, const sparsepr_view* Q, c
   const Plan L = make_plan(a, false);
   bind(a, L, ws);
   a.q = view(Q), a.k = view(K), a.v = view(V), a.o = view(O), a.sel = sel, a.lse = lse;
+  if (spr::use_decode(a)) return cuda_status(spr::launch_decode(a, st), "selected attention: few tokens");
   if ((rc = cuda_status(spr::launch_lists(a, st), "selected attention: lists"))) return rc;
   for (int r = 0; r < L.regions; r += L.chunk)
     if ((rc = cuda_status(spr::launch_selected_forward(a, r, std::min(L.chunk, L.regions - r), st), "selected attention")))
