@@ -35,11 +35,15 @@ constexpr int kSub = 512;
 // Blocks per head that the lists' shared-memory masks hold.
 constexpr int kMaxBlocks = 2048;
 
+// CTAs of the tensor-core kernels: one per SM.
+constexpr int kTcShares = 148;
+
 // One work item of the attention kernels: rows [r0, r0 + rows) of the entries of key block g,
 // whose first entry is `off` of its region's list; row r is query head r % group of entry r / group.
-// rows = 0: none.  live, qs: the length and the position of query 0, both from the block's first key on.
-struct __align__(32) Unit {
-  int g, off, r0, rows, live, qs, b, kh;
+// rows = 0: none.  live, qs: the length and the position of query 0, both from the block's first
+// key on.  total: the block's rows in this region.
+struct __align__(16) Unit {
+  int g, off, r0, rows, live, qs, b, kh, total, pad[3];
 };
 
 struct SelArgs {
@@ -65,7 +69,7 @@ struct SelArgs {
   int unit_rows, unit_cap;
   Unit* units;           // [regions][unit_cap], the last ones empty
   int* n_units;          // [regions]
-  int2* blk;             // [regions][nb] {segments, first slot of the segment sums}
+  int4* blk;             // [regions][nb] {units, first slot of their sums where there are more, first unit, -}
   // partial rows of one chunk of regions: fp32 [chunk regions][slice * top * group][d], or fp16
   // in planes of 64 columns (selected_tc.cu)
   float* part;

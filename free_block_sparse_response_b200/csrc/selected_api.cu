@@ -92,8 +92,8 @@ struct Plan {
 Plan make_plan(SelArgs& a, bool backward) {
   Plan L{};
   const long long subs = spr::ceil_div(a.n, spr::kSub);
-  // the tensor-core forward pass keeps its partial rows in fp16
-  const size_t val = backward || a.f32 ? sizeof(float) : 2;
+  // the tensor-core kernels keep their partial rows in fp16
+  const size_t val = a.f32 ? sizeof(float) : 2;
   const size_t row = val * a.d + sizeof(float2);
   const size_t sub_bytes = row * spr::kSub * a.top * a.group;
   // A backward region is a head's whole token range, so that a key block's gradient is
@@ -109,9 +109,10 @@ Plan make_plan(SelArgs& a, bool backward) {
   const long long entries = static_cast<long long>(a.slice) * a.top, rows = entries * a.group;
   L.chunk = static_cast<int>(std::min<long long>(L.regions, std::max<long long>(1, kPartialBytes / (row * rows))));
   a.plane = rows * L.chunk;
-  a.unit_rows = backward ? 2048 : a.f32 ? 512 : 128;  // the tensor-core forward pass works tile by tile
+  a.unit_rows = !a.f32 ? 128 : backward ? 2048 : 512;  // the tensor-core kernels work tile by tile
   a.unit_cap = a.nb + static_cast<int>(rows / a.unit_rows);
-  a.seg_cap = backward ? static_cast<int>(2 * (rows / a.unit_rows)) + 2 : 0;
+  // sums of split blocks: per region in fp32, two per CTA on the tensor cores
+  a.seg_cap = backward && a.f32 ? static_cast<int>(2 * (rows / a.unit_rows)) + 2 : 0;
   size_t off = 256;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -126,11 +127,12 @@ Plan make_plan(SelArgs& a, bool backward) {
   L.inv = take(sizeof(int) * static_cast<size_t>(a.Bt) * a.Hk * a.n * a.top);
   L.units = take(sizeof(spr::Unit) * R * a.unit_cap);
   L.n_units = take(sizeof(int) * R);
-  L.blk = take(sizeof(int2) * R * a.nb);
+  L.blk = take(sizeof(int4) * R * a.nb);
   L.part = take(val * a.d * rows * L.chunk);
-  L.ml = take(backward ? 0 : sizeof(float2) * rows * L.chunk);
+  L.ml = take(backward && a.f32 ? 0 : sizeof(float2) * rows * L.chunk);
   L.delta = take(backward ? sizeof(float) * static_cast<size_t>(a.Bt) * a.Hq * a.n : 0);
-  L.seg = take(sizeof(float) * 2 * a.block * a.d * static_cast<size_t>(a.seg_cap) * L.chunk);
+  L.seg = take(sizeof(float) * 2 * a.block * a.d *
+               (!backward ? 0 : a.f32 ? static_cast<size_t>(a.seg_cap) * L.chunk : 2 * size_t{spr::kTcShares}));
   L.total = off;
   return L;
 }
@@ -148,7 +150,7 @@ void bind(SelArgs& a, const Plan& L, void* ws) {
   a.inv = at<int>(ws, L.inv);
   a.units = at<spr::Unit>(ws, L.units);
   a.n_units = at<int>(ws, L.n_units);
-  a.blk = at<int2>(ws, L.blk);
+  a.blk = at<int4>(ws, L.blk);
   a.part = at<float>(ws, L.part);
   a.ml = at<float2>(ws, L.ml);
   a.delta = at<float>(ws, L.delta);

@@ -1,5 +1,5 @@
-// Selected-block attention and its backward pass on the fp32 pipes (any type), and the
-// passes that join the partial rows.
+// Selected-block attention and its backward pass in fp32 (on the fp32 pipes), and the passes that
+// join their partial rows.
 //
 // Mathematics: query row i attends to the keys of its selected blocks.  With block g's
 //   m_ig = max_j s_ij,  l_ig = sum_j exp(s_ij - m_ig),  o_ig = sum_j exp(s_ij - m_ig) v_j
@@ -24,27 +24,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <typename T>
-__device__ __forceinline__ float4 load4(const T* p);
-template <>
-__device__ __forceinline__ float4 load4<float>(const float* p) {
+__device__ __forceinline__ float4 load4(const T* p) {
   return *reinterpret_cast<const float4*>(p);
 }
-template <>
-__device__ __forceinline__ float4 load4<__nv_bfloat16>(const __nv_bfloat16* p) {
-  const uint2 v = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
-                     __uint_as_float(v.y & 0xffff0000u));
-}
 template <typename T>
-__device__ __forceinline__ void store4(T* p, float4 v);
-template <>
-__device__ __forceinline__ void store4<float>(float* p, float4 v) {
+__device__ __forceinline__ void store4(T* p, float4 v) {
   *reinterpret_cast<float4*>(p) = v;
-}
-template <>
-__device__ __forceinline__ void store4<__nv_bfloat16>(__nv_bfloat16* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 template <typename T>
@@ -395,7 +380,7 @@ __global__ void __launch_bounds__(kBwdThreads) backward_kernel(const SelArgs a, 
     }
   }
   // a block with one unit writes its gradients; a split block's sums wait for their join
-  const int2 bk = a.blk[static_cast<size_t>(region) * a.nb + un.g];
+  const int4 bk = a.blk[static_cast<size_t>(region) * a.nb + un.g];
   const bool split = bk.x > 1;
   float* seg = a.seg + (static_cast<size_t>(ci) * a.seg_cap + bk.y + un.r0 / a.unit_rows) * 2 * B * D;
 #pragma unroll
@@ -418,7 +403,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(256) join_kv_kernel(const SelArgs a, int first) {
   const int g = blockIdx.x, region = first + blockIdx.y, z = region / a.slices;
   const int b = z / a.Hk, kh = z % a.Hk;
-  const int2 bk = a.blk[static_cast<size_t>(region) * a.nb + g];
+  const int4 bk = a.blk[static_cast<size_t>(region) * a.nb + g];
   if (bk.x == 1) return;
   const size_t tile = static_cast<size_t>(a.block) * D;
   const float* seg = a.seg + (static_cast<size_t>(blockIdx.y) * a.seg_cap + bk.y) * 2 * tile;
@@ -500,13 +485,6 @@ cudaError_t delta(const SelArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-#define SPR_SHAPES(fn, ...)                                                                                        \
-  (a.f32 ? (a.d == 128 ? (a.block == 128 ? fn<float, 128, 128>(__VA_ARGS__) : fn<float, 128, 64>(__VA_ARGS__))       \
-                       : (a.block == 128 ? fn<float, 64, 128>(__VA_ARGS__) : fn<float, 64, 64>(__VA_ARGS__)))        \
-         : (a.d == 128                                                                                             \
-                ? (a.block == 128 ? fn<__nv_bfloat16, 128, 128>(__VA_ARGS__) : fn<__nv_bfloat16, 128, 64>(__VA_ARGS__)) \
-                : (a.block == 128 ? fn<__nv_bfloat16, 64, 128>(__VA_ARGS__) : fn<__nv_bfloat16, 64, 64>(__VA_ARGS__))))
-
 cudaError_t launch_selected_forward(const SelArgs& a, int first, int count, cudaStream_t st) {
   if (!a.f32) return launch_selected_forward_tc(a, first, count, st);
   if (a.d == 128)
@@ -515,7 +493,10 @@ cudaError_t launch_selected_forward(const SelArgs& a, int first, int count, cuda
 }
 
 cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cudaStream_t st) {
-  return SPR_SHAPES(backward, a, first, count, st);
+  if (!a.f32) return launch_selected_backward_tc(a, first, count, st);
+  if (a.d == 128)
+    return a.block == 128 ? backward<float, 128, 128>(a, first, count, st) : backward<float, 128, 64>(a, first, count, st);
+  return a.block == 128 ? backward<float, 64, 128>(a, first, count, st) : backward<float, 64, 64>(a, first, count, st);
 }
 
 cudaError_t launch_delta(const SelArgs& a, cudaStream_t st) {

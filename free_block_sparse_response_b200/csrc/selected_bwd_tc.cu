@@ -1,0 +1,413 @@
+// Backward pass of selected-block attention on the 5th-generation tensor cores (bf16).
+//
+// Mathematics as in selected_attn.cu.  A tile is 128 of the query rows that selected a block;
+// with Q and dO (128 x D) gathered and K and V (B x D) of the block in shared memory,
+//   S = Q K^T, dP = dO V^T                        (128 x B, TMEM)
+//   P = exp(S tau - lse), dS = P (dP - delta)     (bf16, shared memory; tau joins the outputs)
+//   dQ part = dS K (128 x D),  dV^T += dO^T P,  dK^T += Q^T dS  (D x B, TMEM across the tiles)
+// dV and dK are formed transposed, so that their M is D and both operands are read as they lie
+// (rows of the contraction).  At D = 64 one product with M = 128 does both: [dO | Q]^T [P | dS],
+// whose diagonal quarters are dV^T and dK^T.
+//
+// Every CTA takes an equal, contiguous share of the tiles in the order region, block, row.  A
+// block inside one share is written directly; a block that a share's end cuts leaves one fp32
+// sum per CTA (two slots each), added in order by join_kv_tc_kernel: the same in every run.
+// dQ parts go out as in the forward pass (fp16 with a power of two per row, planes of 64).
+//
+// Work of a tile (B = D = 128): 21 MFLOP, 16K exponentials, 64 KB gathered, 32 KB written.
+// Shared memory holds one Q / dO stage beside K, V, P and dS at B = D = 128 (192 KB), two
+// otherwise; TMEM is full (dQ goes over S), so a tile's stages follow one another: products of
+// two tiles do not overlap, the next gather runs under the output.
+//   warps 0-7   softmax and output: two threads a row, half the keys each; dQ and, at a block's
+//               end, dK and dV out of TMEM;
+//   warps 8-11  gather Q and dO rows, their lse, delta and visible keys;
+//   warp 12     issues the products;  warp 13 TMA boxes of K and V, zeros from the length on.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "selected.cuh"
+#include "selected_tc.cuh"
+#include "tcgen05.cuh"
+#include "warp_mma.cuh"
+
+namespace spr {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kInf = __builtin_huge_valf();
+
+constexpr int kThreads = 448, kWork = 256, kLoaders = 128;
+constexpr int kLoadWarp = 8, kMmaWarp = 12;
+
+template <int D, int B>
+struct Bwd {
+  static constexpr uint32_t kRowsD = 128 * D * 2, kRowsB = 128 * B * 2, kKV = B * D * 2;
+  static constexpr int kStages = D == 128 && B == 128 ? 1 : 2;
+  static constexpr uint32_t kTail = 2 * 128 * 12 + 512;  // lse, delta and visible keys of a stage's rows; barriers
+  static constexpr uint32_t kSmem = 2 * kKV + 2 * kRowsB + kStages * 2 * kRowsD + kTail;
+};
+
+enum : int { kKvLand = 0, kKv, kKvFree, kS, kP, kDq, kDqFree, kAcc, kAccFree, kDrain, kQ, kQFree = kQ + 2, kNumBars = kQFree + 2 };
+
+template <int D, int B>
+__global__ void __launch_bounds__(kThreads, 1)
+    selected_backward_tc_kernel(const __grid_constant__ BlockMap mk, const __grid_constant__ BlockMap mv, const SelArgs a,
+                                int first, int count) {
+  using F = Bwd<D, B>;
+  constexpr int ST = F::kStages;
+  extern __shared__ __align__(1024) uint8_t dsmem[];
+  uint8_t* const tail = dsmem + F::kSmem - F::kTail;
+  float* const s_row = reinterpret_cast<float*>(tail);  // [stage][lse | delta | visible keys][128]
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(tail + 2 * 128 * 12);
+  uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(bars + kNumBars);
+  int& abort_flag = *reinterpret_cast<int*>(bars + kNumBars + 1);
+  int* const s_first = reinterpret_cast<int*>(bars + kNumBars + 2);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sK = tc::saddr(dsmem), sV = sK + F::kKV, sP = sV + F::kKV, sdS = sP + F::kRowsB, sRows = sdS + F::kRowsB;
+  // of a stage: dO, then Q (adjacent: one operand of 128 columns at D = 64)
+  auto sG = [&](int st) { return sRows + st * 2 * F::kRowsD; };
+  auto sQ = [&](int st) { return sG(st) + F::kRowsD; };
+  if ((sK & 1023u) != 0) {  // the tiles' swizzle counts from 1024-byte lines
+    if (tid == 0) record_error(a.status, kErrCuda);
+    return;
+  }
+  auto bar = [&](int i) { return tc::saddr(&bars[i]); };
+  if (tid == 0) {
+    tc::mbar_init(bar(kKvLand), 1);
+    tc::mbar_init(bar(kKv), 32);
+    tc::mbar_init(bar(kKvFree), 1);
+    tc::mbar_init(bar(kS), 1);
+    tc::mbar_init(bar(kP), kWork);
+    tc::mbar_init(bar(kDq), 1);
+    tc::mbar_init(bar(kDqFree), kWork);
+    tc::mbar_init(bar(kAcc), 1);
+    tc::mbar_init(bar(kAccFree), kWork);
+    tc::mbar_init(bar(kDrain), 1);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(bar(kQ + i), kLoaders);
+      tc::mbar_init(bar(kQFree + i), 1);
+    }
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(tc::saddr(&tmem_slot), 512);
+    tc::tmem_relinquish();
+  }
+  if (warp == 0) share_of_tiles(a, first, count, s_first);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tS = tmem_slot, tDp = tS + 128, tAcc = tS + 256;  // dQ over S; dV^T, then dK^T from column B on
+  volatile int* abort_v = &abort_flag;
+  const size_t cap = static_cast<size_t>(a.slice) * a.top;
+  auto wait1 = [&](int i, int phase) { return wait_bar(bar(i), phase & 1, abort_v, a.status); };
+  auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, wait1(i, phase)); };
+
+  if (warp < kLoadWarp) {
+    // ---------------------------------------------------------------- softmax, output
+    const int w4 = warp & 3, half = warp >> 2, row = 32 * w4 + lane;
+    const uint32_t lanes = static_cast<uint32_t>(32 * w4) << 16;
+    const float scale2 = a.scale * kLog2e;
+    uint8_t* const part = static_cast<uint8_t*>(static_cast<void*>(a.part));
+    bool cut_open = false;
+    each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int u, bool opens, bool closes) {
+      const int st = t % ST;
+      if (!wait(kQ + st, t / ST) || !wait(kS, t)) return false;  // the row's numbers; S and dP
+      tc::fence_after_sync();
+      const float* rd = s_row + st * 3 * 128 + row;
+      const float lse2 = rd[0], delta = rd[128];
+      const int nv = __float_as_int(rd[256]);
+#pragma unroll 1
+      for (int c0 = half * (B / 2); c0 < (half + 1) * (B / 2); c0 += 32) {
+        uint32_t s[32], dp[32];
+        tc::tmem_ld32(tS + lanes + c0, s);
+        tc::tmem_ld32(tDp + lanes + c0, dp);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c8 = 0; c8 < 4; ++c8) {
+          uint32_t p4[4], d4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = 8 * c8 + 2 * i;
+            float p0 = ex2(fmaf(__uint_as_float(s[c]), scale2, -lse2)), p1 = ex2(fmaf(__uint_as_float(s[c + 1]), scale2, -lse2));
+            float d0 = p0 * (__uint_as_float(dp[c]) - delta), d1 = p1 * (__uint_as_float(dp[c + 1]) - delta);
+            if (c0 + c >= nv) p0 = d0 = 0.f;
+            if (c0 + c + 1 >= nv) p1 = d1 = 0.f;
+            p4[i] = pack_bf16x2(p0, p1);
+            d4[i] = pack_bf16x2(d0, d1);
+          }
+          const uint32_t off = tc::sw128_offset(row, c0 / 8 + c8);
+          st_shared_16(sP + off, p4[0], p4[1], p4[2], p4[3]);
+          st_shared_16(sdS + off, d4[0], d4[1], d4[2], d4[3]);
+        }
+      }
+      tc::fence_proxy_async();
+      tc::fence_before_sync();
+      tc::mbar_arrive(bar(kP));
+      // dQ: this warp's 16 rows (see the forward kernel's output)
+      if (!wait(kDq, t)) return false;
+      tc::fence_after_sync();
+      {
+        const int lane0 = 32 * w4 + 16 * half, q = lane >> 2, i = lane & 3;
+        uint32_t o[D / 2];
+#pragma unroll
+        for (int c = 0; c < D; c += 64)
+          tmem_ld_16x64(tS + (static_cast<uint32_t>(lane0) << 16) + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c / 2]));
+        tc::tmem_wait_ld();
+        tc::fence_before_sync();
+        tc::mbar_arrive(bar(kDqFree));
+        const float unit[2] = {1.f, 1.f};
+        float up[2];
+        const long long out0 = static_cast<long long>((ci * cap + un.off) * a.group + un.r0);
+        store_part<D>(o, unit, lane0 + q, un.rows, part + 32 * i, a.plane, out0, up);
+        if (i == 0) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (lane0 + q + 8 * k < un.rows) a.ml[out0 + lane0 + q + 8 * k] = make_float2(0.f, up[k] * a.scale);
+        }
+      }
+      if (opens) cut_open = un.r0 > 0;  // the block's first tiles are another CTA's
+      if (!closes) return true;
+      // dK and dV: lane = head dim, columns = keys
+      if (!wait(kAcc, u)) return false;
+      tc::fence_after_sync();
+      const bool cut = cut_open || un.r0 + un.rows < un.total;
+      const int which = D == 128 ? half : w4 >> 1;  // 0: dV, 1: dK
+      const int d = D == 128 ? row : row & 63;
+      const int from = D == 128 ? 0 : half * (B / 2), to = D == 128 ? B : from + B / 2;
+      const View& out = which ? a.gk : a.gv;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.p) + un.b * out.sb + un.kh * out.sh +
+                           static_cast<long long>(un.g) * B * out.sn + d;
+      float* seg = a.seg + (static_cast<size_t>(2 * blockIdx.x + (u > 0)) * 2 + which) * B * D + d;
+      const float f = which ? a.scale : 1.f;
+      const int keys = min(B, a.nk - un.g * B);
+#pragma unroll 1
+      for (int c0 = from; c0 < to; c0 += 32) {
+        uint32_t x[32];
+        tc::tmem_ld32(tAcc + lanes + which * B + c0, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float y = __uint_as_float(x[c]) * f;
+          if (cut)
+            seg[static_cast<size_t>(c0 + c) * D] = y;
+          else if (c0 + c < keys)
+            dst[(c0 + c) * out.sn] = __float2bfloat16_rn(y);
+        }
+      }
+      tc::fence_before_sync();
+      tc::mbar_arrive(bar(kAccFree));
+      return true;
+    });
+  } else if (warp < kMmaWarp) {
+    // ---------------------------------------------------------------- Q and dO rows, 32 a warp
+    constexpr int kPer = D / 8, kStep = 32 / kPer;  // lanes per row, rows per instruction
+    const int lw = warp - kLoadWarp, ch = lane % kPer;
+    each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
+      const int st = t % ST, r = 32 * lw + lane;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.p) + un.b * a.q.sb + un.kh * a.group * a.q.sh + ch * 8;
+      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.go.p) + un.b * a.go.sb + un.kh * a.group * a.go.sh + ch * 8;
+      int tok = -1, h = 0, nv = 0;
+      float lse2 = 0.f, delta = 0.f;
+      if (r < un.rows) {
+        const int e = (un.r0 + r) / a.group;
+        tok = __ldg(a.list + (first + ci) * cap + un.off + e);
+        h = un.r0 + r - e * a.group;
+        const size_t at = (static_cast<size_t>(un.b) * a.Hq + un.kh * a.group + h) * a.n + tok;
+        lse2 = __ldg(a.lse + at) * kLog2e;
+        delta = a.delta[at];
+        nv = a.causal ? min(un.live, un.qs + tok + 1) : un.live;
+        if (lse2 == -kInf) nv = 0;  // a zero row of the forward pass
+      }
+      if (t >= ST && !wait(kQFree + st, t / ST - 1)) return false;
+      float* rd = s_row + st * 3 * 128 + r;
+      rd[0] = lse2, rd[128] = delta, rd[256] = __int_as_float(nv);
+#pragma unroll
+      for (int s = 0; s < 32; s += kStep) {
+        const int src = s + lane / kPer;
+        const long long tk = __shfl_sync(0xffffffffu, tok, src);
+        const int hh = __shfl_sync(0xffffffffu, h, src);
+        const uint32_t off = tc::sw128_offset(32 * lw + src, ch);
+        cp_async_16(sQ(st) + off, tk < 0 ? q : q + tk * a.q.sn + hh * a.q.sh, tk < 0 ? 0 : 16);
+        cp_async_16(sG(st) + off, tk < 0 ? g : g + tk * a.go.sn + hh * a.go.sh, tk < 0 ? 0 : 16);
+      }
+      cp_async_commit();
+      cp_async_wait<0>();
+      tc::fence_proxy_async();
+      tc::mbar_arrive(bar(kQ + st));
+      return true;
+    });
+    cp_async_wait<0>();
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- products
+    constexpr uint32_t kIdS = tc::idesc_bf16(128, B, false, false), kIdQ = tc::idesc_bf16(128, D, false, true);
+    constexpr uint32_t kIdAcc = tc::idesc_bf16(128, D == 128 ? B : 2 * B, true, true);
+    if (lane == 0) {
+      each_tile(a, first, s_first, 0, 1, [&](const Unit&, int, int t, int u, bool opens, bool closes) {
+        const int st = t % ST;
+        if (opens && !wait1(kKv, u)) return false;
+        if (!wait1(kQ + st, t / ST)) return false;
+        if (t > 0 && !wait1(kDqFree, t - 1)) return false;  // dQ, over S, is read
+        tc::fence_after_sync();
+        uint64_t dq = tc::sdesc_sw128(sQ(st), 16, 1024), dk = tc::sdesc_sw128(sK, 16, 1024);
+        uint64_t dg = tc::sdesc_sw128(sG(st), 16, 1024), dv = tc::sdesc_sw128(sV, 16, 1024);
+        keep_here(dq, dk);
+        keep_here(dg, dv);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc::mma_ss(tS, dq + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
+                     dk + ((kk >> 2) * (B * 128) + (kk & 3) * 32) / 16, kIdS, kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          tc::mma_ss(tDp, dg + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
+                     dv + ((kk >> 2) * (B * 128) + (kk & 3) * 32) / 16, kIdS, kk > 0 ? 1u : 0u);
+        tc::mma_commit(bar(kS));
+        if (!wait1(kP, t)) return false;
+        if (opens && u > 0 && !wait1(kAccFree, u - 1)) return false;
+        tc::fence_after_sync();
+        uint64_t ds = tc::sdesc_sw128(sdS, 16, 1024), kt = tc::sdesc_sw128(sK, B * 128, 1024);
+        keep_here(ds, kt);
+#pragma unroll
+        for (int kk = 0; kk < B / 16; ++kk)
+          tc::mma_ss(tS, ds + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16, kt + kk * (2048 / 16), kIdQ, kk > 0 ? 1u : 0u);
+        tc::mma_commit(bar(kDq));
+        // contraction over the 128 rows: both operands rows apart, 64-column blocks 16 KB apart
+        uint64_t gt = tc::sdesc_sw128(sG(st), 128 * 128, 1024), pt = tc::sdesc_sw128(sP, 128 * 128, 1024);
+        keep_here(gt, pt);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc::mma_ss(tAcc, gt + kk * (2048 / 16), pt + kk * (2048 / 16), kIdAcc, !opens || kk > 0 ? 1u : 0u);
+        if (D == 128) {
+          uint64_t qt = tc::sdesc_sw128(sQ(st), 128 * 128, 1024), dt = tc::sdesc_sw128(sdS, 128 * 128, 1024);
+          keep_here(qt, dt);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc::mma_ss(tAcc + B, qt + kk * (2048 / 16), dt + kk * (2048 / 16), kIdAcc, !opens || kk > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(bar(kQFree + st));
+        if (closes) {
+          tc::mma_commit(bar(kAcc));
+          tc::mma_commit(bar(kKvFree));
+        }
+        return true;
+      });
+      tc::mma_commit(bar(kDrain));  // every product has finished before TMEM goes back
+      tc::mbar_wait_quiet(bar(kDrain), 0);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- K and V of each block
+    int issued = 0;
+    const bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int, int, int u, bool opens, bool) {
+      if (!opens) return true;
+      if (u > 0 && !wait(kKvFree, u - 1)) return false;
+      if (lane == 0) {
+        tc::mbar_arrive_expect_tx(bar(kKvLand), 2 * F::kKV);
+#pragma unroll
+        for (int c = 0; c < D; c += 64) {
+          load_box(sK + c * (B * 2), mk, c, un.g * B, un.kh, un.b, bar(kKvLand));
+          load_box(sV + c * (B * 2), mv, c, un.g * B, un.kh, un.b, bar(kKvLand));
+        }
+      }
+      __syncwarp();
+      issued = u + 1;
+      if (!wait(kKvLand, u)) return false;
+      for (int i = lane; i < (B - un.live) * (D / 8); i += 32) {  // rows of the block from the length on
+        const uint32_t off = sw128_rows<B>(un.live + i / (D / 8), i % (D / 8));
+        st_shared_zero(sK + off);
+        st_shared_zero(sV + off);
+      }
+      tc::fence_proxy_async();
+      tc::mbar_arrive(bar(kKv));
+      return true;
+    });
+    // boxes still in flight after an abort land before the CTA exits
+    if (!ok && lane == 0 && issued > 0) tc::mbar_wait_quiet(bar(kKvLand), (issued - 1) & 1);
+    __syncwarp();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    __syncwarp();
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tS, 512);
+  }
+}
+
+// dK and dV of the blocks that shares cut (their CTAs' sums, in order) and of blocks that no
+// query selected.  One CTA per (block, region of the chunk); `shares` CTAs ran the backward kernel.
+template <int D>
+__global__ void __launch_bounds__(256) join_kv_tc_kernel(const SelArgs a, int first, int count, int shares) {
+  __shared__ int s_sum, s_before;
+  const int g = blockIdx.x, ci = blockIdx.y, region = first + ci, z = region / a.slices, b = z / a.Hk, kh = z % a.Hk;
+  const int4 bk = a.blk[static_cast<size_t>(region) * a.nb + g];  // tiles, -, first tile of its region
+  int c0 = 0, c1 = -1;
+  long long t0 = 0;
+  if (bk.x > 0) {
+    if (threadIdx.x == 0) s_sum = s_before = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < count; i += blockDim.x) {
+      const int n = __ldg(a.n_units + first + i);
+      atomicAdd(&s_sum, n);
+      if (i < ci) atomicAdd(&s_before, n);
+    }
+    __syncthreads();
+    const long long sum = s_sum;
+    t0 = s_before + bk.z;
+    // share c holds tiles [sum c / shares, sum (c + 1) / shares)
+    auto share = [&](long long t) {
+      int c = static_cast<int>(t * shares / sum);
+      while (sum * (c + 1) / shares <= t) ++c;
+      while (sum * c / shares > t) --c;
+      return c;
+    };
+    c0 = share(t0), c1 = share(t0 + bk.x - 1);
+    if (c0 == c1) return;  // written by its one CTA
+  }
+  const size_t tile = static_cast<size_t>(a.block) * D;
+  const long long sum = bk.x > 0 ? s_sum : 0;
+  for (int i = threadIdx.x * 4; i < a.block * D; i += 1024) {
+    const int j = g * a.block + i / D;
+    if (j >= a.nk) break;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    for (int c = c0; c <= c1; ++c) {
+      if (sum * c / shares == sum * (c + 1) / shares) continue;  // an empty share
+      // a share that starts inside or at this block has it as its first run
+      const int slot = 2 * c + (sum * c / shares >= t0 ? 0 : 1);
+      const float4 v = *reinterpret_cast<const float4*>(a.seg + (2 * static_cast<size_t>(slot)) * tile + i);
+      const float4 k = *reinterpret_cast<const float4*>(a.seg + (2 * static_cast<size_t>(slot) + 1) * tile + i);
+      x.x += k.x, x.y += k.y, x.z += k.z, x.w += k.w;
+      y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+    }
+    __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(a.gk.p) + b * a.gk.sb + kh * a.gk.sh + j * a.gk.sn + i % D;
+    __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(a.gv.p) + b * a.gv.sb + kh * a.gv.sh + j * a.gv.sn + i % D;
+    *reinterpret_cast<uint2*>(dk) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+    *reinterpret_cast<uint2*>(dv) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+  }
+}
+
+template <int D, int B>
+cudaError_t backward(const SelArgs& a, int first, int count, cudaStream_t st) {
+  BlockMap mk, mv;
+  if (!block_map(&mk, a.k, a, B) || !block_map(&mv, a.v, a, B)) return cudaErrorInvalidValue;
+  auto kern = selected_backward_tc_kernel<D, B>;
+  constexpr int smem = static_cast<int>(Bwd<D, B>::kSmem);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<kShares, kThreads, smem, st>>>(mk, mv, a, first, count);
+  if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
+  join_kv_tc_kernel<D><<<dim3(a.nb, count), 256, 0, st>>>(a, first, count, kShares);
+  if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
+  return launch_join_half(a, first, count, true, st);
+}
+
+}  // namespace
+
+cudaError_t launch_selected_backward_tc(const SelArgs& a, int first, int count, cudaStream_t st) {
+  if (a.d == 128) return a.block == 128 ? backward<128, 128>(a, first, count, st) : backward<128, 64>(a, first, count, st);
+  return a.block == 128 ? backward<64, 128>(a, first, count, st) : backward<64, 64>(a, first, count, st);
+}
+
+}  // namespace spr

@@ -146,8 +146,8 @@ __global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
       for (int i = 0; i < nu; ++i)
         a.units[static_cast<size_t>(region) * a.unit_cap + u + i] =
             Unit{g, off, i * a.unit_rows, min(a.unit_rows, rows - i * a.unit_rows), len - g * a.block, qs - g * a.block, b,
-                 z % a.Hk};
-      a.blk[static_cast<size_t>(region) * a.nb + g] = make_int2(nu, slot);
+                 z % a.Hk, rows, {}};
+      a.blk[static_cast<size_t>(region) * a.nb + g] = make_int4(nu, slot, u, 0);
       for (int i = 0; i < live; ++i) {
         const int x = c[i];
         c[i] = off;

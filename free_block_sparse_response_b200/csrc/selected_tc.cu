@@ -119,60 +119,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::tmem_alloc(tc::saddr(&tmem_slot), 512);
     tc::tmem_relinquish();
   }
-  if (warp == kOutWarp) {  // this CTA's first tile (region, tile of it) and number of tiles
-    int sum = 0;
-    for (int i = lane; i < count; i += 32) sum += __ldg(a.n_units + first + i);
-    sum = __reduce_add_sync(0xffffffffu, sum);
-    const int lo = static_cast<int>(static_cast<long long>(sum) * blockIdx.x / gridDim.x);
-    const int hi = static_cast<int>(static_cast<long long>(sum) * (blockIdx.x + 1) / gridDim.x);
-    if (lane == 0) {
-      int ci = 0, before = 0, n = 0;
-      while (ci < count && before + (n = __ldg(a.n_units + first + ci)) <= lo) before += n, ++ci;
-      s_first[0] = ci, s_first[1] = lo - before, s_first[2] = hi - lo;
-    }
-  }
+  if (warp == kOutWarp) share_of_tiles(a, first, count, s_first);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tbase = tmem_slot;  // S of stream x at 128 x, O at 256 + 128 x
   volatile int* abort_v = &abort_flag;
   const size_t cap = static_cast<size_t>(a.slice) * a.top;
-  // This CTA's tiles: an equal share of the chunk's, contiguous in the order region, block, row,
-  // so that K and V change seldom.  Every role walks them in this order (a stream's warps every
-  // second one), the records of the next two in flight.
-  // f(record, region of the chunk, tile, unit = run of tiles of one block, opens it, closes it);
-  // the last three only at step 1.
-  auto each_tile = [&](int from, int step, auto f) {
-    int ci = s_first[0], idx = s_first[1] + from;
-    const int tiles = s_first[2];
-    int n = tiles > 0 ? __ldg(a.n_units + first + ci) : 0;
-    struct Rec {
-      Unit un;
-      int ci;
-    };
-    auto fetch = [&](int t) {  // record of tile t, called in order
-      Rec r{};
-      if (t < tiles) {
-        while (idx >= n) idx -= n, n = __ldg(a.n_units + first + ++ci);
-        r.un = a.units[static_cast<size_t>(first + ci) * a.unit_cap + idx];
-        r.ci = ci;
-        idx += step;
-      }
-      return r;
-    };
-    Rec now = fetch(from), next = fetch(from + step);
-    int u = 0;
-    bool opens = true;
-    for (int t = from; t < tiles; t += step) {
-      const Rec ahead = fetch(t + 2 * step);
-      const bool closes = t + 1 == tiles || next.ci != now.ci || next.un.g != now.un.g;
-      if (!f(now.un, now.ci, t, u, opens, closes)) return false;
-      opens = closes;
-      u += closes;
-      now = next, next = ahead;
-    }
-    return true;
-  };
   auto wait1 = [&](int i, int phase) { return wait_bar(bar(i), phase & 1, abort_v, a.status); };
   auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, wait1(i, phase)); };
 
@@ -183,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int x = warp >> 2, row = tid & 127;
     const uint32_t tS = tbase + 128 * x + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
     const float scale2 = a.scale * kLog2e;
-    each_tile(x, 2, [&](const Unit& un, int ci, int t, int, bool, bool) {
+    each_tile(a, first, s_first, x, 2, [&](const Unit& un, int ci, int t, int, bool, bool) {
         int nv = un.live;  // visible keys of this row in the block
         if (a.causal && row < un.rows)
           nv = min(nv, un.qs + __ldg(a.list + (first + ci) * cap + un.off + (un.r0 + row) / a.group) + 1);
@@ -243,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // row's quad as one 128-byte line (part_column() is the order inside the line).
     const int w4 = warp & 3, q = lane >> 2, i = lane & 3;
     uint8_t* const part = static_cast<uint8_t*>(static_cast<void*>(a.part));
-    each_tile(0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
+    each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
         const int x = t & 1;
         const long long out0 = static_cast<long long>((ci * cap + un.off) * a.group + un.r0);
         if (!wait(kP + x, t >> 1) || !wait(kO + x, t >> 1)) return false;  // the statistics, O
@@ -259,41 +212,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc::tmem_wait_ld();
           // rows lane0 + q and lane0 + q + 8, side by side: this stage is bound by its latencies
           const float2 st[2] = {s_stat[x * 128 + lane0 + q], s_stat[x * 128 + lane0 + q + 8]};
-          float big[2][2] = {};
+          const float inv_l[2] = {st[0].y, st[1].y};
+          float up[2];
+          store_part<D>(o, inv_l, lane0 + q, un.rows, part + 32 * i, a.plane, out0, up);
+          if (i == 0) {
 #pragma unroll
-          for (int c = 0; c < D / 2; c += 8)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              big[k & 1][k >> 1] = fmax3(big[k & 1][k >> 1], fabsf(__uint_as_float(o[c + 2 * k])),
-                                         fabsf(__uint_as_float(o[c + 2 * k + 1])));
-          float mx[2] = {fmaxf(big[0][0], big[0][1]), fmaxf(big[1][0], big[1][1])}, up[2], f[2];
-#pragma unroll
-          for (int m = 1; m < 4; m <<= 1)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], m));
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float down;
-            pow2_scale(mx[k] * st[k].y, up[k], down);
-            f[k] = st[k].y * down;
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int r = lane0 + q + 8 * k;
-            if (r < un.rows) {
-#pragma unroll
-              for (int c = 0; c < D; c += 64) {
-                uint32_t h[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  const __half2 v = __floats2half2_rn(__uint_as_float(o[c / 2 + 4 * j + 2 * k]) * f[k],
-                                                      __uint_as_float(o[c / 2 + 4 * j + 2 * k + 1]) * f[k]);
-                  h[j] = *reinterpret_cast<const uint32_t*>(&v);
-                }
-                st_global_32(part + ((c / 64) * a.plane + out0 + r) * 128 + 32 * i, h);
-              }
-              if (i == 0) a.ml[out0 + r] = make_float2(st[k].x, up[k]);
-            }
+            for (int k = 0; k < 2; ++k)
+              if (lane0 + q + 8 * k < un.rows) a.ml[out0 + lane0 + q + 8 * k] = make_float2(st[k].x, up[k]);
           }
         }
         tc::fence_before_sync();
@@ -335,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return true;
     };
-    bool ok = each_tile(0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
+    bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
       int e = 0;
       if (32 * lw + lane < un.rows)
         e = __ldg(a.list + (first + ci) * cap + un.off + (un.r0 + 32 * lw + lane) / a.group);
@@ -384,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       auto flush = [&]() { return held < 0 || (wait1(kP + x, held >> 1) && issue_o()); };
-      const bool ok = each_tile(0, 1, [&](const Unit&, int, int t, int u, bool opens, bool closes) {
+      const bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit&, int, int t, int u, bool opens, bool closes) {
         if (opens) of_unit = 0;
         if ((t & 1) == x) {
           if (held >= 0) {
@@ -422,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == kKvWarp) {
     // ---------------------------------------------------------------- K and V of each unit
     int issued = 0;
-    const bool ok = each_tile(0, 1, [&](const Unit& un, int, int, int u, bool opens, bool) {
+    const bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int, int, int u, bool opens, bool) {
       if (!opens) return true;
       if (u > 0 && !wait(kKFree, u - 1)) return false;
       if (lane == 0) {
@@ -463,9 +388,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins a query row's parts: D / 8 lanes cover a row with 16-byte loads, the groups of lanes
+// Joins a query row's parts (GRAD: adds the row's dQ parts, whose scales are in ml): D / 8 lanes cover a row with 16-byte loads, the groups of lanes
 // take slots in turn, four parts in flight each.
-template <int D>
+template <int D, bool GRAD>
 __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int first, int count) {
   constexpr int kPer = D / 8, kGroups = 32 / kPer;
   const int lane = threadIdx.x & 31, sub = lane / kPer, ch = lane % kPer;
@@ -483,12 +408,14 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
   const uint8_t* part =
       static_cast<const uint8_t*>(static_cast<const void*>(a.part)) + (ch / 8) * a.plane * 128 + (ch % 8) * 16;
   float m = -kInf;
-  for (int j = lane; j < a.top; j += 32) {
-    const int e = inv[j];
-    if (e >= 0) m = fmaxf(m, a.ml[row0 + static_cast<size_t>(e) * a.group].x);
-  }
+  if (!GRAD) {
+    for (int j = lane; j < a.top; j += 32) {
+      const int e = inv[j];
+      if (e >= 0) m = fmaxf(m, a.ml[row0 + static_cast<size_t>(e) * a.group].x);
+    }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
   const float ms = m == -kInf ? 0.f : m;
   float l = 0.f, acc[8] = {};
   for (int j0 = 0; j0 < a.top; j0 += 32) {
@@ -496,7 +423,7 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
     float f = 0.f;
     if (e >= 0) {
       const float2 st = a.ml[row0 + static_cast<size_t>(e) * a.group];
-      const float wt = exp2f(st.x - ms);
+      const float wt = GRAD ? 1.f : exp2f(st.x - ms);
       l += wt;
       f = wt * st.y;
     }
@@ -533,14 +460,15 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
   for (int o = kPer; o < 32; o <<= 1)
 #pragma unroll
     for (int c = 0; c < 8; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], o);
-  const float inv_l = l > 0.f ? 1.f / l : l != l ? l : 0.f;
+  const float inv_l = GRAD ? 1.f : l > 0.f ? 1.f / l : l != l ? l : 0.f;
   if (sub == 0) {
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o.p) + b * a.o.sb + (kh * a.group + h) * a.o.sh + t * a.o.sn;
+    const View& out = GRAD ? a.gq : a.o;
+    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out.p) + b * out.sb + (kh * a.group + h) * out.sh + t * out.sn;
 #pragma unroll
     for (int c = 0; c < 4; ++c)
       *reinterpret_cast<uint32_t*>(o + part_column(ch, c)) = pack_bf16x2(acc[2 * c] * inv_l, acc[2 * c + 1] * inv_l);
   }
-  if (lane == 0)
+  if (!GRAD && lane == 0)
     a.lse[(static_cast<size_t>(b) * a.Hq + kh * a.group + h) * a.n + t] =
         l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -kInf;
 }
@@ -558,15 +486,24 @@ cudaError_t forward(const SelArgs& a, int first, int count, cudaStream_t st) {
   if (128 * (2 * kRegSoftmax + kRegOut + 2 * kRegRest) > fa.numRegs * kThreads) return cudaErrorInvalidConfiguration;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const long long grid = std::min<long long>(148, static_cast<long long>(count) * a.unit_cap);
-  kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(mk, mv, a, first, count);
+  kern<<<kShares, kThreads, smem, st>>>(mk, mv, a, first, count);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
-  const long long rows = static_cast<long long>(count) * a.slice * a.group;
-  join_half_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, st>>>(a, first, count);
-  return counted(cudaGetLastError(), 1);
+  return launch_join_half(a, first, count, false, st);
 }
 
 }  // namespace
+
+cudaError_t launch_join_half(const SelArgs& a, int first, int count, bool grad, cudaStream_t st) {
+  const long long rows = static_cast<long long>(count) * a.slice * a.group;
+  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+  if (a.d == 128)
+    grad ? join_half_kernel<128, true><<<grid, 256, 0, st>>>(a, first, count)
+         : join_half_kernel<128, false><<<grid, 256, 0, st>>>(a, first, count);
+  else
+    grad ? join_half_kernel<64, true><<<grid, 256, 0, st>>>(a, first, count)
+         : join_half_kernel<64, false><<<grid, 256, 0, st>>>(a, first, count);
+  return counted(cudaGetLastError(), 1);
+}
 
 bool block_map(BlockMap* m, const View& v, const SelArgs& a, int rows) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {

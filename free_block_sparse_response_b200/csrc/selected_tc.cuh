@@ -2,6 +2,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -144,6 +145,108 @@ __device__ __forceinline__ void pow2_scale(float big, float& up, float& down) {
   down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
 }
 
+// The tensor-core kernels run one CTA per SM; CTA c takes tiles [sum c / shares, sum (c + 1) /
+// shares) of a chunk's `sum` tiles, in the order region, block, row.
+constexpr int kShares = kTcShares;
+
+// This CTA's share, by one warp: share[0], share[1] its first tile (region of the chunk, tile
+// of the region), share[2] its number of tiles.
+__device__ __forceinline__ void share_of_tiles(const SelArgs& a, int first, int count, int* share) {
+  const int lane = threadIdx.x & 31;
+  int sum = 0;
+  for (int i = lane; i < count; i += 32) sum += __ldg(a.n_units + first + i);
+  sum = __reduce_add_sync(0xffffffffu, sum);
+  const int lo = static_cast<int>(static_cast<long long>(sum) * blockIdx.x / gridDim.x);
+  const int hi = static_cast<int>(static_cast<long long>(sum) * (blockIdx.x + 1) / gridDim.x);
+  if (lane == 0) {
+    int ci = 0, before = 0, n = 0;
+    while (ci < count && before + (n = __ldg(a.n_units + first + ci)) <= lo) before += n, ++ci;
+    share[0] = ci, share[1] = lo - before, share[2] = hi - lo;
+  }
+}
+
+// The tiles from, from + step, .. of a CTA's share, in order (a stream's warps take every second
+// one); contiguous shares change K and V seldom.  The records of the next two are in flight.
+// f(record, region of the chunk, tile, unit = run of tiles of one block, opens it, closes it);
+// the last three hold at step 1.
+template <typename F>
+__device__ __forceinline__ bool each_tile(const SelArgs& a, int first, const int* share, int from, int step, F f) {
+  int ci = share[0], idx = share[1] + from;
+  const int tiles = share[2];
+  int n = tiles > 0 ? __ldg(a.n_units + first + ci) : 0;
+  struct Rec {
+    Unit un;
+    int ci;
+  };
+  auto fetch = [&](int t) {  // record of tile t, called in order
+    Rec r{};
+    if (t < tiles) {
+      while (idx >= n) idx -= n, n = __ldg(a.n_units + first + ++ci);
+      r.un = a.units[static_cast<size_t>(first + ci) * a.unit_cap + idx];
+      r.ci = ci;
+      idx += step;
+    }
+    return r;
+  };
+  Rec now = fetch(from), next = fetch(from + step);
+  int u = 0;
+  bool opens = true;
+  for (int t = from; t < tiles; t += step) {
+    const Rec ahead = fetch(t + 2 * step);
+    const bool closes = t + 1 == tiles || next.ci != now.ci || next.un.g != now.un.g;
+    if (!f(now.un, now.ci, t, u, opens, closes)) return false;
+    opens = closes;
+    u += closes;
+    now = next, next = ahead;
+  }
+  return true;
+}
+
+// Rows r and r + 8 of a tile, held by the quad's lanes as tmem_ld_16x64 leaves them (D / 2
+// registers), times f[k], to the partial rows out0 + r of a chunk: fp16 with the row's largest
+// magnitude scaled to [1/2, 1); up[k] is the power of two that undoes it.  The two rows go side
+// by side, since this is bound by its latencies.  `part` is the lane's 32 bytes of row 0.
+template <int D>
+__device__ __forceinline__ void store_part(const uint32_t (&o)[D / 2], const float (&f)[2], int r, int rows, uint8_t* part,
+                                           long long plane, long long out0, float (&up)[2]) {
+  float big[2][2] = {}, mx[2], g[2];
+#pragma unroll
+  for (int c = 0; c < D / 2; c += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      big[k & 1][k >> 1] = fmax3(big[k & 1][k >> 1], fabsf(__uint_as_float(o[c + 2 * k])), fabsf(__uint_as_float(o[c + 2 * k + 1])));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) mx[k] = fmaxf(big[k][0], big[k][1]);
+#pragma unroll
+  for (int m = 1; m < 4; m <<= 1)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], m));
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float down;
+    pow2_scale(mx[k] * f[k], up[k], down);
+    g[k] = f[k] * down;
+  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (r + 8 * k >= rows) continue;
+#pragma unroll
+    for (int c = 0; c < D; c += 64) {
+      uint32_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const __half2 v = __floats2half2_rn(__uint_as_float(o[c / 2 + 4 * j + 2 * k]) * g[k],
+                                            __uint_as_float(o[c / 2 + 4 * j + 2 * k + 1]) * g[k]);
+        h[j] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      st_global_32(part + ((c / 64) * plane + out0 + r + 8 * k) * 128, h);
+    }
+  }
+}
+
 cudaError_t launch_selected_forward_tc(const SelArgs& a, int first, int count, cudaStream_t st);
+cudaError_t launch_selected_backward_tc(const SelArgs& a, int first, int count, cudaStream_t st);
+// Joins the parts of a chunk's query rows into a.o and a.lse, or (grad) a.gq.
+cudaError_t launch_join_half(const SelArgs& a, int first, int count, bool grad, cudaStream_t st);
 
 }  // namespace spr
