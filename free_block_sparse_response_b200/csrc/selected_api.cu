@@ -109,7 +109,15 @@ Plan make_plan(SelArgs& a, bool backward) {
   const long long entries = static_cast<long long>(a.slice) * a.top, rows = entries * a.group;
   L.chunk = static_cast<int>(std::min<long long>(L.regions, std::max<long long>(1, kPartialBytes / (row * rows))));
   a.plane = rows * L.chunk;
-  a.unit_rows = !a.f32 ? 128 : backward ? 2048 : 512;  // the tensor-core kernels work tile by tile
+  // The tensor-core kernels work tile by tile.  On the fp32 pipes a unit is one CTA: long units
+  // load K and V seldom (and, backward, leave few sums), short ones fill the SMs when there are
+  // few rows: the longest that still gives four units per SM.
+  a.unit_rows = 128;
+  if (a.f32) {
+    const long long all = rows * L.regions;
+    a.unit_rows = backward ? 2048 : 512;
+    while (a.unit_rows > 64 && all / a.unit_rows < 4 * 148) a.unit_rows /= 2;
+  }
   a.unit_cap = a.nb + static_cast<int>(rows / a.unit_rows);
   // sums of split blocks: per region in fp32, two per CTA on the tensor cores
   a.seg_cap = backward && a.f32 ? static_cast<int>(2 * (rows / a.unit_rows)) + 2 : 0;

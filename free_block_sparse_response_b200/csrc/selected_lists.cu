@@ -118,46 +118,69 @@ __device__ __forceinline__ int block_scan(int v, int& sum, int* s_warp) {
   return before + x - v;
 }
 
+// A warp a block adds the block's counts, the CTA's threads form the prefix sums over blocks,
+// then a warp a block writes its sub-slices' first entries and its units.
 __global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
+  extern __shared__ int4 s_blk[];  // [nb] {entries, then first entry | units | first slot | first unit}
   __shared__ int s_warp[16];
-  const int region = blockIdx.x;
+  const int region = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int s = region % a.slices, z = region / a.slices, b = z / a.Hk;
   const int len = kv_len_of(a, b), qs = q_start_of(a, b);
   // sub-slices of this region that hold tokens
   const int live = min(a.subs, ceil_div(a.n - s * a.slice, kSub));
+  int* offs = a.offs + static_cast<size_t>(region) * a.nb * a.subs;
+  for (int g = warp; g < a.nb; g += 16) {
+    int cnt = 0;
+    for (int i = lane; i < live; i += 32) cnt += offs[static_cast<size_t>(g) * a.subs + i];
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+    if (lane == 0) s_blk[g].x = cnt;
+  }
+  __syncthreads();
   int entry0 = 0, unit0 = 0, slot0 = 0;
   for (int g0 = 0; g0 < a.nb; g0 += 512) {
     const int g = g0 + threadIdx.x;
-    int* c = a.offs + (static_cast<size_t>(region) * a.nb + g) * a.subs;
-    int cnt = 0;
-    if (g < a.nb)
-      for (int i = 0; i < live; ++i) cnt += c[i];
+    const int cnt = g < a.nb ? s_blk[g].x : 0;
+    const int nu = ceil_div(cnt * a.group, a.unit_rows);
     int sum;
-    int off = entry0 + block_scan(cnt, sum, s_warp);
+    const int off = entry0 + block_scan(cnt, sum, s_warp);
     entry0 += sum;
-    const int rows = cnt * a.group;
-    const int nu = ceil_div(rows, a.unit_rows);
     const int u = unit0 + block_scan(nu, sum, s_warp);
     unit0 += sum;
-    const int slots = nu > 1 ? nu : 0;
-    const int slot = slot0 + block_scan(slots, sum, s_warp);
+    const int slot = slot0 + block_scan(nu > 1 ? nu : 0, sum, s_warp);
     slot0 += sum;
     if (g < a.nb) {
-      for (int i = 0; i < nu; ++i)
-        a.units[static_cast<size_t>(region) * a.unit_cap + u + i] =
-            Unit{g, off, i * a.unit_rows, min(a.unit_rows, rows - i * a.unit_rows), len - g * a.block, qs - g * a.block, b,
-                 z % a.Hk, rows, {}};
+      s_blk[g] = make_int4(off, cnt, slot, u);
       a.blk[static_cast<size_t>(region) * a.nb + g] = make_int4(nu, slot, u, 0);
-      for (int i = 0; i < live; ++i) {
-        const int x = c[i];
-        c[i] = off;
-        off += x;
-      }
     }
   }
+  __syncthreads();
+  for (int g = warp; g < a.nb; g += 16) {
+    const int4 k = s_blk[g];
+    int off = k.x;
+    for (int i0 = 0; i0 < live; i0 += 32) {
+      const int i = i0 + lane;
+      int* at = offs + static_cast<size_t>(g) * a.subs + i;
+      const int c = i < live ? *at : 0;
+      int x = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (i < live) *at = off + x - c;
+      off += __shfl_sync(0xffffffffu, x, 31);
+    }
+    const int rows = k.y * a.group, nu = ceil_div(rows, a.unit_rows);
+    for (int i = lane; i < nu; i += 32)
+      a.units[static_cast<size_t>(region) * a.unit_cap + k.w + i] =
+          Unit{g, k.x, i * a.unit_rows, min(a.unit_rows, rows - i * a.unit_rows), len - g * a.block, qs - g * a.block, b,
+               z % a.Hk, rows, {}};
+  }
   if (threadIdx.x == 0) a.n_units[region] = unit0;
-  for (int u = unit0 + threadIdx.x; u < a.unit_cap; u += 512)
-    a.units[static_cast<size_t>(region) * a.unit_cap + u] = Unit{};
+  // the kernels on the fp32 pipes launch a CTA for every unit there may be
+  if (a.f32)
+    for (int u = unit0 + threadIdx.x; u < a.unit_cap; u += 512)
+      a.units[static_cast<size_t>(region) * a.unit_cap + u] = Unit{};
 }
 
 __global__ void __launch_bounds__(256) scatter_kernel(const SelArgs a) {
@@ -200,7 +223,7 @@ cudaError_t launch_lists(const SelArgs& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   count_kernel<<<dim3(subs, heads), 256, mask, st>>>(a);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
-  scan_kernel<<<heads * a.slices, 512, 0, st>>>(a);
+  scan_kernel<<<heads * a.slices, 512, sizeof(int4) * a.nb, st>>>(a);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
   scatter_kernel<<<dim3(subs, heads), 256, both, st>>>(a);
   return counted(cudaGetLastError(), 1);

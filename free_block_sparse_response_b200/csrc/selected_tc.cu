@@ -388,63 +388,58 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins a query row's parts (GRAD: adds the row's dQ parts, whose scales are in ml): D / 8 lanes cover a row with 16-byte loads, the groups of lanes
-// take slots in turn, four parts in flight each.
+// Joins a query row's parts (GRAD: adds the row's dQ parts, whose scales are in ml).  D / 8 lanes
+// take a row, so that a warp has two or four rows under way; each lane looks up the slots of its
+// number (entry, weight), then the lanes read eight parts at a time, 16 bytes each.  Bound by
+// the parts' bytes; what keeps it from them is the chain entry -> weight -> part of each row.
 template <int D, bool GRAD>
 __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int first, int count) {
-  constexpr int kPer = D / 8, kGroups = 32 / kPer;
-  const int lane = threadIdx.x & 31, sub = lane / kPer, ch = lane % kPer;
-  const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  constexpr int kPer = D / 8, kRowsW = 32 / kPer;
+  const int lane = threadIdx.x & 31, ch = lane % kPer;
+  const long long w = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kRowsW + lane / kPer;
   const int per = a.slice * a.group;
-  const int ci = static_cast<int>(w / per);
-  if (ci >= count) return;
+  const int ci = static_cast<int>(min(w / per, static_cast<long long>(count - 1)));
   const int region = first + ci, z = region / a.slices, s = region % a.slices;
   const int lr = static_cast<int>(w % per), t = s * a.slice + lr / a.group, h = lr % a.group;
-  if (t >= a.n) return;
+  const bool live = w < static_cast<long long>(count) * per && t < a.n;  // the warp stays together
   const int b = z / a.Hk, kh = z % a.Hk;
-  const int* inv = a.inv + (static_cast<size_t>(z) * a.n + t) * a.top;
+  const int* inv = a.inv + (static_cast<size_t>(z) * a.n + (live ? t : 0)) * a.top;
   const size_t row0 = ci * static_cast<size_t>(a.slice) * a.top * a.group + h;
   // the lane's 16 bytes of a part: chunk ch % 8 of a line in plane ch / 8
   const uint8_t* part =
       static_cast<const uint8_t*>(static_cast<const void*>(a.part)) + (ch / 8) * a.plane * 128 + (ch % 8) * 16;
-  float m = -kInf;
-  if (!GRAD) {
-    for (int j = lane; j < a.top; j += 32) {
-      const int e = inv[j];
-      if (e >= 0) m = fmaxf(m, a.ml[row0 + static_cast<size_t>(e) * a.group].x);
-    }
+  float m = -kInf, l = 0.f, acc[8] = {};
+  for (int j0 = 0; j0 < a.top; j0 += kPer) {
+    const int e = live && j0 + ch < a.top ? __ldg(inv + j0 + ch) : -1;
+    const float2 st = e >= 0 ? __ldcs(a.ml + row0 + static_cast<size_t>(e) * a.group) : make_float2(-kInf, 0.f);
+    float f = st.y;
+    if (!GRAD) {
+      float mx = st.x;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  }
-  const float ms = m == -kInf ? 0.f : m;
-  float l = 0.f, acc[8] = {};
-  for (int j0 = 0; j0 < a.top; j0 += 32) {
-    const int e = j0 + lane < a.top ? inv[j0 + lane] : -1;
-    float f = 0.f;
-    if (e >= 0) {
-      const float2 st = a.ml[row0 + static_cast<size_t>(e) * a.group];
-      const float wt = GRAD ? 1.f : exp2f(st.x - ms);
-      l += wt;
-      f = wt * st.y;
-    }
-    const int lim = min(32, a.top - j0);
-    for (int j = 0; j < lim; j += 4 * kGroups) {
-      uint4 v[4];
-      float fj[4];
+      for (int o = kPer / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mx = fmaxf(m, mx);
+      const float ms = mx == -kInf ? 0.f : mx, old = exp2f(m - ms), wt = exp2f(st.x - ms);
+      m = mx;
+      l = fmaf(l, old, wt);
+      f *= wt;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int src = j + i * kGroups + sub;
-        const int ej = __shfl_sync(0xffffffffu, e, src & 31);
-        fj[i] = __shfl_sync(0xffffffffu, f, src & 31);
-        v[i] = make_uint4(0, 0, 0, 0);
-        const size_t row = row0 + static_cast<size_t>(ej) * a.group;
-        if (src < lim && ej >= 0)
-          v[i] = __ldcs(reinterpret_cast<const uint4*>(part + row * 128));
-        else
-          fj[i] = 0.f;
+      for (int c = 0; c < 8; ++c) acc[c] *= old;
+    }
+    if (e < 0) f = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; j += 8) {
+      if (j0 + j >= a.top) break;
+      uint4 v[8];
+      float fj[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int ej = __shfl_sync(0xffffffffu, e, j + i, kPer);
+        fj[i] = __shfl_sync(0xffffffffu, f, j + i, kPer);
+        v[i] = ej >= 0 ? __ldcs(reinterpret_cast<const uint4*>(part + (row0 + static_cast<size_t>(ej) * a.group) * 128))
+                       : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -455,20 +450,16 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
       }
     }
   }
-  l = warp_sum(l);
 #pragma unroll
-  for (int o = kPer; o < 32; o <<= 1)
-#pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], o);
+  for (int o = kPer / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  if (!live) return;
   const float inv_l = GRAD ? 1.f : l > 0.f ? 1.f / l : l != l ? l : 0.f;
-  if (sub == 0) {
-    const View& out = GRAD ? a.gq : a.o;
-    __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out.p) + b * out.sb + (kh * a.group + h) * out.sh + t * out.sn;
+  const View& out = GRAD ? a.gq : a.o;
+  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out.p) + b * out.sb + (kh * a.group + h) * out.sh + t * out.sn;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      *reinterpret_cast<uint32_t*>(o + part_column(ch, c)) = pack_bf16x2(acc[2 * c] * inv_l, acc[2 * c + 1] * inv_l);
-  }
-  if (!GRAD && lane == 0)
+  for (int c = 0; c < 4; ++c)
+    *reinterpret_cast<uint32_t*>(o + part_column(ch, c)) = pack_bf16x2(acc[2 * c] * inv_l, acc[2 * c + 1] * inv_l);
+  if (!GRAD && ch == 0)
     a.lse[(static_cast<size_t>(b) * a.Hq + kh * a.group + h) * a.n + t] =
         l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -kInf;
 }
@@ -495,7 +486,8 @@ cudaError_t forward(const SelArgs& a, int first, int count, cudaStream_t st) {
 
 cudaError_t launch_join_half(const SelArgs& a, int first, int count, bool grad, cudaStream_t st) {
   const long long rows = static_cast<long long>(count) * a.slice * a.group;
-  const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+  const int per_cta = 8 * (32 / (a.d / 8));
+  const unsigned grid = static_cast<unsigned>((rows + per_cta - 1) / per_cta);
   if (a.d == 128)
     grad ? join_half_kernel<128, true><<<grid, 256, 0, st>>>(a, first, count)
          : join_half_kernel<128, false><<<grid, 256, 0, st>>>(a, first, count);

@@ -26,6 +26,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import math
 from typing import NamedTuple, Optional, Sequence
 
@@ -110,8 +111,12 @@ def _rows_like(t: torch.Tensor) -> torch.Tensor:
 
 
 def _run(device, name: str, *args) -> None:
-    with torch.cuda.device(device):
-        _s._call(name, *args, ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream))
+    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    if device.index == torch.cuda.current_device():
+        _s._call(name, *args, stream)
+    else:
+        with torch.cuda.device(device):
+            _s._call(name, *args, stream)
 
 
 # ------------------------------------------------------------------------------ rotary
@@ -267,8 +272,16 @@ def selected_workspace(q: torch.Tensor, k: torch.Tensor, cfg: SelectConfig, back
     return ws
 
 
-def _need_ws(ws: torch.Tensor, p: _CSelected, device, backward: bool) -> None:
-    size = int(_s.lib().sparsepr_selected_workspace_size(ctypes.byref(p), 1 if backward else 0))
+@functools.lru_cache(maxsize=256)
+def _ws_size(dtype, bt, hq, hk, nq, nk, d, cfg: SelectConfig, backward: bool) -> int:
+    """Workspace bytes of a problem: a function of its sizes alone."""
+    p = _CSelected(dtype, bt, hq, hk, nq, nk, d, cfg.block, cfg.top, int(bool(cfg.causal)), cfg.n_first, cfg.n_local,
+                   cfg.scale, None, None)
+    return int(_s.lib().sparsepr_selected_workspace_size(ctypes.byref(p), 1 if backward else 0))
+
+
+def _need_ws(ws: torch.Tensor, p: _CSelected, cfg: SelectConfig, device, backward: bool) -> None:
+    size = _ws_size(p.dtype, p.Bt, p.Hq, p.Hkv, p.Nq, p.Nk, p.d, cfg, backward)
     if size and (ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < size or
                  ws.data_ptr() % 256):
         raise ValueError("the workspace is too small for these tensors, misaligned or on another device")
@@ -303,7 +316,7 @@ def select_blocks(q: torch.Tensor, means: torch.Tensor, keys: int, cfg: SelectCo
     _need_flat("means", means, (bt, hk, -(-keys // cfg.block) if cfg.block > 0 else 0, d), torch.float32, q.device)
     _lengths(bt, q.device, kv_len, q_start)
     p = _problem(q, bt, hq, hk, n, keys, d, cfg, kv_len, q_start)
-    _need_ws(ws, p, q.device, False)
+    _need_ws(ws, p, cfg, q.device, False)
     sel = torch.empty(bt, hk, n, cfg.top, dtype=torch.int32, device=q.device) if out is None else out
     _need_flat("out", sel, (bt, hk, n, cfg.top), torch.int32, q.device)
     _run(q.device, "sparsepr_select_blocks", ctypes.byref(p), _view(q), _s._p(means), _s._p(sel), _s._p(ws))
@@ -318,7 +331,7 @@ def _attention_problem(q, k, v, sel, cfg, ws, kv_len, q_start, backward) -> _CSe
     _need_flat("sel", sel, (bt, k.shape[1], n, cfg.top), torch.int32, q.device)
     _lengths(bt, q.device, kv_len, q_start)
     p = _problem(q, bt, hq, k.shape[1], n, k.shape[2], d, cfg, kv_len, q_start)
-    _need_ws(ws, p, q.device, backward)
+    _need_ws(ws, p, cfg, q.device, backward)
     return p
 
 
