@@ -27,9 +27,8 @@ struct Vec;  // 16 bytes of T as floats
 template <>
 struct Vec<float> {
   static constexpr int kN = 4;
-  __device__ static void load(const float* p, float* x) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  __device__ static void unpack(const uint4& v, float* x) {
+    x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y), x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
   }
   __device__ static void store(float* p, const float* x) {
     *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
@@ -38,8 +37,7 @@ struct Vec<float> {
 template <>
 struct Vec<__nv_bfloat16> {
   static constexpr int kN = 8;
-  __device__ static void load(const __nv_bfloat16* p, float* x) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p);
+  __device__ static void unpack(const uint4& v, float* x) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -63,9 +61,8 @@ struct Vec<__nv_bfloat16> {
 __device__ __forceinline__ void turn(const RotaryArgs& a, const int* pos, int pair, float& c, float& s) {
   int axis = 0, first = 0;
   while (axis + 1 < a.axes && pair >= first + a.pairs[axis]) first += a.pairs[axis++];
-  const double t = static_cast<double>(pos[axis]) * a.freqs[pair];
-  const double r = fma(-rint(t * 0.15915494309189535), 6.283185307179586, t);
-  sincosf(static_cast<float>(r), &s, &c);
+  const double turns = static_cast<double>(pos[axis]) * a.freqs[pair] * 0.15915494309189535;
+  sincospif(static_cast<float>(2.0 * (turns - rint(turns))), &s, &c);
   c *= a.factor;
   s *= a.inverse ? -a.factor : a.factor;
 }
@@ -108,35 +105,54 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a) {
     const int w = h >= a.h[0];
     return static_cast<T*>(v[w].p) + b * v[w].sb + (h - (w ? a.h[0] : 0)) * v[w].sh + t * v[w].sn;
   };
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const T* x = at(a.x, h);
-    T* y = at(a.y, h);
-    if constexpr (VEC) {
-      float u[V], w[V];
-      Vec<T>::load(x + lo, u);
-      if (!rotated) {
-        Vec<T>::store(y + lo, u);
-      } else if (HALF) {
-        Vec<T>::load(x + hi, w);
+  if constexpr (VEC) {
+    // kBatch heads' pieces are read before the first is written (in place, a thread writes only
+    // what it has read itself)
+    constexpr int kBatch = 4;
+    for (int hb = h0; hb < h1; hb += kBatch) {
+      uint4 u4[kBatch], w4[kBatch];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const float p = u[i] * c[i % kPairs] - w[i] * s[i % kPairs];
-          w[i] = w[i] * c[i % kPairs] + u[i] * s[i % kPairs];
-          u[i] = p;
-        }
-        Vec<T>::store(y + lo, u);
-        Vec<T>::store(y + hi, w);
-      } else {
-#pragma unroll
-        for (int i = 0; i < V / 2; ++i) {
-          const float p = u[2 * i] * c[i] - u[2 * i + 1] * s[i];
-          u[2 * i + 1] = u[2 * i + 1] * c[i] + u[2 * i] * s[i];
-          u[2 * i] = p;
-        }
-        Vec<T>::store(y + lo, u);
+      for (int k = 0; k < kBatch; ++k) {
+        if (hb + k >= h1) break;
+        const T* x = at(a.x, hb + k);
+        u4[k] = __ldcs(reinterpret_cast<const uint4*>(x + lo));
+        if (HALF && rotated) w4[k] = __ldcs(reinterpret_cast<const uint4*>(x + hi));
       }
-    } else {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (hb + k >= h1) break;
+        T* y = at(a.y, hb + k);
+        if (!rotated) {
+          *reinterpret_cast<uint4*>(y + lo) = u4[k];
+          continue;
+        }
+        float u[V], w[V];
+        Vec<T>::unpack(u4[k], u);
+        if (HALF) {
+          Vec<T>::unpack(w4[k], w);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float p = u[i] * c[i % kPairs] - w[i] * s[i % kPairs];
+            w[i] = w[i] * c[i % kPairs] + u[i] * s[i % kPairs];
+            u[i] = p;
+          }
+          Vec<T>::store(y + lo, u);
+          Vec<T>::store(y + hi, w);
+        } else {
+#pragma unroll
+          for (int i = 0; i < V / 2; ++i) {
+            const float p = u[2 * i] * c[i] - u[2 * i + 1] * s[i];
+            u[2 * i + 1] = u[2 * i + 1] * c[i] + u[2 * i] * s[i];
+            u[2 * i] = p;
+          }
+          Vec<T>::store(y + lo, u);
+        }
+      }
+    }
+  } else {
+    for (int h = h0; h < h1; ++h) {
+      const T* x = at(a.x, h);
+      T* y = at(a.y, h);
       const float p = to_f32<T>(x[lo]);
       if (!rotated) {
         y[lo] = x[lo];

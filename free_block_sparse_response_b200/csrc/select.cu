@@ -165,26 +165,27 @@ __global__ void __launch_bounds__(256) select_row_kernel(const SelArgs a, int* _
 }
 
 // Tiles of ROWS tokens of one (batch, key head) against 64 blocks at a time.
-constexpr int kChunk = 64;
+constexpr int kChunk = 64, kTileWarps = 16, kTileThreads = 32 * kTileWarps;
 
 template <int D, int ROWS>
 size_t tile_smem(int nb) {
   const int ld = (nb + kChunk - 1) / kChunk * kChunk + 4;
   return 2 * 2 * static_cast<size_t>(D) * (ROWS + kChunk) + sizeof(float) * ld * ROWS + sizeof(float) * ROWS +
-         8 * 32 * sizeof(int) + 16;
+         kTileWarps * 32 * sizeof(int) + 16;
 }
 
-template <typename T, int D, int ROWS>
-__global__ void __launch_bounds__(256) select_tile_kernel(const SelArgs a, int* __restrict__ sel, int* __restrict__ list) {
+// VPL: a lane's scores of a row in registers (32 VPL blocks and more), 0: read from shared memory.
+template <typename T, int D, int ROWS, int VPL>
+__global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs a, int* __restrict__ sel, int* __restrict__ list) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kTileQ = ROWS * D * 2, kTileM = kChunk * D * 2;
-  constexpr int RG = ROWS / 16, CG = 8 / RG, NT = kChunk / CG / 8;  // warps over rows, columns; column tiles a warp
+  constexpr int RG = ROWS / 16, CG = kTileWarps / RG < 8 ? kTileWarps / RG : 8, NT = kChunk / CG / 8;  // warps over rows, columns; column tiles a warp
   const int ld = ceil_div(a.nb, kChunk) * kChunk + 4;
   const uint32_t sqh = smem_u32(smem), sql = sqh + kTileQ, smh = sql + kTileQ, sml = smh + kTileM;
   float* score = reinterpret_cast<float*>(smem + 2 * kTileQ + 2 * kTileM);  // [ROWS][ld]
   float* qn = score + static_cast<size_t>(ROWS) * ld;
   int* open = reinterpret_cast<int*>(qn + ROWS);                            // [warp][32]
-  int* mmax = open + 8 * 32;                                                // bits of the largest mean norm squared
+  int* mmax = open + kTileWarps * 32;                                                // bits of the largest mean norm squared
   const int z = blockIdx.y, b = z / a.Hk, kh = z % a.Hk, t0 = blockIdx.x * ROWS;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the tile's last token sees the most
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(256) select_tile_kernel(const SelArgs a, int* 
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(lo_tile + at), "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3]) : "memory");
   };
   // the group's query sums and the norms of their sums of magnitudes: D / 8 threads a row
-  for (int i = tid; i < ROWS * (D / 8); i += 256) {
+  for (int i = tid; i < ROWS * (D / 8); i += kTileThreads) {
     const int r = i / (D / 8), c = i % (D / 8) * 8;
     float x[8] = {}, y = 0.f, mag[8] = {};
     if (t0 + r < a.n) {
@@ -226,7 +227,7 @@ __global__ void __launch_bounds__(256) select_tile_kernel(const SelArgs a, int* 
   const int rg = warp % RG, cg = warp / RG;
   for (int g0 = 0; g0 < most; g0 += kChunk) {
     __syncthreads();  // the chunk before is read
-    for (int i = tid; i < kChunk * (D / 8); i += 256) {
+    for (int i = tid; i < kChunk * (D / 8); i += kTileThreads) {
       const int r = i / (D / 8), c = i % (D / 8) * 8, g = g0 + r;
       float x[8] = {}, y = 0.f;
       if (g < most) {
@@ -242,6 +243,7 @@ __global__ void __launch_bounds__(256) select_tile_kernel(const SelArgs a, int* 
       put(smh, sml, r, c, x);
     }
     __syncthreads();
+    if (cg >= CG) continue;  // more warps than 8-column strips
     float hh[NT][4], rest[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -280,7 +282,7 @@ __global__ void __launch_bounds__(256) select_tile_kernel(const SelArgs a, int* 
   __syncthreads();
   const float mnorm = sqrtf(__int_as_float(*mmax));
   int* my_open = open + warp * 32;
-  for (int r = warp; r < ROWS && t0 + r < a.n; r += 8) {
+  for (int r = warp; r < ROWS && t0 + r < a.n; r += kTileWarps) {
     const long long w = static_cast<long long>(z) * a.n + t0 + r;
     int* out = sel + w * a.top;
     const Scope sc = scope_of(a, b, t0 + r);
@@ -300,25 +302,46 @@ __global__ void __launch_bounds__(256) select_tile_kernel(const SelArgs a, int* 
     unsigned chosen = 0;
     bool slow = split && !(e2 < 0x1p100f);  // not finite
     if (split && !slow) {
-      uint32_t v = 0;
+      // order keys of the blocks to choose from (0: not one), in registers where they fit
+      auto key_of = [&](int g) {
+        return g < sc.cand && !is_forced(a, sc, g) ? float_order_key(sr[g]) : 0u;
+      };
+      uint32_t key[VPL > 0 ? VPL : 1];
+#pragma unroll
+      for (int i = 0; i < VPL; ++i) key[i] = key_of(32 * i + lane);
+      auto each_key = [&](auto f) {
+        if (VPL > 0) {
+#pragma unroll
+          for (int i = 0; i < VPL; ++i) f(key[i]);
+        } else {
+          for (int g = lane; g < sc.cand; g += 32) f(key_of(g));
+        }
+      };
+      // the bits that all of them share need no search
+      uint32_t kmin = 0xffffffffu, kmax = 0;
+      each_key([&](uint32_t k) {
+        kmax = max(kmax, k);
+        kmin = min(kmin, k > 0 ? k : 0xffffffffu);
+      });
+      kmin = __reduce_min_sync(0xffffffffu, kmin), kmax = __reduce_max_sync(0xffffffffu, kmax);
+      const int top_bit = kmin == kmax ? -1 : 31 - __clz(kmin ^ kmax);
+      uint32_t v = top_bit < 0 ? kmin : kmin & ~((2u << top_bit) - 1u);
       int have = pool;
-      for (int bit = 31; bit >= 0 && have != want; --bit) {
+      for (int bit = top_bit; bit >= 0 && have != want; --bit) {
         const uint32_t tryv = v | (1u << bit);
         int c = 0;
-        for (int g = lane; g < sc.cand; g += 32) c += float_order_key(sr[g]) >= tryv && !is_forced(a, sc, g);
+        each_key([&](uint32_t k) { c += k >= tryv; });
         c = __reduce_add_sync(0xffffffffu, c);
         if (c >= want) v = tryv, have = c;
       }
       // the want-th largest, and the one after it
       uint32_t ka = 0xffffffffu, kb = 0;
-      for (int g = lane; g < sc.cand; g += 32) {
-        const uint32_t key = float_order_key(sr[g]);
-        if (is_forced(a, sc, g)) continue;
-        if (key >= v)
-          ka = min(ka, key);
+      each_key([&](uint32_t k) {
+        if (k >= v && k > 0)
+          ka = min(ka, k);
         else
-          kb = max(kb, key);
-      }
+          kb = max(kb, k);
+      });
       const float fa = float_from_order_key(__reduce_min_sync(0xffffffffu, ka));
       const float fb = have > want ? fa : float_from_order_key(__reduce_max_sync(0xffffffffu, kb));
       if (fa - fb > e2) {
@@ -397,28 +420,33 @@ cudaError_t row_select(const SelArgs& a, int* sel, const int* list, cudaStream_t
   return counted(cudaGetLastError(), 1);
 }
 
-template <typename T, int D, int ROWS>
+template <typename T, int D, int ROWS, int VPL>
 cudaError_t tile_select(const SelArgs& a, int* sel, cudaStream_t st) {
   cudaError_t e = cudaMemsetAsync(a.slow, 0, sizeof(int), st);
   if (e != cudaSuccess) return e;
   const size_t smem = tile_smem<D, ROWS>(a.nb);
-  e = cudaFuncSetAttribute(select_tile_kernel<T, D, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(select_tile_kernel<T, D, ROWS, VPL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  select_tile_kernel<T, D, ROWS><<<dim3(ceil_div(a.n, ROWS), a.Bt * a.Hk), 256, smem, st>>>(a, sel, a.slow + 1);
+  select_tile_kernel<T, D, ROWS, VPL><<<dim3(ceil_div(a.n, ROWS), a.Bt * a.Hk), kTileThreads, smem, st>>>(a, sel, a.slow + 1);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
   return row_select<T, D>(a, sel, a.slow + 1, st);
 }
 
 // Up to eight tokens a head leave a tile of 16 half empty: one CTA a row.  Otherwise the tallest
-// tile whose scores fit in shared memory (a mean is read once per tile).
+// tile whose scores fit in shared memory (a mean is read once per tile); a row's keys stay in
+// registers up to 640 blocks (20 a lane).
 template <typename T, int D>
 cudaError_t select_blocks(const SelArgs& a, int* sel, cudaStream_t st) {
   if (a.n <= 8) return row_select<T, D>(a, sel, nullptr, st);
   constexpr size_t kMost = 227 * 1024;
-  if (tile_smem<D, 64>(a.nb) <= kMost) return tile_select<T, D, 64>(a, sel, st);
-  if (tile_smem<D, 32>(a.nb) <= kMost) return tile_select<T, D, 32>(a, sel, st);
-  return tile_select<T, D, 16>(a, sel, st);
+  if (tile_smem<D, 64>(a.nb) <= kMost) {
+    if (a.nb <= 128) return tile_select<T, D, 64, 4>(a, sel, st);
+    return a.nb <= 256 ? tile_select<T, D, 64, 8>(a, sel, st) : tile_select<T, D, 64, 20>(a, sel, st);
+  }
+  if (tile_smem<D, 32>(a.nb) <= kMost)
+    return a.nb <= 640 ? tile_select<T, D, 32, 20>(a, sel, st) : tile_select<T, D, 32, 0>(a, sel, st);
+  return tile_select<T, D, 16, 0>(a, sel, st);
 }
 
 }  // namespace

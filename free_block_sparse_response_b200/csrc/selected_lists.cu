@@ -36,9 +36,17 @@ __device__ __forceinline__ void each_selected(const SelArgs& a, int z, int t0, F
   const int per = 32 / width, slot = lane & (width - 1), sub = lane / width;
   const int len = kv_len_of(a, b), qs = q_start_of(a, b);
   bool bad = false;
+  // the first chunk of a row is read one step ahead
+  auto entry = [&](int i, int j) {
+    const int t = t0 + i;
+    return i < kSub && t < a.n && j < a.top ? __ldg(a.sel + (static_cast<size_t>(z) * a.n + t) * a.top + j) : -1;
+  };
+  int ahead = entry(warp * per + sub, slot);
   for (int i0 = warp * per; i0 < kSub && t0 + i0 < a.n; i0 += warps * per) {
     const int i = i0 + sub, t = t0 + i;
     const bool live = t < a.n;
+    const int head = ahead;
+    ahead = entry(i + warps * per, slot);
     // last block that holds a key the token may attend to (-1: none)
     int last = a.causal ? min(len - 1, qs + t) : len - 1;
     last = last < 0 ? -1 : last / a.block;
@@ -47,7 +55,7 @@ __device__ __forceinline__ void each_selected(const SelArgs& a, int z, int t0, F
     bool ended = false;
     for (int j0 = 0; j0 < a.top; j0 += width) {
       const int j = j0 + slot;
-      int g = live && j < a.top ? __ldg(a.sel + row + j) : -1;
+      const int g = j0 == 0 ? head : entry(i, j);
       // entries from the row's first negative one on do not count
       const unsigned neg = __ballot_sync(0xffffffffu, g < 0) >> (sub * width);
       const unsigned before = width == 32 ? (slot == 31 ? 0x7fffffffu : (1u << slot) - 1u) : (1u << slot) - 1u;
@@ -78,7 +86,7 @@ __device__ __forceinline__ void set_bits(const SelArgs& a, uint32_t* mask, int z
   __syncthreads();
 }
 
-__global__ void __launch_bounds__(256) count_kernel(const SelArgs a) {
+__global__ void __launch_bounds__(512) count_kernel(const SelArgs a) {
   extern __shared__ uint32_t mask[];  // [nb][kWords]
   const int z = blockIdx.y, s = blockIdx.x;  // sub-slice s of the head's tokens
   set_bits(a, mask, z, s * kSub);
@@ -183,7 +191,7 @@ __global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
       a.units[static_cast<size_t>(region) * a.unit_cap + u] = Unit{};
 }
 
-__global__ void __launch_bounds__(256) scatter_kernel(const SelArgs a) {
+__global__ void __launch_bounds__(512) scatter_kernel(const SelArgs a) {
   extern __shared__ uint32_t mask[];  // [nb][kWords], then the words' first entries [nb][kWords]
   const int z = blockIdx.y, s = blockIdx.x, t0 = s * kSub;
   set_bits(a, mask, z, t0);
@@ -221,11 +229,11 @@ cudaError_t launch_lists(const SelArgs& a, cudaStream_t st) {
   cudaError_t e = cudaFuncSetAttribute(count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
-  count_kernel<<<dim3(subs, heads), 256, mask, st>>>(a);
+  count_kernel<<<dim3(subs, heads), 512, mask, st>>>(a);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
   scan_kernel<<<heads * a.slices, 512, sizeof(int4) * a.nb, st>>>(a);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
-  scatter_kernel<<<dim3(subs, heads), 256, both, st>>>(a);
+  scatter_kernel<<<dim3(subs, heads), 512, both, st>>>(a);
   return counted(cudaGetLastError(), 1);
 }
 

@@ -72,8 +72,10 @@ def signatures():
 def _view(t: Optional[torch.Tensor]):
     if t is None:
         return None
+    n0, n1, n2, _ = t.shape
+    s0, s1, s2, _ = t.stride()
     # a dimension of one row has no stride to speak of
-    return ctypes.byref(_CView(t.data_ptr(), *(s if n > 1 else 0 for n, s in zip(t.shape[:3], t.stride()))))
+    return ctypes.byref(_CView(t.data_ptr(), s0 if n0 > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0))
 
 
 def _need_rows(name: str, t: torch.Tensor, shape=None, like: Optional[torch.Tensor] = None) -> None:
@@ -82,36 +84,37 @@ def _need_rows(name: str, t: torch.Tensor, shape=None, like: Optional[torch.Tens
         raise ValueError("SparsePR tensors must live on a CUDA device")
     if t.dim() != 4 or t.stride(3) != 1:
         raise ValueError(f"{name} must be [batch, heads, rows, d] with contiguous rows")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+    if like is None:
+        _s._dtype_code(t)
+    elif t.dtype != like.dtype or t.device != like.device:
         raise ValueError(f"{name} must have the type and device of the other tensors")
-    _s._dtype_code(t)
 
 
 def _need_flat(name: str, t: Optional[torch.Tensor], shape, dtype, device) -> None:
     """A contiguous CUDA tensor of the given shape, type and device, or None."""
-    if t is None:
-        return
-    if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t is not None and (t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+
+
+def _expanded(t: torch.Tensor) -> bool:
+    return 0 in t.stride() and any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride()))
 
 
 def _need_out(name: str, t: torch.Tensor) -> None:
     """No two rows of an output in one place."""
-    if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
+    if _expanded(t):
         raise ValueError(f"{name} must not be an expanded tensor")
 
 
 def _rows_like(t: torch.Tensor) -> torch.Tensor:
     """Empty tensor of t's shape and, unless it is expanded, memory order."""
-    if any(n > 1 and st == 0 for n, st in zip(t.shape, t.stride())):
-        return torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    return torch.empty_like(t)
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device) if _expanded(t) else torch.empty_like(t)
 
 
 def _run(device, name: str, *args) -> None:
-    stream = ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    stream = torch._C._cuda_getCurrentRawStream(device.index)
     if device.index == torch.cuda.current_device():
         _s._call(name, *args, stream)
     else:
