@@ -15,13 +15,14 @@
 // dQ parts go out as in the forward pass (fp16 with a power of two per row, planes of 64).
 //
 // Work of a tile (B = D = 128): 21 MFLOP, 16K exponentials, 64 KB gathered, 32 KB written.
-// Shared memory holds one Q / dO stage beside K, V, P and dS at B = D = 128 (192 KB), two
-// otherwise; TMEM is full (dQ goes over S), so a tile's stages follow one another: products of
-// two tiles do not overlap, the next gather runs under the output.
-//   warps 0-7   softmax and output: two threads a row, half the keys each; dQ and, at a block's
-//               end, dK and dV out of TMEM;
-//   warps 8-11  gather Q and dO rows, their lse, delta and visible keys;
-//   warp 12     issues the products;  warp 13 TMA boxes of K and V, zeros from the length on.
+// Shared memory (7 tiles of 32 KB) holds K, V, P, dS, one dO and two Q; TMEM is full (S, dP, dV^T,
+// dK^T; dQ goes over dP).  So dO is gathered as soon as dV has read it, under the products of dK
+// and dQ; Q a tile ahead; S of the next tile runs under dQ's way out.
+//   warps 0-7    softmax: two threads a row, half the keys each; at a block's end dK and dV;
+//   warps 8-11   dQ parts out of TMEM;
+//   warps 12-15  gather Q and dO rows, their lse, delta and visible keys (three tiles deep: list
+//                entry, numbers, rows);
+//   warp 16      issues the products;  warp 17 TMA boxes of K and V, zeros from the length on.
 #include <cuda.h>
 #include <cuda_fp16.h>
 
@@ -37,37 +38,43 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kInf = __builtin_huge_valf();
 
-constexpr int kThreads = 448, kWork = 256, kLoaders = 128;
-constexpr int kLoadWarp = 8, kMmaWarp = 12;
+constexpr int kThreads = 640, kWork = 256, kLoaders = 128;
+constexpr int kOutWarp = 8, kLoadWarp = 12, kMmaWarp = 16, kKvWarp = 17;
+constexpr int kRegSoftmax = 112, kRegOut = 104, kRegLoad = 88, kRegRest = 56;
 
 template <int D, int B>
 struct Bwd {
   static constexpr uint32_t kRowsD = 128 * D * 2, kRowsB = 128 * B * 2, kKV = B * D * 2;
-  static constexpr int kStages = D == 128 && B == 128 ? 1 : 2;
-  static constexpr uint32_t kTail = 2 * 128 * 12 + 512;  // lse, delta and visible keys of a stage's rows; barriers
-  static constexpr uint32_t kSmem = 2 * kKV + 2 * kRowsB + kStages * 2 * kRowsD + kTail;
+  static constexpr uint32_t kNums = 128 * 9;  // lse, delta and visible keys (a byte) of a tile's rows
+  static constexpr uint32_t kTail = 2 * kNums + 512;
+  // dK and dV leave through 4 KB a warp: at B = 128 where the warp's own part of P lies
+  static constexpr uint32_t kStage = B == 128 ? 0 : 8 * 4096;
+  static constexpr uint32_t kSmem = 2 * kKV + 2 * kRowsB + 3 * kRowsD + kStage + kTail;
 };
+static_assert(Bwd<128, 128>::kSmem <= 227 * 1024, "the largest form fits an SM");
 
-enum : int { kKvLand = 0, kKv, kKvFree, kS, kP, kDq, kDqFree, kAcc, kAccFree, kDrain, kQ, kQFree = kQ + 2, kNumBars = kQFree + 2 };
+enum : int {
+  kKvLand = 0, kKv, kKvFree, kS, kP, kDq, kDqFree, kAcc, kAccFree, kDrain, kG, kGFree, kQ, kQFree = kQ + 2,
+  kNumBars = kQFree + 2
+};
 
 template <int D, int B>
 __global__ void __launch_bounds__(kThreads, 1)
     selected_backward_tc_kernel(const __grid_constant__ BlockMap mk, const __grid_constant__ BlockMap mv, const SelArgs a,
                                 int first, int count) {
   using F = Bwd<D, B>;
-  constexpr int ST = F::kStages;
   extern __shared__ __align__(1024) uint8_t dsmem[];
   uint8_t* const tail = dsmem + F::kSmem - F::kTail;
-  float* const s_row = reinterpret_cast<float*>(tail);  // [stage][lse | delta | visible keys][128]
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(tail + 2 * 128 * 12);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(tail);
+  uint8_t* const s_num = tail + 512;  // [Q stage]: lse [128], delta [128], visible keys [128]
   uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(bars + kNumBars);
   int& abort_flag = *reinterpret_cast<int*>(bars + kNumBars + 1);
   int* const s_first = reinterpret_cast<int*>(bars + kNumBars + 2);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sK = tc::saddr(dsmem), sV = sK + F::kKV, sP = sV + F::kKV, sdS = sP + F::kRowsB, sRows = sdS + F::kRowsB;
-  // of a stage: dO, then Q (adjacent: one operand of 128 columns at D = 64)
-  auto sG = [&](int st) { return sRows + st * 2 * F::kRowsD; };
-  auto sQ = [&](int st) { return sG(st) + F::kRowsD; };
+  // dO, then the two Q tiles (at D = 64, dO and Q are one operand of 128 columns)
+  const uint32_t sG = sRows;
+  auto sQ = [&](int st) { return sRows + (1 + st) * F::kRowsD; };
   if ((sK & 1023u) != 0) {  // the tiles' swizzle counts from 1024-byte lines
     if (tid == 0) record_error(a.status, kErrCuda);
     return;
@@ -80,10 +87,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::mbar_init(bar(kS), 1);
     tc::mbar_init(bar(kP), kWork);
     tc::mbar_init(bar(kDq), 1);
-    tc::mbar_init(bar(kDqFree), kWork);
+    tc::mbar_init(bar(kDqFree), 128);
     tc::mbar_init(bar(kAcc), 1);
     tc::mbar_init(bar(kAccFree), kWork);
     tc::mbar_init(bar(kDrain), 1);
+    tc::mbar_init(bar(kG), kLoaders);
+    tc::mbar_init(bar(kGFree), 1);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(bar(kQ + i), kLoaders);
       tc::mbar_init(bar(kQFree + i), 1);
@@ -99,26 +108,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tS = tmem_slot, tDp = tS + 128, tAcc = tS + 256;  // dQ over S; dV^T, then dK^T from column B on
+  const uint32_t tS = tmem_slot, tDp = tS + 128, tAcc = tS + 256;  // dQ over dP; dV^T, then dK^T from column B on
   volatile int* abort_v = &abort_flag;
   const size_t cap = static_cast<size_t>(a.slice) * a.top;
   auto wait1 = [&](int i, int phase) { return wait_bar(bar(i), phase & 1, abort_v, a.status); };
   auto wait = [&](int i, int phase) { return __all_sync(0xffffffffu, wait1(i, phase)); };
 
-  if (warp < kLoadWarp) {
-    // ---------------------------------------------------------------- softmax, output
+  // registers: 96 a thread at launch, 480 x 128 in all; 2 x 112 + 104 + 88 + 56 of them are used
+  if (warp < kOutWarp) {
+    // ---------------------------------------------------------------- softmax, dK and dV
+    tc::setmaxnreg_inc<kRegSoftmax>();
     const int w4 = warp & 3, half = warp >> 2, row = 32 * w4 + lane;
     const uint32_t lanes = static_cast<uint32_t>(32 * w4) << 16;
     const float scale2 = a.scale * kLog2e;
-    uint8_t* const part = static_cast<uint8_t*>(static_cast<void*>(a.part));
+    const uint32_t stage = B == 128 ? sP + half * (128 * 128) + w4 * 4096 : sRows + 3 * F::kRowsD + warp * 4096;
     bool cut_open = false;
-    each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int u, bool opens, bool closes) {
-      const int st = t % ST;
-      if (!wait(kQ + st, t / ST) || !wait(kS, t)) return false;  // the row's numbers; S and dP
+    each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int, int t, int u, bool opens, bool closes) {
+      const int st = t & 1;
+      if (!wait(kQ + st, t >> 1) || !wait(kS, t)) return false;  // the row's numbers; S and dP
       tc::fence_after_sync();
-      const float* rd = s_row + st * 3 * 128 + row;
-      const float lse2 = rd[0], delta = rd[128];
-      const int nv = __float_as_int(rd[256]);
+      const uint8_t* nums = s_num + st * F::kNums;
+      const float lse2 = reinterpret_cast<const float*>(nums)[row], delta = reinterpret_cast<const float*>(nums)[128 + row];
+      const int nv = nums[1024 + row];
 #pragma unroll 1
       for (int c0 = half * (B / 2); c0 < (half + 1) * (B / 2); c0 += 32) {
         uint32_t s[32], dp[32];
@@ -146,28 +157,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_proxy_async();
       tc::fence_before_sync();
       tc::mbar_arrive(bar(kP));
-      // dQ: this warp's 16 rows (see the forward kernel's output)
-      if (!wait(kDq, t)) return false;
-      tc::fence_after_sync();
-      {
-        const int lane0 = 32 * w4 + 16 * half, q = lane >> 2, i = lane & 3;
-        uint32_t o[D / 2];
-#pragma unroll
-        for (int c = 0; c < D; c += 64)
-          tmem_ld_16x64(tS + (static_cast<uint32_t>(lane0) << 16) + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c / 2]));
-        tc::tmem_wait_ld();
-        tc::fence_before_sync();
-        tc::mbar_arrive(bar(kDqFree));
-        const float unit[2] = {1.f, 1.f};
-        float up[2];
-        const long long out0 = static_cast<long long>((ci * cap + un.off) * a.group + un.r0);
-        store_part<D>(o, unit, lane0 + q, un.rows, part + 32 * i, a.plane, out0, up);
-        if (i == 0) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (lane0 + q + 8 * k < un.rows) a.ml[out0 + lane0 + q + 8 * k] = make_float2(0.f, up[k] * a.scale);
-        }
-      }
       if (opens) cut_open = un.r0 > 0;  // the block's first tiles are another CTA's
       if (!closes) return true;
       // dK and dV: lane = head dim, columns = keys
@@ -175,12 +164,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_after_sync();
       const bool cut = cut_open || un.r0 + un.rows < un.total;
       const int which = D == 128 ? half : w4 >> 1;  // 0: dV, 1: dK
-      const int d = D == 128 ? row : row & 63;
       const int from = D == 128 ? 0 : half * (B / 2), to = D == 128 ? B : from + B / 2;
       const View& out = which ? a.gk : a.gv;
+      const int d0 = D == 128 ? 32 * w4 : 32 * (w4 & 1);  // the warp's first head dim
       __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(out.p) + un.b * out.sb + un.kh * out.sh +
-                           static_cast<long long>(un.g) * B * out.sn + d;
-      float* seg = a.seg + (static_cast<size_t>(2 * blockIdx.x + (u > 0)) * 2 + which) * B * D + d;
+                           static_cast<long long>(un.g) * B * out.sn + d0;
+      float* seg = a.seg + (static_cast<size_t>(2 * blockIdx.x + (u > 0)) * 2 + which) * B * D + d0 + lane;
       const float f = which ? a.scale : 1.f;
       const int keys = min(B, a.nk - un.g * B);
 #pragma unroll 1
@@ -188,116 +177,227 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t x[32];
         tc::tmem_ld32(tAcc + lanes + which * B + c0, x);
         tc::tmem_wait_ld();
+        if (cut) {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float y = __uint_as_float(x[c]) * f;
-          if (cut)
-            seg[static_cast<size_t>(c0 + c) * D] = y;
-          else if (c0 + c < keys)
-            dst[(c0 + c) * out.sn] = __float2bfloat16_rn(y);
+          for (int c = 0; c < 32; ++c) seg[static_cast<size_t>(c0 + c) * D] = __uint_as_float(x[c]) * f;
+          continue;
+        }
+        // 32 keys x 32 dims turned in shared memory (rows of 80 bytes: no two keys
+        // of a group in one bank), so that 4 lanes write 64 bytes of a key
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) st_shared_b16(stage + c * 80 + lane * 2, __float2bfloat16_rn(__uint_as_float(x[c]) * f));
+        __syncwarp();
+#pragma unroll
+        for (int c = 0; c < 32; c += 8) {
+          const int key = c + (lane >> 2);
+          const uint4 v = ld_shared_16(stage + key * 80 + (lane & 3) * 16);
+          if (c0 + key < keys) *reinterpret_cast<uint4*>(dst + (c0 + key) * out.sn + (lane & 3) * 8) = v;
         }
       }
       tc::fence_before_sync();
       tc::mbar_arrive(bar(kAccFree));
       return true;
     });
+  } else if (warp < kLoadWarp) {
+    // ---------------------------------------------------------------- dQ parts
+    tc::setmaxnreg_inc<kRegOut>();
+    const int w4 = warp & 3, q = lane >> 2, i = lane & 3;
+    uint8_t* const part = static_cast<uint8_t*>(static_cast<void*>(a.part));
+    each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
+      const long long out0 = static_cast<long long>((ci * cap + un.off) * a.group + un.r0);
+      if (!wait(kDq, t)) return false;
+      tc::fence_after_sync();
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        const int lane0 = 32 * w4 + 16 * half;
+        uint32_t o[D / 2];
+#pragma unroll
+        for (int c = 0; c < D; c += 64)
+          tmem_ld_16x64(tDp + (static_cast<uint32_t>(lane0) << 16) + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c / 2]));
+        tc::tmem_wait_ld();
+        if (half == 1) {
+          tc::fence_before_sync();
+          tc::mbar_arrive(bar(kDqFree));
+        }
+        const float one[2] = {1.f, 1.f};
+        float up[2];
+        store_part<D>(o, one, lane0 + q, un.rows, part + 32 * i, a.plane, out0, up);
+        if (i == 0) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (lane0 + q + 8 * k < un.rows) a.ml[out0 + lane0 + q + 8 * k] = make_float2(0.f, up[k] * a.scale);
+        }
+      }
+      return true;
+    });
   } else if (warp < kMmaWarp) {
     // ---------------------------------------------------------------- Q and dO rows, 32 a warp
+    tc::setmaxnreg_dec<kRegLoad>();
     constexpr int kPer = D / 8, kStep = 32 / kPer;  // lanes per row, rows per instruction
-    const int lw = warp - kLoadWarp, ch = lane % kPer;
-    each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
-      const int st = t % ST, r = 32 * lw + lane;
-      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q.p) + un.b * a.q.sb + un.kh * a.group * a.q.sh + ch * 8;
-      const __nv_bfloat16* g = static_cast<const __nv_bfloat16*>(a.go.p) + un.b * a.go.sb + un.kh * a.group * a.go.sh + ch * 8;
-      int tok = -1, h = 0, nv = 0;
-      float lse2 = 0.f, delta = 0.f;
-      if (r < un.rows) {
-        const int e = (un.r0 + r) / a.group;
-        tok = __ldg(a.list + (first + ci) * cap + un.off + e);
-        h = un.r0 + r - e * a.group;
-        const size_t at = (static_cast<size_t>(un.b) * a.Hq + un.kh * a.group + h) * a.n + tok;
-        lse2 = __ldg(a.lse + at) * kLog2e;
-        delta = a.delta[at];
-        nv = a.causal ? min(un.live, un.qs + tok + 1) : un.live;
-        if (lse2 == -kInf) nv = 0;  // a zero row of the forward pass
-      }
-      if (t >= ST && !wait(kQFree + st, t / ST - 1)) return false;
-      float* rd = s_row + st * 3 * 128 + r;
-      rd[0] = lse2, rd[128] = delta, rd[256] = __int_as_float(nv);
+    const int lw = warp - kLoadWarp, ch = lane % kPer, r = 32 * lw + lane;
+    struct Row {  // this lane's row of a tile, and what its warp copies from
+      const __nv_bfloat16 *q, *g;
+      int tok, h, live, qs;
+      float lse, delta;
+      size_t base;  // row of lse and delta of token 0 of the group's first head
+    };
+    // The walk is two tiles ahead of the copies: list entry, then the row's numbers, then rows.
+    Row fresh{}, known{};
+    bool have_fresh = false, have_known = false;
+    int t = 0;  // tile whose Q is copied next; dO follows one behind
+    auto copy = [&](uint32_t tile, const __nv_bfloat16* from, const View& v, int tok, int h) {
 #pragma unroll
       for (int s = 0; s < 32; s += kStep) {
         const int src = s + lane / kPer;
         const long long tk = __shfl_sync(0xffffffffu, tok, src);
         const int hh = __shfl_sync(0xffffffffu, h, src);
-        const uint32_t off = tc::sw128_offset(32 * lw + src, ch);
-        cp_async_16(sQ(st) + off, tk < 0 ? q : q + tk * a.q.sn + hh * a.q.sh, tk < 0 ? 0 : 16);
-        cp_async_16(sG(st) + off, tk < 0 ? g : g + tk * a.go.sn + hh * a.go.sh, tk < 0 ? 0 : 16);
+        cp_async_16(tile + tc::sw128_offset(32 * lw + src, ch), tk < 0 ? from : from + tk * v.sn + hh * v.sh, tk < 0 ? 0 : 16);
       }
       cp_async_commit();
-      cp_async_wait<0>();
-      tc::fence_proxy_async();
-      tc::mbar_arrive(bar(kQ + st));
+    };
+    Row held{};  // tile t - 1, whose dO is still to be copied
+    // dO of tile t - 1 and Q of tile t (either may be none), in flight together
+    auto load = [&](const Row* row) {
+      if (t > 0) {
+        if (t > 1 && !wait(kGFree, t - 2)) return false;
+        copy(sG, held.g, a.go, held.tok, held.h);
+      }
+      if (row != nullptr) {
+        const int st = t & 1;
+        if (t >= 2 && !wait(kQFree + st, (t >> 1) - 1)) return false;
+        uint8_t* nums = s_num + st * F::kNums;
+        reinterpret_cast<float*>(nums)[r] = row->lse * kLog2e;
+        reinterpret_cast<float*>(nums)[128 + r] = row->delta;
+        // no row, or a zero row of the forward pass: nothing visible
+        const int nv = min(a.causal ? min(row->live, row->qs + row->tok + 1) : row->live, B);
+        nums[1024 + r] = static_cast<uint8_t>(row->tok < 0 || row->lse == -kInf ? 0 : max(nv, 0));
+        copy(sQ(st), row->q, a.q, row->tok, row->h);
+      }
+      if (t > 0) {
+        if (row != nullptr)
+          cp_async_wait<1>();
+        else
+          cp_async_wait<0>();
+        tc::fence_proxy_async();
+        tc::mbar_arrive(bar(kG));
+      }
+      if (row != nullptr) {
+        cp_async_wait<0>();
+        tc::fence_proxy_async();
+        tc::mbar_arrive(bar(kQ + (t & 1)));
+        held = *row;
+        ++t;
+      }
+      return true;
+    };
+    auto step = [&]() {  // numbers of the fresh row; copies of the known one
+      Row next = fresh;
+      const bool ok = !have_known || load(&known);
+      if (have_fresh && next.tok >= 0) {
+        const size_t at = next.base + static_cast<size_t>(next.h) * a.n + next.tok;
+        next.lse = __ldg(a.lse + at);
+        next.delta = a.delta[at];
+      }
+      known = next;
+      have_known = have_fresh;
+      return ok;
+    };
+    bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int, int, bool, bool) {
+      if (!step()) return false;
+      fresh = Row{};
+      fresh.q = static_cast<const __nv_bfloat16*>(a.q.p) + un.b * a.q.sb + un.kh * a.group * a.q.sh + ch * 8;
+      fresh.g = static_cast<const __nv_bfloat16*>(a.go.p) + un.b * a.go.sb + un.kh * a.group * a.go.sh + ch * 8;
+      fresh.tok = -1, fresh.live = un.live, fresh.qs = un.qs;
+      fresh.base = (static_cast<size_t>(un.b) * a.Hq + un.kh * a.group) * a.n;
+      if (r < un.rows) {
+        const int e = (un.r0 + r) / a.group;
+        fresh.tok = __ldg(a.list + (first + ci) * cap + un.off + e);
+        fresh.h = un.r0 + r - e * a.group;
+      }
+      have_fresh = true;
       return true;
     });
+    if (ok && have_fresh) {
+      ok = step();
+      have_fresh = false;
+      ok = ok && step() && load(nullptr);
+    }
     cp_async_wait<0>();
-  } else if (warp == kMmaWarp) {
+  } else {
+    tc::setmaxnreg_dec<kRegRest>();
+  }
+  if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- products
     constexpr uint32_t kIdS = tc::idesc_bf16(128, B, false, false), kIdQ = tc::idesc_bf16(128, D, false, true);
     constexpr uint32_t kIdAcc = tc::idesc_bf16(128, D == 128 ? B : 2 * B, true, true);
     if (lane == 0) {
-      each_tile(a, first, s_first, 0, 1, [&](const Unit&, int, int t, int u, bool opens, bool closes) {
-        const int st = t % ST;
-        if (opens && !wait1(kKv, u)) return false;
-        if (!wait1(kQ + st, t / ST)) return false;
-        if (t > 0 && !wait1(kDqFree, t - 1)) return false;  // dQ, over S, is read
+      const int tiles = s_first[2];
+      auto issue_s = [&](int t) {  // once Q of the tile is there
+        if (!wait1(kQ + (t & 1), t >> 1)) return false;
         tc::fence_after_sync();
-        uint64_t dq = tc::sdesc_sw128(sQ(st), 16, 1024), dk = tc::sdesc_sw128(sK, 16, 1024);
-        uint64_t dg = tc::sdesc_sw128(sG(st), 16, 1024), dv = tc::sdesc_sw128(sV, 16, 1024);
+        uint64_t dq = tc::sdesc_sw128(sQ(t & 1), 16, 1024), dk = tc::sdesc_sw128(sK, 16, 1024);
         keep_here(dq, dk);
-        keep_here(dg, dv);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           tc::mma_ss(tS, dq + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
                      dk + ((kk >> 2) * (B * 128) + (kk & 3) * 32) / 16, kIdS, kk > 0 ? 1u : 0u);
+        return true;
+      };
+      if (tiles > 0 && wait1(kKv, 0) && issue_s(0))
+        each_tile(a, first, s_first, 0, 1, [&](const Unit&, int, int t, int u, bool opens, bool closes) {
+          const int st = t & 1;
+          if (!wait1(kG, t)) return false;
+          if (t > 0 && !wait1(kDqFree, t - 1)) return false;  // dQ, over dP, is read
+          tc::fence_after_sync();
+          uint64_t dg = tc::sdesc_sw128(sG, 16, 1024), dv = tc::sdesc_sw128(sV, 16, 1024);
+          keep_here(dg, dv);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_ss(tDp, dg + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
-                     dv + ((kk >> 2) * (B * 128) + (kk & 3) * 32) / 16, kIdS, kk > 0 ? 1u : 0u);
-        tc::mma_commit(bar(kS));
-        if (!wait1(kP, t)) return false;
-        if (opens && u > 0 && !wait1(kAccFree, u - 1)) return false;
-        tc::fence_after_sync();
-        uint64_t ds = tc::sdesc_sw128(sdS, 16, 1024), kt = tc::sdesc_sw128(sK, B * 128, 1024);
-        keep_here(ds, kt);
-#pragma unroll
-        for (int kk = 0; kk < B / 16; ++kk)
-          tc::mma_ss(tS, ds + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16, kt + kk * (2048 / 16), kIdQ, kk > 0 ? 1u : 0u);
-        tc::mma_commit(bar(kDq));
-        // contraction over the 128 rows: both operands rows apart, 64-column blocks 16 KB apart
-        uint64_t gt = tc::sdesc_sw128(sG(st), 128 * 128, 1024), pt = tc::sdesc_sw128(sP, 128 * 128, 1024);
-        keep_here(gt, pt);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc::mma_ss(tAcc, gt + kk * (2048 / 16), pt + kk * (2048 / 16), kIdAcc, !opens || kk > 0 ? 1u : 0u);
-        if (D == 128) {
-          uint64_t qt = tc::sdesc_sw128(sQ(st), 128 * 128, 1024), dt = tc::sdesc_sw128(sdS, 128 * 128, 1024);
-          keep_here(qt, dt);
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc::mma_ss(tDp, dg + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
+                       dv + ((kk >> 2) * (B * 128) + (kk & 3) * 32) / 16, kIdS, kk > 0 ? 1u : 0u);
+          tc::mma_commit(bar(kS));
+          if (!wait1(kP, t)) return false;
+          if (opens && u > 0 && !wait1(kAccFree, u - 1)) return false;
+          tc::fence_after_sync();
+          // dV first, so that the next dO can be gathered, then dQ, so that its way out runs under dK
+          // and the next S.  Contraction over the 128 rows: both operands rows apart, 64-column blocks of P and dS
+          // 16 KB apart, of dO (at D = 64: of dO and Q) as they lie
+          uint64_t gt = tc::sdesc_sw128(sG, D == 128 ? 128 * 128 : sQ(st) - sG, 1024);
+          uint64_t pt = tc::sdesc_sw128(sP, 128 * 128, 1024);
+          keep_here(gt, pt);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc::mma_ss(tAcc + B, qt + kk * (2048 / 16), dt + kk * (2048 / 16), kIdAcc, !opens || kk > 0 ? 1u : 0u);
-        }
-        tc::mma_commit(bar(kQFree + st));
-        if (closes) {
-          tc::mma_commit(bar(kAcc));
-          tc::mma_commit(bar(kKvFree));
-        }
-        return true;
-      });
+            tc::mma_ss(tAcc, gt + kk * (2048 / 16), pt + kk * (2048 / 16), kIdAcc, !opens || kk > 0 ? 1u : 0u);
+          tc::mma_commit(bar(kGFree));
+          if (D == 64) tc::mma_commit(bar(kQFree + st));
+          uint64_t ds = tc::sdesc_sw128(sdS, 16, 1024), kt = tc::sdesc_sw128(sK, B * 128, 1024);
+          keep_here(ds, kt);
+#pragma unroll
+          for (int kk = 0; kk < B / 16; ++kk)
+            tc::mma_ss(tDp, ds + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16, kt + kk * (2048 / 16), kIdQ, kk > 0 ? 1u : 0u);
+          tc::mma_commit(bar(kDq));
+          if (D == 128) {
+            uint64_t qt = tc::sdesc_sw128(sQ(st), 128 * 128, 1024), dt = tc::sdesc_sw128(sdS, 128 * 128, 1024);
+            keep_here(qt, dt);
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc::mma_ss(tAcc + B, qt + kk * (2048 / 16), dt + kk * (2048 / 16), kIdAcc, !opens || kk > 0 ? 1u : 0u);
+            tc::mma_commit(bar(kQFree + st));
+          }
+          if (closes) {
+            tc::mma_commit(bar(kAcc));
+            tc::mma_commit(bar(kKvFree));
+          }
+          // S of the next tile: the softmax has read this one's
+          if (t + 1 < tiles && ((closes && !wait1(kKv, u + 1)) || !issue_s(t + 1))) return false;
+          return true;
+        });
       tc::mma_commit(bar(kDrain));  // every product has finished before TMEM goes back
       tc::mbar_wait_quiet(bar(kDrain), 0);
     }
     __syncwarp();
-  } else {
+  } else if (warp == kKvWarp) {
     // ---------------------------------------------------------------- K and V of each block
     int issued = 0;
     const bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int, int, int u, bool opens, bool) {
@@ -394,7 +494,12 @@ cudaError_t backward(const SelArgs& a, int first, int count, cudaStream_t st) {
   if (!block_map(&mk, a.k, a, B) || !block_map(&mv, a.v, a, B)) return cudaErrorInvalidValue;
   auto kern = selected_backward_tc_kernel<D, B>;
   constexpr int smem = static_cast<int>(Bwd<D, B>::kSmem);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // the register split must fit in what a block is launched with, or its increase would wait for good
+  cudaFuncAttributes fa;
+  cudaError_t e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  if (128 * (2 * kRegSoftmax + kRegOut + kRegLoad + kRegRest) > fa.numRegs * kThreads) return cudaErrorInvalidConfiguration;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kern<<<kShares, kThreads, smem, st>>>(mk, mv, a, first, count);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
