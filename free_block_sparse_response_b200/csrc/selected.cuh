@@ -41,9 +41,12 @@ constexpr int kTcShares = 148;
 // One work item of the attention kernels: rows [r0, r0 + rows) of the entries of key block g,
 // whose first entry is `off` of its region's list; row r is query head r % group of entry r / group.
 // rows = 0: none.  live, qs: the length and the position of query 0, both from the block's first
-// key on.  total: the block's rows in this region.
+// key on.  total: the block's rows in this region.  k: power of two that the forward parts of
+// the block are divided by.
 struct __align__(16) Unit {
-  int g, off, r0, rows, live, qs, b, kh, total, pad[3];
+  int g, off, r0, rows, live, qs, b, kh, total;
+  float k;
+  int pad[2];
 };
 
 struct SelArgs {
@@ -74,7 +77,10 @@ struct SelArgs {
   // in planes of 64 columns (selected_tc.cu)
   float* part;
   long long plane;       // rows of a plane
-  float2* ml;            // forward: running maximum (log2 units) and sum of each partial row
+  // statistics of each partial row.  fp32: its maximum (log2 units) and sum; fp16 forward: its
+  // log-sum-exp and the exponent that its values are to be multiplied by 2^ of; fp16 dQ: -, scale
+  float2* ml;
+  float* vexp;           // [Bt * Hk][nb] Unit::k of each block (fp16 forward parts), or null
   float* delta;          // backward: sum of o * go per query row
   float* seg;            // backward: [chunk regions][seg_cap][2][block][d] sums of split blocks
   int seg_cap;
@@ -91,6 +97,8 @@ __device__ __forceinline__ int q_start_of(const SelArgs& a, int b) {
 cudaError_t launch_key_means(const SelArgs& a, const int* kv_start, int max_new, float* means, cudaStream_t st);
 cudaError_t launch_select(const SelArgs& a, int* sel, cudaStream_t st);
 cudaError_t launch_lists(const SelArgs& a, cudaStream_t st);
+// Unit::k of every block into a.vexp, before the lists.
+cudaError_t launch_value_exponents(const SelArgs& a, cudaStream_t st);
 // One chunk of `count` regions starting at region `first`.
 cudaError_t launch_selected_forward(const SelArgs& a, int first, int count, cudaStream_t st);
 cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cudaStream_t st);

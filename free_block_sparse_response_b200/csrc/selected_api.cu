@@ -86,7 +86,7 @@ constexpr size_t kPartialBytes = 1ull << 30;
 // status header).
 struct Plan {
   int regions, chunk;  // chunk: regions per launch
-  size_t slow, offs, list, inv, units, n_units, blk, part, ml, delta, seg, total;
+  size_t slow, vexp, offs, list, inv, units, n_units, blk, part, ml, delta, seg, total;
 };
 
 Plan make_plan(SelArgs& a, bool backward) {
@@ -130,6 +130,7 @@ Plan make_plan(SelArgs& a, bool backward) {
   const size_t R = L.regions;
   // the selection's list comes first: its place depends on nothing else
   L.slow = take(sizeof(int) * (static_cast<size_t>(a.Bt) * a.Hk * a.n + 1));
+  L.vexp = take(backward || a.f32 ? 0 : sizeof(float) * static_cast<size_t>(a.Bt) * a.Hk * a.nb);
   L.offs = take(sizeof(int) * R * a.nb * a.subs);
   L.list = take(sizeof(int) * R * entries);
   L.inv = take(sizeof(int) * static_cast<size_t>(a.Bt) * a.Hk * a.n * a.top);
@@ -262,6 +263,10 @@ int sparsepr_selected_attn(const sparsepr_selected* p, const sparsepr_view* Q, c
   bind(a, L, ws);
   a.q = view(Q), a.k = view(K), a.v = view(V), a.o = view(O), a.sel = sel, a.lse = lse;
   if (spr::use_decode(a)) return cuda_status(spr::launch_decode(a, st), "selected attention: few tokens");
+  if (!a.f32) {
+    a.vexp = at<float>(ws, L.vexp);
+    if ((rc = cuda_status(spr::launch_value_exponents(a, st), "selected attention: value exponents"))) return rc;
+  }
   if ((rc = cuda_status(spr::launch_lists(a, st), "selected attention: lists"))) return rc;
   for (int r = 0; r < L.regions; r += L.chunk)
     if ((rc = cuda_status(spr::launch_selected_forward(a, r, std::min(L.chunk, L.regions - r), st), "selected attention")))

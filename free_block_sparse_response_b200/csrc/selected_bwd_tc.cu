@@ -437,54 +437,83 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // dK and dV of the blocks that shares cut (their CTAs' sums, in order) and of blocks that no
-// query selected.  One CTA per (block, region of the chunk); `shares` CTAs ran the backward kernel.
+// query selected; `shares` CTAs ran the backward kernel.  A CTA looks at eight blocks of a
+// region, a warp each (most were written already), then works on those left, four loads a
+// thread under way.
 template <int D>
 __global__ void __launch_bounds__(256) join_kv_tc_kernel(const SelArgs a, int first, int count, int shares) {
-  __shared__ int s_sum, s_before;
-  const int g = blockIdx.x, ci = blockIdx.y, region = first + ci, z = region / a.slices, b = z / a.Hk, kh = z % a.Hk;
-  const int4 bk = a.blk[static_cast<size_t>(region) * a.nb + g];  // tiles, -, first tile of its region
-  int c0 = 0, c1 = -1;
-  long long t0 = 0;
-  if (bk.x > 0) {
-    if (threadIdx.x == 0) s_sum = s_before = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < count; i += blockDim.x) {
-      const int n = __ldg(a.n_units + first + i);
-      atomicAdd(&s_sum, n);
-      if (i < ci) atomicAdd(&s_before, n);
-    }
-    __syncthreads();
-    const long long sum = s_sum;
-    t0 = s_before + bk.z;
-    // share c holds tiles [sum c / shares, sum (c + 1) / shares)
-    auto share = [&](long long t) {
-      int c = static_cast<int>(t * shares / sum);
-      while (sum * (c + 1) / shares <= t) ++c;
-      while (sum * c / shares > t) --c;
-      return c;
-    };
-    c0 = share(t0), c1 = share(t0 + bk.x - 1);
-    if (c0 == c1) return;  // written by its one CTA
+  __shared__ int s_c0[8], s_c1[8], s_slot[8];  // shares of the block (c0 > c1: none, -1: nothing to do), slot of c0
+  const int ci = blockIdx.y, region = first + ci, z = region / a.slices, b = z / a.Hk, kh = z % a.Hk;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g0 = blockIdx.x * 8;
+  int all = 0, before = 0;
+  for (int i = lane; i < count; i += 32) {
+    const int n = __ldg(a.n_units + first + i);
+    all += n;
+    if (i < ci) before += n;
   }
-  const size_t tile = static_cast<size_t>(a.block) * D;
-  const long long sum = bk.x > 0 ? s_sum : 0;
-  for (int i = threadIdx.x * 4; i < a.block * D; i += 1024) {
-    const int j = g * a.block + i / D;
-    if (j >= a.nk) break;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-    for (int c = c0; c <= c1; ++c) {
-      if (sum * c / shares == sum * (c + 1) / shares) continue;  // an empty share
-      // a share that starts inside or at this block has it as its first run
-      const int slot = 2 * c + (sum * c / shares >= t0 ? 0 : 1);
-      const float4 v = *reinterpret_cast<const float4*>(a.seg + (2 * static_cast<size_t>(slot)) * tile + i);
-      const float4 k = *reinterpret_cast<const float4*>(a.seg + (2 * static_cast<size_t>(slot) + 1) * tile + i);
-      x.x += k.x, x.y += k.y, x.z += k.z, x.w += k.w;
-      y.x += v.x, y.y += v.y, y.z += v.z, y.w += v.w;
+  const long long sum = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
+  // first tile of share c
+  auto start = [&](int c) { return sum * c / shares; };
+  if (lane == 0) {
+    int c0 = -1, c1 = -1, slot = 0;
+    if (g0 + warp < a.nb) {
+      const int4 bk = a.blk[static_cast<size_t>(region) * a.nb + g0 + warp];  // tiles, -, first tile of its region
+      if (bk.x == 0) {
+        c0 = 0;  // zeros
+      } else {
+        const long long t0 = static_cast<long long>(before) + bk.z;
+        auto share = [&](long long t) {
+          int c = static_cast<int>(t * shares / sum);
+          while (start(c + 1) <= t) ++c;
+          while (start(c) > t) --c;
+          return c;
+        };
+        c0 = share(t0), c1 = share(t0 + bk.x - 1);
+        // the block is the first run of a share that starts at it or inside it, else the last
+        slot = 2 * c0 + (start(c0) >= t0 ? 0 : 1);
+        if (c0 == c1) c0 = c1 = -1;  // written by its one CTA
+      }
     }
-    __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(a.gk.p) + b * a.gk.sb + kh * a.gk.sh + j * a.gk.sn + i % D;
-    __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(a.gv.p) + b * a.gv.sb + kh * a.gv.sh + j * a.gv.sn + i % D;
-    *reinterpret_cast<uint2*>(dk) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-    *reinterpret_cast<uint2*>(dv) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    s_c0[warp] = c0, s_c1[warp] = c1, s_slot[warp] = slot;
+  }
+  __syncthreads();
+  const size_t tile = static_cast<size_t>(a.block) * D;
+  constexpr int kBatch = 4;
+  for (int w = 0; w < 8; ++w) {
+    const int c0 = s_c0[w], c1 = s_c1[w], g = g0 + w;
+    if (c0 < 0) continue;
+    for (int i0 = threadIdx.x * 4; i0 < a.block * D; i0 += kBatch * 1024) {
+      float4 x[kBatch], y[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) x[k] = y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int c = c0; c <= c1; ++c) {
+        if (start(c) == start(c + 1)) continue;  // an empty share
+        const size_t slot = c == c0 ? s_slot[w] : 2 * c;
+        float4 u[kBatch], v[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (i0 + k * 1024 < a.block * D) {
+            u[k] = *reinterpret_cast<const float4*>(a.seg + (2 * slot + 1) * tile + i0 + k * 1024);
+            v[k] = *reinterpret_cast<const float4*>(a.seg + 2 * slot * tile + i0 + k * 1024);
+          }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (i0 + k * 1024 < a.block * D) {
+            x[k].x += u[k].x, x[k].y += u[k].y, x[k].z += u[k].z, x[k].w += u[k].w;
+            y[k].x += v[k].x, y[k].y += v[k].y, y[k].z += v[k].z, y[k].w += v[k].w;
+          }
+      }
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const int i = i0 + k * 1024, j = g * a.block + i / D;
+        if (i >= a.block * D || j >= a.nk) continue;
+        __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(a.gk.p) + b * a.gk.sb + kh * a.gk.sh + j * a.gk.sn + i % D;
+        __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(a.gv.p) + b * a.gv.sb + kh * a.gv.sh + j * a.gv.sn + i % D;
+        *reinterpret_cast<uint2*>(dk) = make_uint2(pack_bf16x2(x[k].x, x[k].y), pack_bf16x2(x[k].z, x[k].w));
+        *reinterpret_cast<uint2*>(dv) = make_uint2(pack_bf16x2(y[k].x, y[k].y), pack_bf16x2(y[k].z, y[k].w));
+      }
+    }
   }
 }
 
@@ -503,7 +532,7 @@ cudaError_t backward(const SelArgs& a, int first, int count, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   kern<<<kShares, kThreads, smem, st>>>(mk, mv, a, first, count);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
-  join_kv_tc_kernel<D><<<dim3(a.nb, count), 256, 0, st>>>(a, first, count, kShares);
+  join_kv_tc_kernel<D><<<dim3(ceil_div(a.nb, 8), count), 256, 0, st>>>(a, first, count, kShares);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
   return launch_join_half(a, first, count, true, st);
 }

@@ -19,6 +19,7 @@
 
 #include "common.cuh"
 #include "selected.cuh"
+#include "selected_tc.cuh"
 #include "warp_mma.cuh"
 
 namespace cg = cooperative_groups;
@@ -32,7 +33,7 @@ constexpr float kInf = __builtin_huge_valf();
 constexpr int kWarps = 4, kPiece = 32;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kWarps) decode_kernel(const SelArgs a, int splits) {
+__global__ void __launch_bounds__(32 * kWarps, 2) decode_kernel(const SelArgs a, int splits) {
   constexpr int S = D / 32, H = D / 64;  // dim steps of a K load, column halves
   __shared__ float s_o[kWarps][16][D];
   __shared__ float2 s_ml[kWarps][16];
@@ -62,110 +63,132 @@ __global__ void __launch_bounds__(32 * kWarps) decode_kernel(const SelArgs a, in
       qa[2 * s][half] = v.x, qa[2 * s][2 + half] = v.y;
       qa[2 * s + 1][half] = v.z, qa[2 * s + 1][2 + half] = v.w;
     }
-  float o[8 * H][4] = {}, m[2] = {-kInf, -kInf}, l[2] = {0.f, 0.f};
+  float acc[8 * H][4] = {}, m[2] = {-kInf, -kInf}, l[2] = {0.f, 0.f};
   const float scale2 = a.scale * kLog2e;
   const __nv_bfloat16* kbase = static_cast<const __nv_bfloat16*>(a.k.p) + b * a.k.sb + kh * a.k.sh + 8 * t4;
   const __nv_bfloat16* vbase = static_cast<const __nv_bfloat16*>(a.v.p) + b * a.v.sb + kh * a.v.sh + 8 * g;
   const int per = a.block / kPiece;  // pieces of a block
-  int prev = -1;
-  bool bad = false, ended = false;
-  int slot = 0;
   const int stride = splits * kWarps;
-  // every warp walks the whole row (ascending entries, up to the first negative one) and takes
-  // every stride-th piece of 32 keys
-  int piece = (split * kWarps + warp) % stride;
-  for (; slot < a.top && !ended; ++slot) {
-    const int blk = __ldg(row + slot);
-    if (blk < 0) {
-      ended = true;
-      continue;
+  // The row's valid entries (ascending, in range, up to the first negative one), 32 slots at a
+  // time by the lanes; their pieces go to the cluster's warps in turn.
+  bool bad = false, ended = false;
+  int above = -1, piece = split * kWarps + warp;
+  for (int s0 = 0; s0 < a.top && !ended; s0 += 32) {
+    const int blk = s0 + lane < a.top ? __ldg(row + s0 + lane) : -1;
+    const unsigned neg = __ballot_sync(0xffffffffu, blk < 0);
+    const bool past = (neg & ((2u << lane) - 1u)) != 0;
+    const int v = past || blk >= a.nb ? -1 : blk;
+    int mx = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, mx, o);
+      if (lane >= o) mx = max(mx, y);
     }
-    if (blk >= a.nb || blk <= prev) {
-      bad = true;
-      continue;
+    int prev = __shfl_up_sync(0xffffffffu, mx, 1);
+    prev = max(above, lane > 0 ? prev : -1);
+    if (!past && (blk >= a.nb || blk <= prev)) bad = true;
+    const unsigned valid = __ballot_sync(0xffffffffu, v >= 0 && v > prev && v * a.block <= last);
+    above = max(above, __shfl_sync(0xffffffffu, mx, 31));
+    ended = neg != 0;
+    const int n_pieces = __popc(valid) * per;
+    // this warp's steps of 16 keys: two a piece; K of the next step is asked for once S is formed,
+    // V once O is, so that loads are under way during the arithmetic
+    const int steps = piece < n_pieces ? 2 * ((n_pieces - piece + stride - 1) / stride) : 0;
+    auto key_of = [&](int k) {  // first key of step k
+      const int p = piece + (k >> 1) * stride, at = static_cast<int>(__fns(valid, 0, p / per + 1));
+      return __shfl_sync(0xffffffffu, blk, at) * a.block + p % per * kPiece + 16 * (k & 1);
+    };
+    uint4 kv[2][S], vv[4][H];
+    auto load_k = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int key = j + 8 * i + g;
+        const __nv_bfloat16* p = kbase + key * a.k.sn;
+#pragma unroll
+        for (int x = 0; x < S; ++x)
+          kv[i][x] = key <= last ? __ldcs(reinterpret_cast<const uint4*>(p + 32 * x)) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    auto load_v = [&](int j) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+        const int key = j + 2 * t4 + (i & 1) + 8 * (i >> 1);
+        const __nv_bfloat16* p = vbase + key * a.v.sn;
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+          vv[i][h] = key <= last ? __ldcs(reinterpret_cast<const uint4*>(p + 64 * h)) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    int j = 0;
+    if (steps > 0) {
+      j = key_of(0);
+      load_k(j);
+      load_v(j);
     }
-    prev = blk;
-    for (; piece < per; piece += stride) {
-      const int j0 = blk * a.block + piece * kPiece;
-      if (j0 > last) continue;
 #pragma unroll 1
-      for (int j = j0; j < j0 + kPiece && j <= last; j += 16) {
-        uint4 kv[2][S], vv[4][H];
+    for (int k = 0; k < steps; ++k) {
+      const int next = k + 1 < steps ? key_of(k + 1) : 0;
+      float s[2][4] = {};
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int key = j + 8 * i + g;
-          const __nv_bfloat16* p = kbase + key * a.k.sn;
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int s = 0; s < S; ++s)
-            kv[i][s] = key <= last ? __ldcs(reinterpret_cast<const uint4*>(p + 32 * s)) : make_uint4(0, 0, 0, 0);
+        for (int x = 0; x < S; ++x) {
+          const uint32_t b0[2] = {kv[i][x].x, kv[i][x].y}, b1[2] = {kv[i][x].z, kv[i][x].w};
+          mma_bf16_16816(s[i], qa[2 * x], b0);
+          mma_bf16_16816(s[i], qa[2 * x + 1], b1);
         }
+      if (k + 1 < steps) load_k(next);
+      float p[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
-          const int key = j + 2 * t4 + (i & 1) + 8 * (i >> 1);
-          const __nv_bfloat16* p = vbase + key * a.v.sn;
-#pragma unroll
-          for (int h = 0; h < H; ++h)
-            vv[i][h] = key <= last ? __ldcs(reinterpret_cast<const uint4*>(p + 64 * h)) : make_uint4(0, 0, 0, 0);
-        }
-        float s[2][4] = {};
+      for (int r = 0; r < 2; ++r) {  // rows g and g + 8
+        float mx = -kInf;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int k = 0; k < S; ++k) {
-            const uint32_t b0[2] = {kv[i][k].x, kv[i][k].y}, b1[2] = {kv[i][k].z, kv[i][k].w};
-            mma_bf16_16816(s[i], qa[2 * k], b0);
-            mma_bf16_16816(s[i], qa[2 * k + 1], b1);
+          for (int c = 0; c < 2; ++c) {
+            float& x = s[i][2 * r + c];
+            x = j + 8 * i + 2 * t4 + c <= last ? x * scale2 : -kInf;
+            mx = fmaxf(mx, x);
           }
-        float p[2][4];
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[r], mx), ms = mn == -kInf ? 0.f : mn;
+        const float f = ex2(m[r] - ms);
+        m[r] = mn;
+        l[r] *= f;
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {  // rows g and g + 8
-          float mx = -kInf;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float& x = s[i][2 * r + c];
-              x = j + 8 * i + 2 * t4 + c <= last ? x * scale2 : -kInf;
-              mx = fmaxf(mx, x);
-            }
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(m[r], mx), ms = mn == -kInf ? 0.f : mn;
-          const float f = exp2f(m[r] - ms);
-          m[r] = mn;
-          l[r] *= f;
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              p[i][2 * r + c] = exp2f(s[i][2 * r + c] - ms);
-              l[r] += p[i][2 * r + c];
-            }
-#pragma unroll
-          for (int n = 0; n < 8 * H; ++n) o[n][2 * r] *= f, o[n][2 * r + 1] *= f;
-        }
-        const uint32_t pa[4] = {pack_bf16x2(p[0][0], p[0][1]), pack_bf16x2(p[0][2], p[0][3]), pack_bf16x2(p[1][0], p[1][1]),
-                                pack_bf16x2(p[1][2], p[1][3])};
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t* x[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) x[i] = reinterpret_cast<const uint32_t*>(&vv[i][h]);
-#pragma unroll
-            for (int odd = 0; odd < 2; ++odd) {  // columns 64 h + 8 g + 2 w + odd
-              const uint32_t sel = odd ? 0x7632 : 0x5410;
-              const uint32_t bb[2] = {__byte_perm(x[0][w], x[1][w], sel), __byte_perm(x[2][w], x[3][w], sel)};
-              mma_bf16_16816(o[8 * h + 2 * w + odd], pa, bb);
-            }
+          for (int c = 0; c < 2; ++c) {
+            p[i][2 * r + c] = ex2(s[i][2 * r + c] - ms);
+            l[r] += p[i][2 * r + c];
           }
+#pragma unroll
+        for (int n = 0; n < 8 * H; ++n) acc[n][2 * r] *= f, acc[n][2 * r + 1] *= f;
       }
+      const uint32_t pa[4] = {pack_bf16x2(p[0][0], p[0][1]), pack_bf16x2(p[0][2], p[0][3]), pack_bf16x2(p[1][0], p[1][1]),
+                              pack_bf16x2(p[1][2], p[1][3])};
+#pragma unroll
+      for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t* x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = reinterpret_cast<const uint32_t*>(&vv[i][h]);
+#pragma unroll
+          for (int odd = 0; odd < 2; ++odd) {  // columns 64 h + 8 g + 2 w + odd
+            const uint32_t sel = odd ? 0x7632 : 0x5410;
+            const uint32_t bb[2] = {__byte_perm(x[0][w], x[1][w], sel), __byte_perm(x[2][w], x[3][w], sel)};
+            mma_bf16_16816(acc[8 * h + 2 * w + odd], pa, bb);
+          }
+        }
+      if (k + 1 < steps) load_v(next);
+      j = next;
     }
-    piece -= per;
+    piece += steps / 2 * stride - n_pieces;
   }
-  if (bad && split == 0 && warp == 0 && lane == 0) record_error(a.status, kErrInvalidArg);
-  // o[8 h + n][2 r + c]: row g + 8 r, column 64 h + 8 (2 t4 + c) + n
+  if (bad && split == 0 && warp == 0) record_error(a.status, kErrInvalidArg);
+  // acc[8 h + n][2 r + c]: row g + 8 r, column 64 h + 8 (2 t4 + c) + n
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
@@ -178,8 +201,8 @@ __global__ void __launch_bounds__(32 * kWarps) decode_kernel(const SelArgs a, in
 #pragma unroll
         for (int n = 0; n < 8; n += 4)
           *reinterpret_cast<float4*>(&s_o[warp][g + 8 * r][64 * h + 8 * (2 * t4 + c) + n]) =
-              make_float4(o[8 * h + n][2 * r + c], o[8 * h + n + 1][2 * r + c], o[8 * h + n + 2][2 * r + c],
-                          o[8 * h + n + 3][2 * r + c]);
+              make_float4(acc[8 * h + n][2 * r + c], acc[8 * h + n + 1][2 * r + c], acc[8 * h + n + 2][2 * r + c],
+                          acc[8 * h + n + 3][2 * r + c]);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < heads * D; i += 32 * kWarps) {
@@ -188,14 +211,14 @@ __global__ void __launch_bounds__(32 * kWarps) decode_kernel(const SelArgs a, in
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, s_ml[w][h].x);
     const float ms = mx == -kInf ? 0.f : mx;
-    float sum = 0.f, acc = 0.f;
+    float sum = 0.f, x = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f(s_ml[w][h].x - ms);
+      const float f = ex2(s_ml[w][h].x - ms);
       sum = fmaf(f, s_ml[w][h].y, sum);
-      acc = fmaf(f, s_o[w][h][c], acc);
+      x = fmaf(f, s_o[w][h][c], x);
     }
-    s_co[h][c] = acc;
+    s_co[h][c] = x;
     if (c == 0) s_cml[h] = make_float2(mx, sum);
   }
   cg::cluster_group cluster = cg::this_cluster();
@@ -209,16 +232,16 @@ __global__ void __launch_bounds__(32 * kWarps) decode_kernel(const SelArgs a, in
     float mx = -kInf;
     for (int w = 0; w < splits; ++w) mx = fmaxf(mx, (splits > 1 ? cluster.map_shared_rank(s_cml, w) : s_cml)[h].x);
     const float ms = mx == -kInf ? 0.f : mx;
-    float sum = 0.f, acc = 0.f;
+    float sum = 0.f, x = 0.f;
     for (int w = 0; w < splits; ++w) {
       const float2 st = (splits > 1 ? cluster.map_shared_rank(s_cml, w) : s_cml)[h];
-      const float f = exp2f(st.x - ms);
+      const float f = ex2(st.x - ms);
       sum = fmaf(f, st.y, sum);
-      acc = fmaf(f, *((splits > 1 ? cluster.map_shared_rank(&s_co[0][0], w) : &s_co[0][0]) + i), acc);
+      x = fmaf(f, *((splits > 1 ? cluster.map_shared_rank(&s_co[0][0], w) : &s_co[0][0]) + i), x);
     }
     const int hq = kh * a.group + h0 + h;
     static_cast<__nv_bfloat16*>(a.o.p)[b * a.o.sb + hq * a.o.sh + t * a.o.sn + c] =
-        __float2bfloat16_rn(sum > 0.f ? acc / sum : sum != sum ? sum : 0.f);
+        __float2bfloat16_rn(sum > 0.f ? x / sum : sum != sum ? sum : 0.f);
     if (c == 0)
       a.lse[(static_cast<size_t>(b) * a.Hq + hq) * a.n + t] = sum > 0.f || sum != sum ? (mx + log2f(sum)) * kLn2 : -kInf;
   }
@@ -228,10 +251,11 @@ __global__ void __launch_bounds__(32 * kWarps) decode_kernel(const SelArgs a, in
 template <int D>
 cudaError_t decode(const SelArgs& a, cudaStream_t st) {
   const long long units = static_cast<long long>(a.Bt) * a.Hk * a.n * ceil_div(a.group, 16);
-  // The smallest cluster that covers the SMs twice, up to eight CTAs and to a warp for each piece.
+  // Three CTAs fit an SM: the smallest cluster that gives four per SM, up to eight CTAs and to a
+  // warp for each piece.
   const int pieces = std::min(a.top, a.nb) * (a.block / kPiece);
   int splits = 1;
-  while (splits < 8 && units * splits < 2 * 148 && 2 * splits * kWarps <= pieces) splits *= 2;
+  while (splits < 8 && units * splits < 4 * 148 && 2 * splits * kWarps <= pieces) splits *= 2;
   if (units * splits > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units * splits));

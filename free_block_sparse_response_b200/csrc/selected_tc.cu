@@ -4,10 +4,11 @@
 // query rows that selected it.  K and V of the block stay in shared memory; 128 rows at a time
 //   S = Q K^T (128 x B),  P = exp(S - row max),  O = P V (128 x D)
 // need no running maximum, since one tile holds all the keys of the row's part.  The part goes
-// out as O / l in fp16 times a power of two per row (the row's largest magnitude scaled to
-// 1/2 .. 1), with its log-sum-exp; join_half_kernel adds a row's parts.  fp16 with its own scale
-// rounds a part by 2^-12 of the row's largest element, 16 times finer than the result's bf16;
-// fp32 parts would double the traffic that bounds the pass.
+// out in fp16, with its log-sum-exp; join_half_kernel adds a row's parts.  So that O needs no
+// scaling on its way out, P is formed as exp(S - row max) 2^-k: with |V| < 2^e in the block
+// (value_exponents_kernel), k = e + log2 B - 15 keeps |O| <= 2^15, inside fp16, and leaves its 11
+// bits to everything down to 2^-29 of that bound.  A part's rounding, 2^-12, is 16 times finer
+// than the result's bf16; fp32 parts would double the traffic of the output and the join.
 //
 // Work of a tile (B = D = 128): 8.4 MFLOP, 16K exponentials, 32 KB of Q gathered, 32 KB written.
 // A tile passes through five stages of ~1 us (gather, S, softmax, O, output), so one persistent
@@ -21,7 +22,8 @@
 //   warps 16-17  issue the products of one stream each: S of the stream's next tile as soon as
 //                the softmax has read the last one, O when P is written;
 //   warp 18      TMA boxes of the units' K and V, and zeros over V rows at or past the length
-//                (their P is 0, but 0 times what a cache holds there need not be).
+//                (their P is 0, but 0 times what a cache holds there need not be);
+//   warp 19      reads the tiles' records and list entries into L1 ahead of the others.
 // All waits are bounded; on a timeout every role leaves, products and copies in flight drained.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -43,11 +45,12 @@ constexpr float kInf = __builtin_huge_valf();
 constexpr int kThreads = 640, kLoaders = 128;
 constexpr int kRegSoftmax = 112, kRegOut = 136, kRegRest = 56;
 constexpr int kOutWarp = 8, kLoadWarp = 12, kMmaWarp = 16, kKvWarp = 18;
+constexpr float kFold = 60.f;  // the part of k that P takes; the rest (values above 2^68) the output
 
 template <int D, int B>
 struct Fwd {
   static constexpr uint32_t kSlot = 128 * (D > B ? D : B) * 2, kKV = B * D * 2;
-  static constexpr uint32_t kTail = 2 * 128 * sizeof(float2) + 512;  // row statistics, barriers
+  static constexpr uint32_t kTail = 512;  // barriers
   static constexpr int kFit = (227 * 1024 - 2 * kKV - kTail) / kSlot;
   static constexpr int kSlots = kFit < 8 ? kFit : 8;
   static constexpr uint32_t kSmem = kSlots * kSlot + 2 * kKV + kTail;
@@ -83,8 +86,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int R = F::kSlots;
   extern __shared__ __align__(1024) uint8_t dsmem[];
   uint8_t* const tail = dsmem + R * F::kSlot + 2 * F::kKV;
-  float2* const s_stat = reinterpret_cast<float2*>(tail);  // [stream][row] log-sum-exp (log2 units), 1 / sum
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(tail + 2 * 128 * sizeof(float2));
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(tail);
   uint32_t& tmem_slot = *reinterpret_cast<uint32_t*>(bars + kNumBars);
   int& abort_flag = *reinterpret_cast<int*>(bars + kNumBars + 1);
   int* const s_first = reinterpret_cast<int*>(bars + kNumBars + 2);
@@ -152,9 +154,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (cut) mask_from(s, nv - c0);
           max_into(mx, s);
         }
-        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2;
-        const float ms = m == -kInf ? 0.f : m;
-        const uint64_t sc2 = f32x2(scale2, scale2), nm2 = f32x2(-ms, -ms);
+        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2, kf = fminf(un.k, kFold);
+        const float shift = (m == -kInf ? 0.f : m) + kf;
+        const uint64_t sc2 = f32x2(scale2, scale2), nm2 = f32x2(-shift, -shift);
         uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
         const uint32_t sP = sSlot + (t % R) * F::kSlot;  // over Q, which S has read
 #pragma unroll 1
@@ -176,16 +178,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             st_shared_16(sP + tc::sw128_offset(row, c0 / 8 + c), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2], pk[4 * c + 3]);
         }
         tc::fence_proxy_async();
+        tc::fence_before_sync();
+        tc::mbar_arrive(bar(kP + x));
         float l0, l1, l2, l3;
         f32x2_split(sum[0], l0, l1);
         f32x2_split(sum[1], l2, l3);
-        // the output warps have taken the statistics of the stream's tile before
-        if (t > 1 && !wait(kOFree + x, (t >> 1) - 1)) return false;
         const float l = (l0 + l1) + (l2 + l3);  // not above 0: no visible key (or a NaN, which stays one)
-        s_stat[x * 128 + row] = make_float2(l > 0.f || l != l ? m + __log2f(l) : -kInf,
-                                            l > 0.f ? __fdividef(1.f, l) : l != l ? l : 0.f);
-        tc::fence_before_sync();
-        tc::mbar_arrive(bar(kP + x));
+        if (row < un.rows)
+          a.ml[(ci * cap + un.off) * a.group + un.r0 + row] =
+              l > 0.f || l != l ? make_float2(shift + __log2f(l), shift + (un.k - kf)) : make_float2(-kInf, -kInf);
         return true;
     });
   } else if (warp < kLoadWarp) {
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
         const int x = t & 1;
         const long long out0 = static_cast<long long>((ci * cap + un.off) * a.group + un.r0);
-        if (!wait(kP + x, t >> 1) || !wait(kO + x, t >> 1)) return false;  // the statistics, O
+        if (!wait(kO + x, t >> 1)) return false;
         tc::fence_after_sync();
         const uint32_t tO = tbase + 256 + 128 * x;
 #pragma unroll 1
@@ -210,16 +211,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < D; c += 64)
             tmem_ld_16x64(tO + (static_cast<uint32_t>(lane0) << 16) + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c / 2]));
           tc::tmem_wait_ld();
-          // rows lane0 + q and lane0 + q + 8, side by side: this stage is bound by its latencies
-          const float2 st[2] = {s_stat[x * 128 + lane0 + q], s_stat[x * 128 + lane0 + q + 8]};
-          const float inv_l[2] = {st[0].y, st[1].y};
-          float up[2];
-          store_part<D>(o, inv_l, lane0 + q, un.rows, part + 32 * i, a.plane, out0, up);
-          if (i == 0) {
+          if (un.k > kFold) {
+            const float f = exp2f(kFold - un.k);
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              if (lane0 + q + 8 * k < un.rows) a.ml[out0 + lane0 + q + 8 * k] = make_float2(st[k].x, up[k]);
+            for (int c = 0; c < D / 2; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
           }
+          store_part_as_is<D>(o, lane0 + q, un.rows, part + 32 * i, a.plane, out0);
         }
         tc::fence_before_sync();
         tc::mbar_arrive(bar(kOFree + x));
@@ -235,16 +232,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_proxy_async();
       tc::mbar_arrive(bar(kQ + tile % R));
     };
-    // The copies of a tile are issued when the walk is at the next one, so that the list entry
-    // read here has arrived.
-    Unit last{};
-    int entry = 0;
-    auto copy = [&](int t) {
+    const bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
       const __nv_bfloat16* q =
-          static_cast<const __nv_bfloat16*>(a.q.p) + last.b * a.q.sb + last.kh * a.group * a.q.sh + ch * 8;
-      const int row = last.r0 + 32 * lw + lane;
-      const long long off =
-          32 * lw + lane < last.rows ? entry * a.q.sn + (row % a.group) * a.q.sh : -1;
+          static_cast<const __nv_bfloat16*>(a.q.p) + un.b * a.q.sb + un.kh * a.group * a.q.sh + ch * 8;
+      const int r = 32 * lw + lane;  // this lane's row of the tile
+      long long off = -1;
+      if (r < un.rows) {
+        const int row = un.r0 + r, e = row / a.group;
+        off = a.list[(first + ci) * cap + un.off + e] * a.q.sn + (row - e * a.group) * a.q.sh;
+      }
       if (t >= R && !wait(kFree + t % R, t / R - 1)) return false;
       const uint32_t sQ = sSlot + (t % R) * F::kSlot;
 #pragma unroll
@@ -259,19 +255,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         landed(t - 1);
       }
       return true;
-    };
-    bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
-      int e = 0;
-      if (32 * lw + lane < un.rows)
-        e = __ldg(a.list + (first + ci) * cap + un.off + (un.r0 + 32 * lw + lane) / a.group);
-      if (t > 0 && !copy(t - 1)) return false;
-      last = un, entry = e;
-      return true;
     });
     const int tiles = s_first[2];
-    ok = ok && tiles > 0 && copy(tiles - 1);
     cp_async_wait<0>();
-    if (ok) landed(tiles - 1);
+    if (ok && tiles > 0) landed(tiles - 1);
   } else {
     tc::setmaxnreg_dec<kRegRest>();
   if (warp < kKvWarp) {
@@ -377,6 +364,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (issued % 2 == 0) tc::mbar_wait_quiet(bar(kVLand), (issued / 2 - 1) & 1);
     }
     __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- records and lists into L1
+    // up to two rings ahead of the slots' release (a wait may match a later phase of the same
+    // parity: it then holds on for that one)
+    touch_ahead(a, first, s_first, [&](int t) { return t < 3 * R || wait(kFree + t % R, t / R - 3); });
   }
   }
   tc::fence_before_sync();
@@ -411,7 +403,7 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
   float m = -kInf, l = 0.f, acc[8] = {};
   for (int j0 = 0; j0 < a.top; j0 += kPer) {
     const int e = live && j0 + ch < a.top ? __ldg(inv + j0 + ch) : -1;
-    const float2 st = e >= 0 ? __ldcs(a.ml + row0 + static_cast<size_t>(e) * a.group) : make_float2(-kInf, 0.f);
+    const float2 st = e >= 0 ? __ldcs(a.ml + row0 + static_cast<size_t>(e) * a.group) : make_float2(-kInf, GRAD ? 0.f : -kInf);
     float f = st.y;
     if (!GRAD) {
       float mx = st.x;
@@ -421,7 +413,7 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
       const float ms = mx == -kInf ? 0.f : mx, old = exp2f(m - ms), wt = exp2f(st.x - ms);
       m = mx;
       l = fmaf(l, old, wt);
-      f *= wt;
+      f = exp2f(st.y - ms);
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] *= old;
     }
@@ -464,6 +456,38 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
         l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -kInf;
 }
 
+// Unit::k of each block: e + log2 B - 15 with |V| < 2^e over the block's finite values.
+template <int D>
+__global__ void __launch_bounds__(256) value_exponents_kernel(const SelArgs a) {
+  constexpr int kPer = D / 8, kRows = 256 / kPer;
+  __shared__ int s_max;
+  const int g = blockIdx.x, kh = blockIdx.y, b = blockIdx.z;
+  const int rows = min(a.block, kv_len_of(a, b) - g * a.block);
+  if (threadIdx.x == 0) s_max = 0;
+  __syncthreads();
+  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v.p) + b * a.v.sb + kh * a.v.sh +
+                           static_cast<long long>(g) * a.block * a.v.sn + threadIdx.x % kPer * 8;
+  int mx = 0;  // largest magnitude's bits: ordered as integers, without sign
+#pragma unroll 4
+  for (int r = threadIdx.x / kPer; r < rows; r += kRows) {
+    const uint4 x = *reinterpret_cast<const uint4*>(v + r * a.v.sn);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int lo = static_cast<int>(w[i] & 0x7fffu), hi = static_cast<int>(w[i] >> 16 & 0x7fffu);
+      mx = max(mx, max(lo < 0x7f80 ? lo : 0, hi < 0x7f80 ? hi : 0));
+    }
+  }
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  if ((threadIdx.x & 31) == 0) atomicMax(&s_max, mx);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    const int e = (s_max >> 7) - 126;  // |V| < 2^e
+    a.vexp[(static_cast<size_t>(b) * a.Hk + kh) * a.nb + g] =
+        s_max == 0 ? 0.f : static_cast<float>(max(e + (a.block == 128 ? 7 : 6) - 15, -100));
+  }
+}
+
 template <int D, int B>
 cudaError_t forward(const SelArgs& a, int first, int count, cudaStream_t st) {
   BlockMap mk, mv;
@@ -483,6 +507,12 @@ cudaError_t forward(const SelArgs& a, int first, int count, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t launch_value_exponents(const SelArgs& a, cudaStream_t st) {
+  const dim3 grid(a.nb, a.Hk, a.Bt);
+  a.d == 128 ? value_exponents_kernel<128><<<grid, 256, 0, st>>>(a) : value_exponents_kernel<64><<<grid, 256, 0, st>>>(a);
+  return counted(cudaGetLastError(), 1);
+}
 
 cudaError_t launch_join_half(const SelArgs& a, int first, int count, bool grad, cudaStream_t st) {
   const long long rows = static_cast<long long>(count) * a.slice * a.group;

@@ -175,7 +175,9 @@ __device__ __forceinline__ void share_of_tiles(const SelArgs& a, int first, int 
 }
 
 // The tiles from, from + step, .. of a CTA's share, in order (a stream's warps take every second
-// one); contiguous shares change K and V seldom.  The records of the next two are in flight.
+// one); contiguous shares change K and V seldom.  A record is read one tile ahead; what makes
+// that cheap is that another role (touch_ahead, or the loaders) has brought it to L1: a value
+// carried through the loop is waited for where it is moved, so reading further ahead gains nothing.
 // f(record, region of the chunk, tile, unit = run of tiles of one block, opens it, closes it);
 // the last three hold at step 1.
 template <typename F>
@@ -197,18 +199,35 @@ __device__ __forceinline__ bool each_tile(const SelArgs& a, int first, const int
     }
     return r;
   };
-  Rec now = fetch(from), next = fetch(from + step);
+  Rec now = fetch(from);
   int u = 0;
   bool opens = true;
   for (int t = from; t < tiles; t += step) {
-    const Rec ahead = fetch(t + 2 * step);
+    const Rec next = fetch(t + step);
     const bool closes = t + 1 == tiles || next.ci != now.ci || next.un.g != now.un.g;
     if (!f(now.un, now.ci, t, u, opens, closes)) return false;
     opens = closes;
     u += closes;
-    now = next, next = ahead;
+    now = next;
   }
   return true;
+}
+
+// Reads the records and list entries of the share's tiles into L1 ahead of the roles that work
+// from them; wait(t) holds it back.
+template <typename W>
+__device__ __forceinline__ void touch_ahead(const SelArgs& a, int first, const int* share, W wait) {
+  const int lane = threadIdx.x & 31;
+  const size_t cap = static_cast<size_t>(a.slice) * a.top;
+  each_tile(a, first, share, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
+    if (!wait(t)) return false;
+    const int e0 = un.r0 / a.group, e = e0 + 8 * lane;  // a sector of entries a lane
+    if (e <= (un.r0 + un.rows - 1) / a.group) {
+      int x;
+      asm volatile("ld.global.ca.b32 %0, [%1];" : "=r"(x) : "l"(a.list + (first + ci) * cap + un.off + e));
+    }
+    return true;
+  });
 }
 
 // Rows r and r + 8 of a tile, held by the quad's lanes as tmem_ld_16x64 leaves them (D / 2
@@ -246,6 +265,26 @@ __device__ __forceinline__ void store_part(const uint32_t (&o)[D / 2], const flo
       for (int j = 0; j < 8; ++j) {
         const __half2 v = __floats2half2_rn(__uint_as_float(o[c / 2 + 4 * j + 2 * k]) * g[k],
                                             __uint_as_float(o[c / 2 + 4 * j + 2 * k + 1]) * g[k]);
+        h[j] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      st_global_32(part + ((c / 64) * plane + out0 + r + 8 * k) * 128, h);
+    }
+  }
+}
+
+// The same without a scale: the values are inside fp16.
+template <int D>
+__device__ __forceinline__ void store_part_as_is(const uint32_t (&o)[D / 2], int r, int rows, uint8_t* part, long long plane,
+                                                 long long out0) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (r + 8 * k >= rows) continue;
+#pragma unroll
+    for (int c = 0; c < D; c += 64) {
+      uint32_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const __half2 v = __floats2half2_rn(__uint_as_float(o[c / 2 + 4 * j + 2 * k]), __uint_as_float(o[c / 2 + 4 * j + 2 * k + 1]));
         h[j] = *reinterpret_cast<const uint32_t*>(&v);
       }
       st_global_32(part + ((c / 64) * plane + out0 + r + 8 * k) * 128, h);
