@@ -331,34 +331,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- products
     constexpr uint32_t kIdS = tc::idesc_bf16(128, B, false, false), kIdQ = tc::idesc_bf16(128, D, false, true);
     constexpr uint32_t kIdAcc = tc::idesc_bf16(128, D == 128 ? B : 2 * B, true, true);
-    if (lane == 0) {
+    // the whole warp walks and waits, lane 0 issues
+    {
       const int tiles = s_first[2];
       auto issue_s = [&](int t) {  // once Q of the tile is there
-        if (!wait1(kQ + (t & 1), t >> 1)) return false;
+        if (!wait(kQ + (t & 1), t >> 1)) return false;
         tc::fence_after_sync();
         uint64_t dq = tc::sdesc_sw128(sQ(t & 1), 16, 1024), dk = tc::sdesc_sw128(sK, 16, 1024);
         keep_here(dq, dk);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          tc::mma_ss(tS, dq + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
+          if (lane == 0) tc::mma_ss(tS, dq + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
                      dk + ((kk >> 2) * (B * 128) + (kk & 3) * 32) / 16, kIdS, kk > 0 ? 1u : 0u);
         return true;
       };
-      if (tiles > 0 && wait1(kKv, 0) && issue_s(0))
+      if (tiles > 0 && wait(kKv, 0) && issue_s(0))
         each_tile(a, first, s_first, 0, 1, [&](const Unit&, int, int t, int u, bool opens, bool closes) {
           const int st = t & 1;
-          if (!wait1(kG, t)) return false;
-          if (t > 0 && !wait1(kDqFree, t - 1)) return false;  // dQ, over dP, is read
+          if (!wait(kG, t)) return false;
+          if (t > 0 && !wait(kDqFree, t - 1)) return false;  // dQ, over dP, is read
           tc::fence_after_sync();
           uint64_t dg = tc::sdesc_sw128(sG, 16, 1024), dv = tc::sdesc_sw128(sV, 16, 1024);
           keep_here(dg, dv);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            tc::mma_ss(tDp, dg + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
+            if (lane == 0) tc::mma_ss(tDp, dg + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
                        dv + ((kk >> 2) * (B * 128) + (kk & 3) * 32) / 16, kIdS, kk > 0 ? 1u : 0u);
-          tc::mma_commit(bar(kS));
-          if (!wait1(kP, t)) return false;
-          if (opens && u > 0 && !wait1(kAccFree, u - 1)) return false;
+          if (lane == 0) tc::mma_commit(bar(kS));
+          if (!wait(kP, t)) return false;
+          if (opens && u > 0 && !wait(kAccFree, u - 1)) return false;
           tc::fence_after_sync();
           // dV first, so that the next dO can be gathered, then dQ, so that its way out runs under dK
           // and the next S.  Contraction over the 128 rows: both operands rows apart, 64-column blocks of P and dS
@@ -368,35 +369,37 @@ __global__ void __launch_bounds__(kThreads, 1)
           keep_here(gt, pt);
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            tc::mma_ss(tAcc, gt + kk * (2048 / 16), pt + kk * (2048 / 16), kIdAcc, !opens || kk > 0 ? 1u : 0u);
-          tc::mma_commit(bar(kGFree));
-          if (D == 64) tc::mma_commit(bar(kQFree + st));
+            if (lane == 0) tc::mma_ss(tAcc, gt + kk * (2048 / 16), pt + kk * (2048 / 16), kIdAcc, !opens || kk > 0 ? 1u : 0u);
+          if (lane == 0) tc::mma_commit(bar(kGFree));
+          if (D == 64 && lane == 0) tc::mma_commit(bar(kQFree + st));
           uint64_t ds = tc::sdesc_sw128(sdS, 16, 1024), kt = tc::sdesc_sw128(sK, B * 128, 1024);
           keep_here(ds, kt);
 #pragma unroll
           for (int kk = 0; kk < B / 16; ++kk)
-            tc::mma_ss(tDp, ds + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16, kt + kk * (2048 / 16), kIdQ, kk > 0 ? 1u : 0u);
-          tc::mma_commit(bar(kDq));
+            if (lane == 0) tc::mma_ss(tDp, ds + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16, kt + kk * (2048 / 16), kIdQ, kk > 0 ? 1u : 0u);
+          if (lane == 0) tc::mma_commit(bar(kDq));
           if (D == 128) {
             uint64_t qt = tc::sdesc_sw128(sQ(st), 128 * 128, 1024), dt = tc::sdesc_sw128(sdS, 128 * 128, 1024);
             keep_here(qt, dt);
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
-              tc::mma_ss(tAcc + B, qt + kk * (2048 / 16), dt + kk * (2048 / 16), kIdAcc, !opens || kk > 0 ? 1u : 0u);
-            tc::mma_commit(bar(kQFree + st));
+              if (lane == 0) tc::mma_ss(tAcc + B, qt + kk * (2048 / 16), dt + kk * (2048 / 16), kIdAcc, !opens || kk > 0 ? 1u : 0u);
+            if (lane == 0) tc::mma_commit(bar(kQFree + st));
           }
           if (closes) {
-            tc::mma_commit(bar(kAcc));
-            tc::mma_commit(bar(kKvFree));
+            if (lane == 0) tc::mma_commit(bar(kAcc));
+            if (lane == 0) tc::mma_commit(bar(kKvFree));
           }
           // S of the next tile: the softmax has read this one's
-          if (t + 1 < tiles && ((closes && !wait1(kKv, u + 1)) || !issue_s(t + 1))) return false;
+          if (t + 1 < tiles && ((closes && !wait(kKv, u + 1)) || !issue_s(t + 1))) return false;
           return true;
         });
-      tc::mma_commit(bar(kDrain));  // every product has finished before TMEM goes back
-      tc::mbar_wait_quiet(bar(kDrain), 0);
+      if (lane == 0) {
+        tc::mma_commit(bar(kDrain));  // every product has finished before TMEM goes back
+        tc::mbar_wait_quiet(bar(kDrain), 0);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else if (warp == kKvWarp) {
     // ---------------------------------------------------------------- K and V of each block
     int issued = 0;

@@ -22,8 +22,7 @@
 //   warps 16-17  issue the products of one stream each: S of the stream's next tile as soon as
 //                the softmax has read the last one, O when P is written;
 //   warp 18      TMA boxes of the units' K and V, and zeros over V rows at or past the length
-//                (their P is 0, but 0 times what a cache holds there need not be);
-//   warp 19      reads the tiles' records and list entries into L1 ahead of the others.
+//                (their P is 0, but 0 times what a cache holds there need not be).
 // All waits are bounded; on a timeout every role leaves, products and copies in flight drained.
 #include <cuda.h>
 #include <cuda_fp16.h>
@@ -232,15 +231,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc::fence_proxy_async();
       tc::mbar_arrive(bar(kQ + tile % R));
     };
-    const bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
-      const __nv_bfloat16* q =
-          static_cast<const __nv_bfloat16*>(a.q.p) + un.b * a.q.sb + un.kh * a.group * a.q.sh + ch * 8;
-      const int r = 32 * lw + lane;  // this lane's row of the tile
-      long long off = -1;
-      if (r < un.rows) {
-        const int row = un.r0 + r, e = row / a.group;
-        off = a.list[(first + ci) * cap + un.off + e] * a.q.sn + (row - e * a.group) * a.q.sh;
-      }
+    // The copies of a tile are issued when the walk is at the next one, so that the list entry
+    // read here has arrived.
+    const __nv_bfloat16* q = nullptr;
+    int entry = -1, h = 0;
+    auto copy = [&](int t) {
+      const long long off = entry < 0 ? -1 : entry * a.q.sn + h * a.q.sh;
       if (t >= R && !wait(kFree + t % R, t / R - 1)) return false;
       const uint32_t sQ = sSlot + (t % R) * F::kSlot;
 #pragma unroll
@@ -255,10 +251,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         landed(t - 1);
       }
       return true;
+    };
+    bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
+      const int r = 32 * lw + lane, row = un.r0 + r, e = row / a.group;  // this lane's row of the tile
+      const int next = r < un.rows ? __ldg(a.list + (first + ci) * cap + un.off + e) : -1;
+      if (t > 0 && !copy(t - 1)) return false;
+      q = static_cast<const __nv_bfloat16*>(a.q.p) + un.b * a.q.sb + un.kh * a.group * a.q.sh + ch * 8;
+      entry = next, h = row - e * a.group;
+      return true;
     });
     const int tiles = s_first[2];
+    ok = ok && tiles > 0 && copy(tiles - 1);
     cp_async_wait<0>();
-    if (ok && tiles > 0) landed(tiles - 1);
+    if (ok) landed(tiles - 1);
   } else {
     tc::setmaxnreg_dec<kRegRest>();
   if (warp < kKvWarp) {
@@ -266,67 +271,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdS = tc::idesc_bf16(128, B, false, false), kIdO = tc::idesc_bf16(128, D, false, true);
     const int x = warp - kMmaWarp;
     const uint32_t tS = tbase + 128 * x, tO = tbase + 256 + 128 * x;
-    if (lane == 0) {
-      int held = -1;           // tile whose O is still to be issued, of the unit held_u
-      int held_u = 0;
-      bool held_last = false;  // ... and the stream's last of that unit
-      int of_unit = 0;         // the stream's tiles of the current unit
-      auto issue_s = [&](int tile) {
-        uint64_t dq = tc::sdesc_sw128(sSlot + (tile % R) * F::kSlot, 16, 1024), dk = tc::sdesc_sw128(sK, 16, 1024);
-        keep_here(dq, dk);
+    // the whole warp walks and waits, lane 0 issues
+    int held = -1;           // tile whose O is still to be issued, of the unit held_u
+    int held_u = 0;
+    bool held_last = false;  // ... and the stream's last of that unit
+    int of_unit = 0;         // the stream's tiles of the current unit
+    auto issue_s = [&](int tile) {
+      uint64_t dq = tc::sdesc_sw128(sSlot + (tile % R) * F::kSlot, 16, 1024), dk = tc::sdesc_sw128(sK, 16, 1024);
+      keep_here(dq, dk);
+      if (lane == 0) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           tc::mma_ss(tS, dq + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16,
                      dk + ((kk >> 2) * (B * 128) + (kk & 3) * 32) / 16, kIdS, kk > 0 ? 1u : 0u);
         tc::mma_commit(bar(kS + x));
-      };
-      auto issue_o = [&]() {  // of the held tile, whose P is written
-        if (!wait1(kV, held_u)) return false;
-        if (held > 1 && !wait1(kOFree + x, (held >> 1) - 1)) return false;
-        tc::fence_after_sync();
-        uint64_t dp = tc::sdesc_sw128(sSlot + (held % R) * F::kSlot, 16, 1024), dv = tc::sdesc_sw128(sV, B * 128, 1024);
-        keep_here(dp, dv);
+      }
+      __syncwarp();
+    };
+    auto issue_o = [&]() {  // of the held tile, whose P is written
+      if (!wait(kV, held_u)) return false;
+      if (held > 1 && !wait(kOFree + x, (held >> 1) - 1)) return false;
+      tc::fence_after_sync();
+      uint64_t dp = tc::sdesc_sw128(sSlot + (held % R) * F::kSlot, 16, 1024), dv = tc::sdesc_sw128(sV, B * 128, 1024);
+      keep_here(dp, dv);
+      if (lane == 0) {
 #pragma unroll
         for (int kk = 0; kk < B / 16; ++kk)
           tc::mma_ss(tO, dp + ((kk >> 2) * (128 * 128) + (kk & 3) * 32) / 16, dv + kk * (2048 / 16), kIdO, kk > 0 ? 1u : 0u);
         tc::mma_commit(bar(kO + x));
         tc::mma_commit(bar(kFree + held % R));
         if (held_last) tc::mma_commit(bar(kVFree));
-        held = -1;
-        return true;
-      };
-      auto flush = [&]() { return held < 0 || (wait1(kP + x, held >> 1) && issue_o()); };
-      const bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit&, int, int t, int u, bool opens, bool closes) {
-        if (opens) of_unit = 0;
-        if ((t & 1) == x) {
-          if (held >= 0) {
-            if (!wait1(kP + x, held >> 1)) return false;  // P written, S read
-            tc::fence_after_sync();
-            // S first where its operands are there, so that the softmax goes on at once
-            if (!(bar_done(bar(kK), u & 1) && bar_done(bar(kQ + t % R), (t / R) & 1)) && !issue_o()) return false;
-          }
-          if (!wait1(kK, u) || !wait1(kQ + t % R, t / R)) return false;
+      }
+      __syncwarp();
+      held = -1;
+      return true;
+    };
+    auto flush = [&]() { return held < 0 || (wait(kP + x, held >> 1) && issue_o()); };
+    const bool ok = each_tile(a, first, s_first, 0, 1, [&](const Unit&, int, int t, int u, bool opens, bool closes) {
+      if (opens) of_unit = 0;
+      if ((t & 1) == x) {
+        if (held >= 0) {
+          if (!wait(kP + x, held >> 1)) return false;  // P written, S read
           tc::fence_after_sync();
-          issue_s(t);
-          if (held >= 0 && !issue_o()) return false;
-          held = t, held_u = u, held_last = false;
-          ++of_unit;
+          // S first where its operands are there, so that the softmax goes on at once
+          const bool there = bar_done(bar(kK), u & 1) && bar_done(bar(kQ + t % R), (t / R) & 1);
+          if (!__all_sync(0xffffffffu, there) && !issue_o()) return false;
         }
-        if (!closes) return true;
-        // this stream's share of the unit's releases: K behind its last S, V behind its last O.
-        // Without a tile in the unit, once the unit before is released (two arrivals of one
-        // stream in a phase would stand for the other stream's).
-        if (of_unit > 0) {
-          tc::mma_commit(bar(kKFree));
-          held_last = true;
-        } else {
-          if (!flush() || !wait1(kK, u) || !wait1(kV, u)) return false;
+        if (!wait(kK, u) || !wait(kQ + t % R, t / R)) return false;
+        tc::fence_after_sync();
+        issue_s(t);
+        if (held >= 0 && !issue_o()) return false;
+        held = t, held_u = u, held_last = false;
+        ++of_unit;
+      }
+      if (!closes) return true;
+      // this stream's share of the unit's releases: K behind its last S, V behind its last O.
+      // Without a tile in the unit, once the unit before is released (two arrivals of one
+      // stream in a phase would stand for the other stream's).
+      if (of_unit > 0) {
+        if (lane == 0) tc::mma_commit(bar(kKFree));
+        __syncwarp();
+        held_last = true;
+      } else {
+        if (!flush() || !wait(kK, u) || !wait(kV, u)) return false;
+        if (lane == 0) {
           tc::mbar_arrive(bar(kKFree));
           tc::mbar_arrive(bar(kVFree));
         }
-        return true;
-      });
-      if (ok) flush();
+        __syncwarp();
+      }
+      return true;
+    });
+    if (ok) flush();
+    if (lane == 0) {
       tc::mma_commit(bar(kDrain + x));  // every product has finished before TMEM goes back
       tc::mbar_wait_quiet(bar(kDrain + x), 0);
     }
@@ -364,11 +381,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (issued % 2 == 0) tc::mbar_wait_quiet(bar(kVLand), (issued / 2 - 1) & 1);
     }
     __syncwarp();
-  } else {
-    // ---------------------------------------------------------------- records and lists into L1
-    // up to two rings ahead of the slots' release (a wait may match a later phase of the same
-    // parity: it then holds on for that one)
-    touch_ahead(a, first, s_first, [&](int t) { return t < 3 * R || wait(kFree + t % R, t / R - 3); });
   }
   }
   tc::fence_before_sync();

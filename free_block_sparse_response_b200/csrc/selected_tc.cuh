@@ -175,59 +175,43 @@ __device__ __forceinline__ void share_of_tiles(const SelArgs& a, int first, int 
 }
 
 // The tiles from, from + step, .. of a CTA's share, in order (a stream's warps take every second
-// one); contiguous shares change K and V seldom.  A record is read one tile ahead; what makes
-// that cheap is that another role (touch_ahead, or the loaders) has brought it to L1: a value
-// carried through the loop is waited for where it is moved, so reading further ahead gains nothing.
+// one); contiguous shares change K and V seldom.  Called by whole warps: the lanes read the records
+// of the next 32 tiles at once and hand them out by shuffles.  (One record a tile read ahead in
+// registers costs its full latency, ~700 cycles, at the move that carries it through the loop.)
 // f(record, region of the chunk, tile, unit = run of tiles of one block, opens it, closes it);
 // the last three hold at step 1.
 template <typename F>
 __device__ __forceinline__ bool each_tile(const SelArgs& a, int first, const int* share, int from, int step, F f) {
-  int ci = share[0], idx = share[1] + from;
-  const int tiles = share[2];
-  int n = tiles > 0 ? __ldg(a.n_units + first + ci) : 0;
-  struct Rec {
-    Unit un;
-    int ci;
-  };
-  auto fetch = [&](int t) {  // record of tile t, called in order
-    Rec r{};
-    if (t < tiles) {
-      while (idx >= n) idx -= n, n = __ldg(a.n_units + first + ++ci);
-      r.un = a.units[static_cast<size_t>(first + ci) * a.unit_cap + idx];
-      r.ci = ci;
-      idx += step;
-    }
-    return r;
-  };
-  Rec now = fetch(from);
-  int u = 0;
+  const int lane = threadIdx.x & 31, tiles = share[2];
+  int base_ci = share[0], base_idx = share[1], base_t = 0;  // a known place: tile base_t
+  Unit rec{};
+  int rec_ci = 0, u = 0;
+  unsigned ends = 0;
   bool opens = true;
-  for (int t = from; t < tiles; t += step) {
-    const Rec next = fetch(t + step);
-    const bool closes = t + 1 == tiles || next.ci != now.ci || next.un.g != now.un.g;
-    if (!f(now.un, now.ci, t, u, opens, closes)) return false;
+  for (int i = 0, t = from; t < tiles; ++i, t += step) {
+    if ((i & 31) == 0) {
+      const int mine = min(t + lane * step, tiles - 1);
+      int ci = base_ci, idx = base_idx + mine - base_t, n;
+      while (idx >= (n = __ldg(a.n_units + first + ci))) idx -= n, ++ci;
+      const Unit* at = a.units + static_cast<size_t>(first + ci) * a.unit_cap + idx;
+      rec = *at;
+      rec_ci = ci;
+      const bool end = mine + 1 == tiles || idx + 1 == n || at[1].g != rec.g;
+      ends = __ballot_sync(0xffffffffu, end);
+      base_ci = __shfl_sync(0xffffffffu, ci, 0), base_idx = __shfl_sync(0xffffffffu, idx, 0), base_t = t;
+    }
+    const int src = i & 31;
+    auto get = [&](int x) { return __shfl_sync(0xffffffffu, x, src); };
+    Unit un;
+    un.g = get(rec.g), un.off = get(rec.off), un.r0 = get(rec.r0), un.rows = get(rec.rows), un.live = get(rec.live);
+    un.qs = get(rec.qs), un.b = get(rec.b), un.kh = get(rec.kh), un.total = get(rec.total);
+    un.k = __int_as_float(get(__float_as_int(rec.k)));
+    const bool closes = (ends >> src) & 1u;
+    if (!f(un, get(rec_ci), t, u, opens, closes)) return false;
     opens = closes;
     u += closes;
-    now = next;
   }
   return true;
-}
-
-// Reads the records and list entries of the share's tiles into L1 ahead of the roles that work
-// from them; wait(t) holds it back.
-template <typename W>
-__device__ __forceinline__ void touch_ahead(const SelArgs& a, int first, const int* share, W wait) {
-  const int lane = threadIdx.x & 31;
-  const size_t cap = static_cast<size_t>(a.slice) * a.top;
-  each_tile(a, first, share, 0, 1, [&](const Unit& un, int ci, int t, int, bool, bool) {
-    if (!wait(t)) return false;
-    const int e0 = un.r0 / a.group, e = e0 + 8 * lane;  // a sector of entries a lane
-    if (e <= (un.r0 + un.rows - 1) / a.group) {
-      int x;
-      asm volatile("ld.global.ca.b32 %0, [%1];" : "=r"(x) : "l"(a.list + (first + ci) * cap + un.off + e));
-    }
-    return true;
-  });
 }
 
 // Rows r and r + 8 of a tile, held by the quad's lanes as tmem_ld_16x64 leaves them (D / 2
