@@ -440,7 +440,7 @@ template <typename T, int D>
 cudaError_t select_blocks(const SelArgs& a, int* sel, cudaStream_t st) {
   if (a.n <= 8) return row_select<T, D>(a, sel, nullptr, st);
   constexpr size_t kMost = 227 * 1024;
-  if (tile_smem<D, 64>(a.nb) <= kMost) {
+  if (a.nb <= 640 && tile_smem<D, 64>(a.nb) <= kMost) {
     if (a.nb <= 128) return tile_select<T, D, 64, 4>(a, sel, st);
     return a.nb <= 256 ? tile_select<T, D, 64, 8>(a, sel, st) : tile_select<T, D, 64, 20>(a, sel, st);
   }

@@ -405,3 +405,169 @@ def test_sparsepr_attention_with_rotary_positions():
     assert torch.equal(got, spr.attention(qr, kr, v, cfg))
     assert torch.equal(got, spr.attention_call(q, k, v, cfg, rotary=(plan, pos)))
     assert torch.equal(q, keep)
+
+
+# ------------------------------------------------------------------- sizes where paths change
+
+WIDE = [
+    # rows of more than 32 slots, groups past one 16-row step, every block selected
+    (1, 2, 1, 300, 4096, 64, 64, 40, False, 0, 0, None, BF),
+    (2, 24, 1, 1, 900, 128, 64, 9, True, 1, 1, (900, 77), BF),
+    (1, 40, 2, 2, 2600, 64, 64, 41, True, 2, 3, None, BF),
+    (1, 3, 1, 40, 500, 128, 128, 100, False, 0, 0, (450,), F),
+    (1, 2, 2, 1, 260, 128, 64, 70, True, 0, 1, None, F),
+    (4, 2, 1, 140, 140, 64, 128, 1, True, 0, 1, (1, 0, 140, 129), BF),
+]
+
+
+@pytest.mark.parametrize("shape", WIDE, ids=lambda s: "-".join(str(x) for x in s[:9]))
+def test_wide_rows_and_groups(shape):
+    test_selection_and_attention_match_the_definitions(shape, False)
+    test_backward_matches_the_formula(shape)
+
+
+@pytest.mark.parametrize("nb,d,n", [(130, 128, 70), (300, 64, 65), (600, 128, 33), (700, 64, 40), (1500, 128, 17), (2048, 64, 20),
+                                    (2048, 128, 3)])
+def test_selection_over_many_blocks(nb, d, n):
+    """The tile heights and key registers of the selection, causal and forced blocks among them."""
+    gen = gen_of(nb + d)
+    bt, hq, hk, top = 1, 4, 2, 11
+    q, mean = rnd(gen, bt, hq, n, d), rnd(gen, bt, hk, nb, d, dtype=F)
+    mean[:, :, 5] = mean[:, :, 3]
+    keys = nb * 64 - 13
+    lens = torch.tensor([keys - 200], dtype=torch.int32, device=DEV)
+    for causal, first, local in ((False, 1, 0), (True, 2, 2)):
+        cfg = spr.SelectConfig(block=64, top=top, causal=causal, n_first=first, n_local=local)
+        start = torch.tensor([keys // 2 if causal else 0], dtype=torch.int32, device=DEV)
+        k = torch.zeros(1, 1, 1, d, dtype=BF, device=DEV).expand(bt, hk, keys, d)
+        ws = spr.selected_workspace(q, k, cfg)
+        sel = spr.select_blocks(q, mean, keys, cfg, ws, kv_len=lens, q_start=start)
+        spr.check(ws)
+        assert torch.equal(sel, R.select(q, mean, keys, 64, top, lens, start, causal, first, local))
+
+
+def test_rows_that_leave_many_blocks_open_are_decided_exactly():
+    """Equal scores far past 32 blocks (zero queries, equal means) among ordinary rows."""
+    gen = gen_of(41)
+    n, nb, d, top = 200, 150, 64, 20
+    q, mean = rnd(gen, 1, 2, n, d), rnd(gen, 1, 1, nb, d, dtype=F)
+    q[:, :, 7::9] = 0
+    mean[:, :, 40:110] = mean[:, :, 40:41]
+    cfg = spr.SelectConfig(block=64, top=top)
+    ws = spr.selected_workspace(q, torch.zeros(1, 1, nb * 64, d, dtype=BF, device=DEV), cfg)
+    lens = torch.tensor([nb * 64], device=DEV)
+    for _ in range(2):  # the list of left-over rows starts empty in every call
+        sel = spr.select_blocks(q, mean, nb * 64, cfg, ws)
+        assert torch.equal(sel, R.select(q, mean, nb * 64, 64, top, lens, torch.zeros_like(lens), False, 0, 0))
+    spr.check(ws)
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-4, 3e4, 1e30])
+def test_values_of_any_size(size):
+    """Parts travel in 16 bits: values far outside that range, and blocks of very different sizes."""
+    q, k, v, lens, starts, cfg = problem((1, 2, 2, 200, 640, 128, 64, 4, False, 0, 0, None, BF), 42)
+    v = (v.float() * size).to(BF)
+    v[:, :, 64:128] = (v[:, :, 64:128].float() * 1e-5).to(BF)
+    ws = spr.selected_workspace(q, k, cfg)
+    sel = spr.select_blocks(q, spr.key_means(k, 64), 640, cfg, ws)
+    out, _ = spr.selected_attn(q, k, v, sel, cfg, ws)
+    ok = R.mask(sel, 200, 640, 64, lens, starts, False)
+    want, _, p = R.attention(q, k, v, ok, 128 ** -0.5)
+    close(out, want, U[BF] * want.abs() + (U[BF] + E) * (p @ v.double().abs()) + 1e-38, "out")
+
+
+def test_an_infinite_value_reaches_its_queries_and_columns_only():
+    q, k, v, lens, starts, cfg = problem((1, 1, 1, 130, 256, 128, 64, 2, False, 0, 0, None, BF), 43)
+    v[0, 0, 70, 5] = math.inf   # block 1
+    sel = torch.tensor([0, 3], dtype=torch.int32, device=DEV).expand(1, 1, 130, 2).contiguous()
+    sel[:, :, ::3] = torch.tensor([1, 2], dtype=torch.int32, device=DEV)
+    ws = spr.selected_workspace(q, k, cfg)
+    out, _ = spr.selected_attn(q, k, v, sel, cfg, ws)
+    bad = ~torch.isfinite(out[0, 0])
+    want = torch.zeros_like(bad)
+    want[::3, 5] = True
+    assert torch.equal(bad, want)
+    clean = v.clone()
+    clean[0, 0, 70, 5] = 0
+    ref, _ = spr.selected_attn(q, k, clean, sel, cfg, ws)
+    assert torch.equal(out[0, 0][~bad], ref[0, 0][~bad])
+
+
+def test_repeated_heads_and_batches_by_stride_zero():
+    """K and V expanded over heads and batch (one cache read by all)."""
+    gen = gen_of(44)
+    q = rnd(gen, 2, 4, 150, 64)
+    k, v = (rnd(gen, 1, 1, 300, 64).expand(2, 2, 300, 64) for _ in range(2))
+    cfg = spr.SelectConfig(block=64, top=3)
+    a = spr.block_attention(q, k, v, cfg)
+    assert torch.equal(a, spr.block_attention(q, k.contiguous(), v.contiguous(), cfg))
+    one = spr.block_attention(q[:, :, :1], k, v, cfg)
+    assert torch.equal(one, spr.block_attention(q[:, :, :1], k.contiguous(), v.contiguous(), cfg))
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Overlapping calls with workspaces of their own give what they give alone."""
+    cases = [problem((1, 8, 2, 3000, 3000, 128, 64, 8, True, 1, 1, None, BF), s) for s in (45, 46)]
+    dout = [rnd(gen_of(47 + i), *c[0].shape) for i, c in enumerate(cases)]
+
+    def step(i, ws):
+        q, k, v, lens, starts, cfg = cases[i]
+        sel = spr.select_blocks(q, spr.key_means(k, 64), 3000, cfg, ws, q_start=starts)
+        out, lse = spr.selected_attn(q, k, v, sel, cfg, ws, q_start=starts)
+        return (sel, out, lse) + spr.selected_attn_backward(dout[i], q, k, v, out, lse, sel, cfg, ws, q_start=starts)
+
+    wss = [spr.selected_workspace(c[0], c[1], c[5], backward=True) for c in cases]
+    alone = [[t.clone() for t in step(i, wss[i])] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(3):
+        got = []
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append(step(i, wss[i]))
+        torch.cuda.synchronize()
+    for i in range(2):
+        spr.check(wss[i])
+        for a, b in zip(alone[i], got[i]):
+            assert torch.equal(a, b)
+
+
+def test_refusals_on_the_gpu():
+    q = rnd(gen_of(50), 1, 2, 40, 64)
+    k = rnd(gen_of(51), 1, 2, 200, 64)
+    cfg = spr.SelectConfig(block=64, top=2)
+    ws = spr.selected_workspace(q, k, cfg)
+    mean = spr.key_means(k, 64)
+    sel = spr.select_blocks(q, mean, 200, cfg, ws)
+    with pytest.raises(ValueError):
+        spr.selected_attn(q, k, k[:, :, :100], sel, cfg, ws)
+    with pytest.raises(ValueError):
+        spr.selected_attn(q, k, k, sel.long(), cfg, ws)
+    with pytest.raises(ValueError):
+        spr.selected_attn(q, k, k.float(), sel, cfg, ws)
+    with pytest.raises(ValueError):
+        spr.selected_attn(q, k, k, sel, cfg, ws[:256])
+    with pytest.raises(ValueError):
+        spr.selected_attn(q, k, k, sel, cfg, ws, out=q[:, :, :1].expand(1, 2, 40, 64))
+    with pytest.raises(ValueError):
+        spr.select_blocks(q, mean, 400, cfg, ws)
+    with pytest.raises(ValueError):
+        spr.selected_attn(q, k, k, sel, cfg, ws, kv_len=torch.tensor([200], device=DEV))
+    with pytest.raises(ValueError):
+        spr.key_means(k, 64, kv_start=torch.zeros(1, dtype=torch.int32, device=DEV))
+    with pytest.raises(spr.SparsePRError):
+        spr.key_means(k, 32)
+    with pytest.raises(spr.SparsePRError):
+        spr.selected_workspace(q, k, spr.SelectConfig(block=64, top=0))
+    with pytest.raises(spr.SparsePRError):
+        wide = rnd(gen_of(52), 1, 2, 40, 65)
+        spr.key_means(wide[..., 1:], 64)
+    plan = spr.rotary_plan(64, DEV)
+    with pytest.raises(ValueError):
+        spr.rotary(plan, torch.zeros(1, 40, 1, device=DEV), q)
+    with pytest.raises(ValueError):
+        spr.rotary(plan, torch.zeros(1, 39, dtype=torch.int32, device=DEV), q)
+    with pytest.raises(ValueError):
+        spr.rotary(spr.rotary_plan(128, DEV), torch.zeros(1, 40, dtype=torch.int32, device=DEV), q)
+    spr.check(ws)
