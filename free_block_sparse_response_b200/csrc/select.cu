@@ -8,15 +8,17 @@
 //      x = hi + lo + r, |lo| <= 2^-9 |x| and |r| <= 2^-18 |x|, the products hi hi + hi lo + lo hi
 //      leave out at most 3 * 2^-18 sum |q||m|, and eight chained fp32 accumulations add at most
 //      2^-18 of it: |s~ - s| <= e = 2^-16 |q| max |m_g| (Cauchy-Schwarz; for a group, |q| is the
-//      norm of the sum of magnitudes, which also covers the fp32 sum over the heads).
+//      norm of the sum of magnitudes, which also covers the fp32 sum over the heads).  Single
+//      bf16 queries have no lo part: two products, 2 * 2^-18, e = 2^-17 |q| max |m_g|.
 //   2. The k-th and (k+1)-th largest s~, a and b.  Scores above b + 2e are in and scores below
 //      a - 2e are out whatever the rounding; with a - b > 2e nothing is left between.
 //   3. The few blocks between are compared by their scores in 64 bits.
 //
 // Rows that leave more than 32 blocks open (equal keys, zero or non-finite queries) go to a
 // list that select_row_kernel works off, one CTA a row, all scores in 64 bits; it also takes
-// the calls of a few tokens, where there is no tile to fill.  A tile's time goes to the
-// selection of step 2 (a warp per row over shared memory), then to the products.
+// the calls of a few rows.  Bound by instructions: of 327 us for 2 x 8 key heads x 16,383 tokens in
+// groups of 4, 128 blocks, step 2 takes 185 (halving the range of the scores 52), the sums of the
+// group, the splits into parts and the products 142; the bytes would take 55.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -175,7 +177,7 @@ size_t tile_smem(int nb) {
 }
 
 // VPL: a lane's scores of a row in registers (32 VPL blocks and more), 0: read from shared memory.
-template <typename T, int D, int ROWS, int VPL>
+template <typename T, int D, int ROWS, int VPL, bool QLO>
 __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs a, int* __restrict__ sel, int* __restrict__ list) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kTileQ = ROWS * D * 2, kTileM = kChunk * D * 2;
@@ -256,7 +258,7 @@ __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs
       for (int s = 0; s < 2; ++s) {
         const uint32_t at = swz<D>(rg * 16 + (lane & 15), (2 * k2 + s) * 2 + (lane >> 4));
         ldmatrix_x4(ah[s], sqh + at);
-        ldmatrix_x4(al[s], sql + at);
+        if (QLO) ldmatrix_x4(al[s], sql + at);
       }
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
@@ -268,7 +270,7 @@ __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs
         for (int s = 0; s < 2; ++s) {
           mma_bf16_16816(hh[n], ah[s], bh + 2 * s);
           mma_bf16_16816(rest[n], ah[s], bl + 2 * s);
-          mma_bf16_16816(rest[n], al[s], bh + 2 * s);
+          if (QLO) mma_bf16_16816(rest[n], al[s], bh + 2 * s);
         }
       }
     }
@@ -287,7 +289,7 @@ __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs
     int* out = sel + w * a.top;
     const Scope sc = scope_of(a, b, t0 + r);
     const float* sr = score + static_cast<size_t>(r) * ld;
-    const float e2 = 2.f * 0x1p-16f * qn[r] * mnorm;  // 2e
+    const float e2 = (QLO ? 0x1p-15f : 0x1p-16f) * qn[r] * mnorm;  // 2e
     int forced = 0;
     if (sc.cand > 0) {
       const int f0 = min(a.n_first, sc.cand);  // [0, f0) and [l0, l1)
@@ -302,48 +304,69 @@ __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs
     unsigned chosen = 0;
     bool slow = split && !(e2 < 0x1p100f);  // not finite
     if (split && !slow) {
-      // order keys of the blocks to choose from (0: not one), in registers where they fit
-      auto key_of = [&](int g) {
-        return g < sc.cand && !is_forced(a, sc, g) ? float_order_key(sr[g]) : 0u;
-      };
-      uint32_t key[VPL > 0 ? VPL : 1];
+      // the scores to choose from (-inf: not one; the finite bound above rules out others), in
+      // registers where they fit
+      auto score_of = [&](int g) { return g < sc.cand && !is_forced(a, sc, g) ? sr[g] : -__builtin_huge_valf(); };
+      float val[VPL > 0 ? VPL : 1];
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) key[i] = key_of(32 * i + lane);
-      auto each_key = [&](auto f) {
+      for (int i = 0; i < VPL; ++i) val[i] = score_of(32 * i + lane);
+      auto each_score = [&](auto f) {
         if (VPL > 0) {
 #pragma unroll
-          for (int i = 0; i < VPL; ++i) f(key[i]);
+          for (int i = 0; i < VPL; ++i) f(val[i]);
         } else {
-          for (int g = lane; g < sc.cand; g += 32) f(key_of(g));
+          for (int g = lane; g < sc.cand; g += 32) f(score_of(g));
         }
       };
-      // the bits that all of them share need no search
-      uint32_t kmin = 0xffffffffu, kmax = 0;
-      each_key([&](uint32_t k) {
-        kmax = max(kmax, k);
-        kmin = min(kmin, k > 0 ? k : 0xffffffffu);
-      });
-      kmin = __reduce_min_sync(0xffffffffu, kmin), kmax = __reduce_max_sync(0xffffffffu, kmax);
-      const int top_bit = kmin == kmax ? -1 : 31 - __clz(kmin ^ kmax);
-      uint32_t v = top_bit < 0 ? kmin : kmin & ~((2u << top_bit) - 1u);
-      int have = pool;
-      for (int bit = top_bit; bit >= 0 && have != want; --bit) {
-        const uint32_t tryv = v | (1u << bit);
+      auto count = [&](float v) {
         int c = 0;
-        each_key([&](uint32_t k) { c += k >= tryv; });
-        c = __reduce_add_sync(0xffffffffu, c);
-        if (c >= want) v = tryv, have = c;
+        each_score([&](float x) { c += x >= v; });
+        return __reduce_add_sync(0xffffffffu, c);
+      };
+      auto least = [&](float x) { return float_from_order_key(__reduce_min_sync(0xffffffffu, float_order_key(x))); };
+      auto most = [&](float x) { return float_from_order_key(__reduce_max_sync(0xffffffffu, float_order_key(x))); };
+      // Halving the range of the values finds a threshold between the want-th and the next one in
+      // about log2(range / gap) steps (seven for 16 of 128 normal scores; over the keys' bits the
+      // sign and exponent alone take nine).
+      float vlo = __builtin_huge_valf(), vhi = -__builtin_huge_valf();
+      each_score([&](float x) {
+        vhi = fmaxf(vhi, x);
+        vlo = fminf(vlo, x == -__builtin_huge_valf() ? vlo : x);
+      });
+      vlo = least(vlo), vhi = most(vhi);
+      float v = vlo;
+      int have = pool;  // scores >= v
+      for (int step = 0; step < 24 && have != want; ++step) {
+        const float mid = 0.5f * vlo + 0.5f * vhi;
+        if (!(mid > vlo && mid < vhi)) break;
+        const int c = count(mid);
+        if (c >= want)
+          v = vlo = mid, have = c;
+        else
+          vhi = mid;
+      }
+      if (have != want) {  // (nearly) equal scores: the exact one by its bits
+        uint32_t bits = 0;
+        have = pool;
+        for (int bit = 31; bit >= 0 && have != want; --bit) {
+          const uint32_t next = bits | (1u << bit);
+          int c = 0;
+          each_score([&](float x) { c += x > -__builtin_huge_valf() && float_order_key(x) >= next; });
+          c = __reduce_add_sync(0xffffffffu, c);
+          if (c >= want) bits = next, have = c;
+        }
+        v = float_from_order_key(bits);
       }
       // the want-th largest, and the one after it
-      uint32_t ka = 0xffffffffu, kb = 0;
-      each_key([&](uint32_t k) {
-        if (k >= v && k > 0)
-          ka = min(ka, k);
+      float fa = __builtin_huge_valf(), fb = -__builtin_huge_valf();
+      each_score([&](float x) {
+        if (x >= v)
+          fa = fminf(fa, x);
         else
-          kb = max(kb, k);
+          fb = fmaxf(fb, x);
       });
-      const float fa = float_from_order_key(__reduce_min_sync(0xffffffffu, ka));
-      const float fb = have > want ? fa : float_from_order_key(__reduce_max_sync(0xffffffffu, kb));
+      fa = least(fa);
+      fb = have > want ? fa : most(fb);
       if (fa - fb > e2) {
         hi = fb;
       } else {
@@ -420,25 +443,32 @@ cudaError_t row_select(const SelArgs& a, int* sel, const int* list, cudaStream_t
   return counted(cudaGetLastError(), 1);
 }
 
-template <typename T, int D, int ROWS, int VPL>
+template <typename T, int D, int ROWS, int VPL, bool QLO>
 cudaError_t tile_select(const SelArgs& a, int* sel, cudaStream_t st) {
   cudaError_t e = cudaMemsetAsync(a.slow, 0, sizeof(int), st);
   if (e != cudaSuccess) return e;
   const size_t smem = tile_smem<D, ROWS>(a.nb);
-  e = cudaFuncSetAttribute(select_tile_kernel<T, D, ROWS, VPL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem));
+  auto kern = select_tile_kernel<T, D, ROWS, VPL, QLO>;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  select_tile_kernel<T, D, ROWS, VPL><<<dim3(ceil_div(a.n, ROWS), a.Bt * a.Hk), kTileThreads, smem, st>>>(a, sel, a.slow + 1);
+  kern<<<dim3(ceil_div(a.n, ROWS), a.Bt * a.Hk), kTileThreads, smem, st>>>(a, sel, a.slow + 1);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
   return row_select<T, D>(a, sel, a.slow + 1, st);
 }
 
-// Up to eight tokens a head leave a tile of 16 half empty: one CTA a row.  Otherwise the tallest
-// tile whose scores fit in shared memory (a mean is read once per tile); a row's keys stay in
-// registers up to 640 blocks (20 a lane).
+template <typename T, int D, int ROWS, int VPL>
+cudaError_t tile_select(const SelArgs& a, int* sel, cudaStream_t st) {
+  if (sizeof(T) == 2 && a.group == 1) return tile_select<T, D, ROWS, VPL, sizeof(T) != 2>(a, sel, st);
+  return tile_select<T, D, ROWS, VPL, true>(a, sel, st);
+}
+
+// Few rows: a CTA each.  Otherwise tiles, the tallest whose scores fit in shared memory (a mean is
+// read once per tile); a row's scores stay in registers up to 640 blocks (20 a lane).  Measured,
+// row and tile kernels in us: 512 rows of 64 blocks, groups of 4, 13 and 21, 1,024 rows 21 and 21;
+// 512 rows, single heads, 10.6 and 10.6, 1,024 rows 17 and 14; 256 rows of 512 blocks 23 and 43.
 template <typename T, int D>
 cudaError_t select_blocks(const SelArgs& a, int* sel, cudaStream_t st) {
-  if (a.n <= 8) return row_select<T, D>(a, sel, nullptr, st);
+  if (static_cast<long long>(a.Bt) * a.Hk * a.n <= 4 * 148) return row_select<T, D>(a, sel, nullptr, st);
   constexpr size_t kMost = 227 * 1024;
   if (a.nb <= 640 && tile_smem<D, 64>(a.nb) <= kMost) {
     if (a.nb <= 128) return tile_select<T, D, 64, 4>(a, sel, st);

@@ -26,52 +26,62 @@ constexpr int kWords = kSub / 32;
 // The valid entries of the sub-slice's rows: ascending, in [0, nb), up to the first negative
 // one.  An entry out of range or not above all earlier ones is reported and skipped; a block with
 // no key that the token may attend to is skipped (f gets -1).  The lanes of a warp take the slots
-// of one or more rows (a power of two of at least 4 lanes a row), a prefix maximum over them
-// finds the entries that ascend.
+// of one or more rows (a power of two of at least 4 lanes a row).  Rows that only ascend need one
+// comparison with the neighbour; a prefix maximum sorts out the others.  Bound by instructions.
 template <typename F>
 __device__ __forceinline__ void each_selected(const SelArgs& a, int z, int t0, F f) {
   const int b = z / a.Hk, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   int width = 4;
   while (width < 32 && width < a.top) width *= 2;
   const int per = 32 / width, slot = lane & (width - 1), sub = lane / width;
-  const int len = kv_len_of(a, b), qs = q_start_of(a, b);
+  const int len = kv_len_of(a, b), qs = q_start_of(a, b), shift = a.block == 128 ? 7 : 6;
+  const int* row0 = a.sel + static_cast<size_t>(z) * a.n * a.top;
+  const int rows = min(kSub, a.n - t0);
   bool bad = false;
   // the first chunk of a row is read one step ahead
   auto entry = [&](int i, int j) {
-    const int t = t0 + i;
-    return i < kSub && t < a.n && j < a.top ? __ldg(a.sel + (static_cast<size_t>(z) * a.n + t) * a.top + j) : -1;
+    return i < rows && j < a.top ? __ldg(row0 + static_cast<size_t>(t0 + i) * a.top + j) : -1;
   };
   int ahead = entry(warp * per + sub, slot);
-  for (int i0 = warp * per; i0 < kSub && t0 + i0 < a.n; i0 += warps * per) {
-    const int i = i0 + sub, t = t0 + i;
-    const bool live = t < a.n;
+  for (int i0 = warp * per; i0 < rows; i0 += warps * per) {
+    const int i = i0 + sub;
     const int head = ahead;
     ahead = entry(i + warps * per, slot);
-    // last block that holds a key the token may attend to (-1: none)
-    int last = a.causal ? min(len - 1, qs + t) : len - 1;
-    last = last < 0 ? -1 : last / a.block;
-    const size_t row = (static_cast<size_t>(z) * a.n + t) * a.top;
-    int above = -1;  // largest valid-range entry of the slots before this chunk
+    // last block that holds a key the token may attend to (negative: none)
+    const int last = (a.causal ? min(len - 1, qs + t0 + i) : len - 1) >> shift;
+    int above = -1;  // largest entry of the chunks before
     bool ended = false;
     for (int j0 = 0; j0 < a.top; j0 += width) {
       const int j = j0 + slot;
       const int g = j0 == 0 ? head : entry(i, j);
-      // entries from the row's first negative one on do not count
-      const unsigned neg = __ballot_sync(0xffffffffu, g < 0) >> (sub * width);
-      const unsigned before = width == 32 ? (slot == 31 ? 0x7fffffffu : (1u << slot) - 1u) : (1u << slot) - 1u;
-      const bool past = ended || g < 0 || (neg & before) != 0;
-      const int v = past || g >= a.nb ? -1 : g;
-      int mx = v;  // inclusive prefix maximum over the row's lanes
-      for (int o = 1; o < width; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, mx, o, width);
-        if (slot >= o) mx = max(mx, y);
+      int prev = __shfl_up_sync(0xffffffffu, g, 1, width);
+      if (slot == 0) prev = ended ? -1 : above;
+      bool take = g >= 0;
+      const bool plain = g < 0 || (g < a.nb && g > prev && (prev >= 0 || (j == 0)));
+      if (__all_sync(0xffffffffu, plain)) {
+        if (j0 + width < a.top) {
+          const int end = __shfl_sync(0xffffffffu, g, width - 1, width);
+          above = max(above, end);
+          ended = end < 0;
+        }
+      } else {
+        // entries from the row's first negative one on do not count
+        const unsigned neg = __ballot_sync(0xffffffffu, g < 0) >> (sub * width);
+        const bool past = ended || g < 0 || (neg & ((1u << slot) - 1u)) != 0;
+        const int v = past || g >= a.nb ? -1 : g;
+        int mx = v;  // inclusive prefix maximum over the row's lanes
+        for (int o = 1; o < width; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, mx, o, width);
+          if (slot >= o) mx = max(mx, y);
+        }
+        const int y = __shfl_up_sync(0xffffffffu, mx, 1, width);
+        prev = max(above, slot > 0 ? y : -1);
+        if (!past && (g >= a.nb || g <= prev)) bad = true;
+        take = v >= 0 && v > prev;
+        above = max(above, __shfl_sync(0xffffffffu, mx, width - 1, width));
+        ended = ended || (neg & (width == 32 ? 0xffffffffu : (1u << width) - 1u)) != 0;
       }
-      int prev = __shfl_up_sync(0xffffffffu, mx, 1, width);
-      prev = max(above, slot > 0 ? prev : -1);
-      if (!past && (g >= a.nb || g <= prev)) bad = true;
-      if (live && j < a.top) f(i, row + j, v >= 0 && v > prev && v <= last ? v : -1);
-      above = max(above, __shfl_sync(0xffffffffu, mx, width - 1, width));
-      ended = ended || (neg & (width == 32 ? 0xffffffffu : (1u << width) - 1u)) != 0;
+      if (i < rows && j < a.top) f(i, (static_cast<size_t>(z) * a.n + t0 + i) * a.top + j, take && g <= last ? g : -1);
     }
   }
   if (bad) record_error(a.status, kErrInvalidArg);

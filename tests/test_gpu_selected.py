@@ -167,7 +167,7 @@ def test_selection_breaks_ties_to_the_lower_block():
 
 def test_near_ties_are_decided_in_64_bits():
     """Blocks whose means differ in the last bits of 32-bit sums."""
-    n, d, nb, top = 400, 128, 96, 7
+    n, d, nb, top = 700, 128, 96, 7
     gen = gen_of(4)
     base = rnd(gen, 1, 1, 1, d, dtype=F)
     mean = base + 1e-6 * rnd(gen, 1, 1, nb, d, dtype=F)
@@ -426,12 +426,12 @@ def test_wide_rows_and_groups(shape):
     test_backward_matches_the_formula(shape)
 
 
-@pytest.mark.parametrize("nb,d,n", [(130, 128, 70), (300, 64, 65), (600, 128, 33), (700, 64, 40), (1500, 128, 17), (2048, 64, 20),
-                                    (2048, 128, 3)])
+@pytest.mark.parametrize("nb,d,n", [(130, 128, 70), (130, 128, 333), (300, 64, 300), (600, 128, 297), (700, 64, 299), (1500, 128, 301),
+                                    (2048, 64, 300), (2048, 128, 3)])
 def test_selection_over_many_blocks(nb, d, n):
     """The tile heights and key registers of the selection, causal and forced blocks among them."""
     gen = gen_of(nb + d)
-    bt, hq, hk, top = 1, 4, 2, 11
+    bt, hq, hk, top = 1, 4, 2, 11  # (up to 592 rows go to the row kernel: both kernels below)
     q, mean = rnd(gen, bt, hq, n, d), rnd(gen, bt, hk, nb, d, dtype=F)
     mean[:, :, 5] = mean[:, :, 3]
     keys = nb * 64 - 13
@@ -449,7 +449,7 @@ def test_selection_over_many_blocks(nb, d, n):
 def test_rows_that_leave_many_blocks_open_are_decided_exactly():
     """Equal scores far past 32 blocks (zero queries, equal means) among ordinary rows."""
     gen = gen_of(41)
-    n, nb, d, top = 200, 150, 64, 20
+    n, nb, d, top = 700, 150, 64, 20
     q, mean = rnd(gen, 1, 2, n, d), rnd(gen, 1, 1, nb, d, dtype=F)
     q[:, :, 7::9] = 0
     mean[:, :, 40:110] = mean[:, :, 40:41]
