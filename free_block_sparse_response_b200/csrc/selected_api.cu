@@ -37,6 +37,19 @@ int check_view(const sparsepr_view* v, int elem, bool aligned) {
   return SPARSEPR_OK;
 }
 
+// No two rows of an output in one place.
+int check_output(const sparsepr_view* v, int32_t Bt, int32_t H, int32_t N) {
+  if ((Bt > 1 && v->stride_b == 0) || (H > 1 && v->stride_h == 0) || (N > 1 && v->stride_n == 0))
+    return bad("an output must not repeat rows (stride 0)");
+  return SPARSEPR_OK;
+}
+
+// Key rows that repeat have no box in a tensor map (repeated heads and batch elements have).
+int check_keys(const sparsepr_view* v, int32_t Nk) {
+  if (Nk > 1 && v->stride_n == 0) return bad("the rows of K and V must not repeat (stride_n 0)");
+  return SPARSEPR_OK;
+}
+
 View view(const sparsepr_view* v) { return View{v->data, v->stride_b, v->stride_h, v->stride_n}; }
 
 int check_problem(const sparsepr_selected* p) {
@@ -197,6 +210,7 @@ int sparsepr_rotary(const sparsepr_rotary_params* p, const double* freqs, const 
   int rc;
   if ((rc = check_view(X1, elem, false)) || (rc = check_view(Y1, elem, false))) return rc;
   if (H2 > 0 && ((rc = check_view(X2, elem, false)) || (rc = check_view(Y2, elem, false)))) return rc;
+  if ((rc = check_output(Y1, Bt, H1, N)) || (H2 > 0 && (rc = check_output(Y2, Bt, H2, N)))) return rc;
   auto same = [](const sparsepr_view* x, const sparsepr_view* y) {
     return x->data != y->data || (x->stride_b == y->stride_b && x->stride_h == y->stride_h && x->stride_n == y->stride_n);
   };
@@ -256,6 +270,7 @@ int sparsepr_selected_attn(const sparsepr_selected* p, const sparsepr_view* Q, c
   const int elem = p->dtype == SPARSEPR_F32 ? 4 : 2;
   for (const sparsepr_view* v : {Q, K, V, O})
     if ((rc = check_view(v, elem, true))) return rc;
+  if ((rc = check_keys(K, p->Nk)) || (rc = check_keys(V, p->Nk)) || (rc = check_output(O, p->Bt, p->Hq, p->Nq))) return rc;
   if (sel == nullptr || lse == nullptr || ws == nullptr) return bad("null pointer argument");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   SelArgs a = base_args(p);
@@ -283,6 +298,9 @@ int sparsepr_selected_attn_backward(const sparsepr_selected* p, const sparsepr_v
   const int elem = p->dtype == SPARSEPR_F32 ? 4 : 2;
   for (const sparsepr_view* v : {dO, Q, K, V, O, dQ, dK, dV})
     if ((rc = check_view(v, elem, true))) return rc;
+  if ((rc = check_keys(K, p->Nk)) || (rc = check_keys(V, p->Nk)) || (rc = check_output(dQ, p->Bt, p->Hq, p->Nq)) ||
+      (rc = check_output(dK, p->Bt, p->Hkv, p->Nk)) || (rc = check_output(dV, p->Bt, p->Hkv, p->Nk)))
+    return rc;
   if (sel == nullptr || lse == nullptr || ws == nullptr) return bad("null pointer argument");
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   SelArgs a = base_args(p);

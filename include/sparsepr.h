@@ -323,7 +323,7 @@ SPARSEPR_API int sparsepr_apply_residual(const float* S_out, const float* M, con
  * sparsepr_reset_workspace. */
 typedef struct sparsepr_view {
   void* data;                          /* device */
-  int64_t stride_b, stride_h, stride_n; /* elements; 0 repeats (inputs only) */
+  int64_t stride_b, stride_h, stride_n; /* elements; 0 repeats (inputs only; K and V rows may not) */
 } sparsepr_view;
 
 /* Layout of a pair in the R = rot_dim rotated dims: HALF pairs dim i with i + R/2,

@@ -505,6 +505,22 @@ def test_repeated_heads_and_batches_by_stride_zero():
     assert torch.equal(one, spr.block_attention(q[:, :, :1], k.contiguous(), v.contiguous(), cfg))
 
 
+def test_token_slices_of_a_large_call():
+    """A head whose partial rows pass the workspace's chunk is worked off slice by slice: the same as
+    calls on parts of the tokens."""
+    gen = gen_of(60)
+    n, keys, grp, top, d = 33000, 4096, 16, 16, 64
+    q, k, v = rnd(gen, 1, grp, n, d), rnd(gen, 1, 1, keys, d), rnd(gen, 1, 1, keys, d)
+    cfg = spr.SelectConfig(block=64, top=top)
+    ws = spr.selected_workspace(q, k, cfg)
+    sel = spr.select_blocks(q, spr.key_means(k, 64), keys, cfg, ws)
+    out, lse = spr.selected_attn(q, k, v, sel, cfg, ws)
+    spr.check(ws)
+    for a, b in ((0, 1000), (1000, 20000), (20000, n)):
+        o, l = spr.selected_attn(q[:, :, a:b], k, v, sel[:, :, a:b].contiguous(), cfg, ws)
+        assert torch.equal(o, out[:, :, a:b]) and torch.equal(l, lse[:, :, a:b])
+
+
 def test_two_calls_at_once_on_two_streams():
     """Overlapping calls with workspaces of their own give what they give alone."""
     cases = [problem((1, 8, 2, 3000, 3000, 128, 64, 8, True, 1, 1, None, BF), s) for s in (45, 46)]

@@ -84,11 +84,24 @@ def test_null_and_misaligned_tensors_are_refused(L):
     assert L.sparsepr_selected_attn(p, ok, ok, ok, FAKE, ok, FAKE, None, None) == spr.ERR_INVALID_ARG
 
 
+def test_rows_that_repeat_are_refused_where_they_cannot_be(L):
+    p, ok, flat = problem(Bt=2, Nq=10, Nk=300), view(b=1 << 20, h=1 << 16), view(b=1 << 20, h=1 << 16, n=0)
+    one = view(b=0, h=1 << 16)
+    for bad in ((ok, flat, ok, ok), (ok, ok, flat, ok), (ok, ok, ok, flat), (ok, ok, ok, one)):
+        assert L.sparsepr_selected_attn(p, bad[0], bad[1], bad[2], FAKE, bad[3], FAKE, FAKE, None) == spr.ERR_INVALID_ARG
+        assert b"repeat" in L.sparsepr_last_error()
+    for at in (5, 6, 7):
+        vs = [one if i == at else ok for i in range(8)]
+        assert L.sparsepr_selected_attn_backward(p, *vs[:5], FAKE, FAKE, *vs[5:], FAKE, None) == spr.ERR_INVALID_ARG
+        assert b"repeat" in L.sparsepr_last_error()
+    assert rotary_rc(L, y=view(data=8192, h=128, n=0)) == spr.ERR_INVALID_ARG
+
+
 def rotary_rc(L, par=None, x=None, y=None, x2=None, y2=None, h2=0, d=128, h1=2, dtype=spr.BF16, **kw):
     base = dict(rot_dim=64, first=0, layout=0, axes=1, pairs=(ctypes.c_int32 * 4)(32, 0, 0, 0), inverse=0, factor=1.0)
     base.update(kw)
-    return L.sparsepr_rotary(ctypes.byref(S._CRotary(**base)), FAKE, FAKE, 0, 1, dtype, 1, 10, d, h1, x or view(),
-                             y or view(data=8192), h2, x2, y2, None)
+    return L.sparsepr_rotary(ctypes.byref(S._CRotary(**base)), FAKE, FAKE, 0, 1, dtype, 1, 10, d, h1, x or view(h=2048),
+                             y or view(data=8192, h=2048), h2, x2, y2, None)
 
 
 @pytest.mark.parametrize("kw", [dict(rot_dim=0), dict(rot_dim=63), dict(rot_dim=130), dict(first=65), dict(first=-1),
@@ -101,7 +114,7 @@ def test_rotary_refuses_bad_arguments(L, kw):
 
 
 def test_rotary_in_place_needs_the_same_strides(L):
-    assert rotary_rc(L, x=view(n=128), y=view(n=256)) == spr.ERR_INVALID_ARG
+    assert rotary_rc(L, x=view(h=4096, n=128), y=view(h=4096, n=256)) == spr.ERR_INVALID_ARG
     assert b"in place" in L.sparsepr_last_error()
 
 
