@@ -28,6 +28,7 @@ import ctypes
 import dataclasses
 import functools
 import math
+import threading
 from typing import NamedTuple, Optional, Sequence
 
 import torch
@@ -69,13 +70,13 @@ def signatures():
     }
 
 
-def _view(t: Optional[torch.Tensor]):
+def _view(t: Optional[torch.Tensor]) -> _CView:
     if t is None:
-        return None
+        return _CView(None, 0, 0, 0)
     n0, n1, n2, _ = t.shape
     s0, s1, s2, _ = t.stride()
     # a dimension of one row has no stride to speak of
-    return ctypes.byref(_CView(t.data_ptr(), s0 if n0 > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0))
+    return _CView(t.data_ptr(), s0 if n0 > 1 else 0, s1 if n1 > 1 else 0, s2 if n2 > 1 else 0)
 
 
 def _need_rows(name: str, t: torch.Tensor, shape=None, like: Optional[torch.Tensor] = None) -> None:
@@ -113,13 +114,46 @@ def _rows_like(t: torch.Tensor) -> torch.Tensor:
     return torch.empty(t.shape, dtype=t.dtype, device=t.device) if _expanded(t) else torch.empty_like(t)
 
 
-def _run(device, name: str, *args) -> None:
-    stream = torch._C._cuda_getCurrentRawStream(device.index)
-    if device.index == torch.cuda.current_device():
-        _s._call(name, *args, stream)
-    else:
-        with torch.cuda.device(device):
-            _s._call(name, *args, stream)
+class _Call:
+    """An entry point with its arguments checked and marshalled for one signature (shapes,
+    strides, types, devices, options): a call fills in the pointers.  Kept per thread, because
+    the structures are filled in place; nothing in it depends on an address or a value."""
+
+    def __init__(self, name: str, device: torch.device):
+        self.fn, self.name, self.device, self.index = getattr(_s.lib(), name), name, device, device.index
+
+    def run(self, *args) -> None:
+        stream = torch._C._cuda_getCurrentRawStream(self.index)
+        if self.index == torch.cuda.current_device():
+            rc = self.fn(*args, stream)
+        else:
+            with torch.cuda.device(self.index):
+                rc = self.fn(*args, stream)
+        if rc != _s.OK:
+            raise _s.SparsePRError(rc, f"{self.name}: {_s.lib().sparsepr_last_error().decode(errors='replace')}")
+
+
+_CALLS = threading.local()
+
+
+def _signature(*tensors):
+    return tuple([None if t is None else (t.shape, t.stride(), t.dtype, t.get_device()) for t in tensors])
+
+
+def _prepared(key, make, *args):
+    """The call of this signature, checked by ``make`` the first time."""
+    calls = _CALLS.__dict__.setdefault("calls", {})
+    call = calls.get(key)
+    if call is None:
+        call = make(*args)
+        if len(calls) >= 512:
+            calls.clear()
+        calls[key] = call
+    return call
+
+
+def _ptr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 # ------------------------------------------------------------------------------ rotary
@@ -204,7 +238,19 @@ def rotary(plan: RotaryPlan, positions: torch.Tensor, q: torch.Tensor, k: Option
     dimension contiguous.  ``inverse`` rotates back: the gradient of the rotation (the factor
     is applied in both directions).  ``out``: the output tensor or pair, which may be the input
     itself or a strided view such as the new rows of a key cache."""
-    outs = (None, None) if out is None else tuple(out) if k is not None else (out, None)
+    qo, ko = (None, None) if out is None else tuple(out) if k is not None else (out, None)
+    key = ("rotary", plan[1:], plan.freqs.get_device(), bool(inverse), _signature(positions, q, k, qo, ko))
+    c = _prepared(key, _rotary_call, plan, positions, q, k, inverse, qo, ko)
+    qo = _rows_like(q) if qo is None else qo
+    if k is not None:
+        ko = _rows_like(k) if ko is None else ko
+        c.k.data, c.ko.data = k.data_ptr(), ko.data_ptr()
+    c.q.data, c.qo.data = q.data_ptr(), qo.data_ptr()
+    c.run(c.par_ref, plan.freqs.data_ptr(), positions.data_ptr(), *c.sizes, c.q_ref, c.qo_ref, c.h2, c.k_ref, c.ko_ref)
+    return qo if k is None else (qo, ko)
+
+
+def _rotary_call(plan, positions, q, k, inverse, qo, ko) -> _Call:
     for name, t in (("q", q), ("k", k)):
         if t is not None:
             _need_rows(name, t, (q.shape[0], t.shape[1], q.shape[2], q.shape[3]), q)
@@ -212,27 +258,25 @@ def rotary(plan: RotaryPlan, positions: torch.Tensor, q: torch.Tensor, k: Option
     if d != plan.d or plan.freqs.device != q.device:
         raise ValueError("the plan was made for another head dim or device")
     axes = len(plan.sections)
-    if positions.dim() == 2 and axes == 1:
-        positions = positions[..., None]
-    if positions.dtype != torch.int32 or positions.device != q.device or positions.dim() != 3 or \
-            positions.shape[0] not in (1, bt) or tuple(positions.shape[1:]) != (n, axes) or \
-            (axes > 1 and positions.stride(2) != 1):
+    at = positions[..., None] if positions.dim() == 2 and axes == 1 else positions
+    if at.dtype != torch.int32 or at.device != q.device or at.dim() != 3 or at.shape[0] not in (1, bt) or \
+            tuple(at.shape[1:]) != (n, axes) or (axes > 1 and at.stride(2) != 1):
         raise ValueError(f"positions must be int32 [{bt} or 1, {n}, {axes}] on the tensors' device")
-    res = []
-    for name, t, o in (("out of q", q, outs[0]), ("out of k", k, outs[1])):
-        if t is None:
-            res.append(None)
-            continue
-        o = _rows_like(t) if o is None else o
-        _need_rows(name, o, t.shape, t)
-        _need_out(name, o)
-        res.append(o)
+    for name, t, o in (("out of q", q, qo), ("out of k", k, ko)):
+        if t is not None and o is not None:
+            _need_rows(name, o, t.shape, t)
+            _need_out(name, o)
+    c = _Call("sparsepr_rotary", q.device)
     pairs = (ctypes.c_int32 * 4)(*(plan.sections + (0,) * (4 - axes)))
-    par = _CRotary(plan.rot_dim, plan.first, plan.layout, axes, pairs, 1 if inverse else 0, plan.factor)
-    _run(q.device, "sparsepr_rotary", ctypes.byref(par), _s._p(plan.freqs), _s._p(positions),
-         positions.stride(0) if positions.shape[0] > 1 else 0, positions.stride(1), _s._dtype_code(q), bt, n, d, h, _view(q),
-         _view(res[0]), 0 if k is None else k.shape[1], _view(k), _view(res[1]))
-    return res[0] if k is None else (res[0], res[1])
+    c.par = _CRotary(plan.rot_dim, plan.first, plan.layout, axes, pairs, 1 if inverse else 0, plan.factor)
+    c.q, c.k = _view(q), _view(k)
+    # outputs that the call makes have the strides of _rows_like
+    c.qo = _view(_rows_like(q) if qo is None else qo)
+    c.ko = _view(None if k is None else _rows_like(k) if ko is None else ko)
+    c.par_ref, c.q_ref, c.k_ref, c.qo_ref, c.ko_ref = (ctypes.byref(x) for x in (c.par, c.q, c.k, c.qo, c.ko))
+    c.h2 = 0 if k is None else k.shape[1]
+    c.sizes = (at.stride(0) if at.shape[0] > 1 else 0, at.stride(1), _s._dtype_code(q), bt, n, d, h)
+    return c
 
 
 # ------------------------------------------------------------- attention over selected blocks
@@ -250,10 +294,9 @@ class SelectConfig:
     scale: float = 0.0
 
 
-def _problem(dtype_of, bt, hq, hk, nq, nk, d, cfg: SelectConfig, kv_len, q_start) -> _CSelected:
+def _problem(dtype_of, bt, hq, hk, nq, nk, d, cfg: SelectConfig) -> _CSelected:
     return _CSelected(_s._dtype_code(dtype_of), bt, hq, hk, nq, nk, d, cfg.block, cfg.top, int(bool(cfg.causal)),
-                      cfg.n_first, cfg.n_local, cfg.scale, None if kv_len is None else kv_len.data_ptr(),
-                      None if q_start is None else q_start.data_ptr())
+                      cfg.n_first, cfg.n_local, cfg.scale, None, None)
 
 
 def _lengths(bt: int, device, kv_len, q_start) -> None:
@@ -265,7 +308,7 @@ def selected_workspace(q: torch.Tensor, k: torch.Tensor, cfg: SelectConfig, back
     """Workspace of the calls below for tensors of these shapes (status header zeroed)."""
     _need_rows("q", q)
     _need_rows("k", k, (q.shape[0], k.shape[1], k.shape[2], q.shape[3]), q)
-    p = _problem(q, q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3], cfg, None, None)
+    p = _problem(q, q.shape[0], q.shape[1], k.shape[1], q.shape[2], k.shape[2], q.shape[3], cfg)
     size = int(_s.lib().sparsepr_selected_workspace_size(ctypes.byref(p), 1 if backward else 0))
     if size == 0:
         raise _s.SparsePRError(_s.ERR_INVALID_ARG,
@@ -285,9 +328,13 @@ def _ws_size(dtype, bt, hq, hk, nq, nk, d, cfg: SelectConfig, backward: bool) ->
 
 def _need_ws(ws: torch.Tensor, p: _CSelected, cfg: SelectConfig, device, backward: bool) -> None:
     size = _ws_size(p.dtype, p.Bt, p.Hq, p.Hkv, p.Nq, p.Nk, p.d, cfg, backward)
-    if size and (ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < size or
-                 ws.data_ptr() % 256):
-        raise ValueError("the workspace is too small for these tensors, misaligned or on another device")
+    if size and (ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.numel() < size):
+        raise ValueError("the workspace is too small for these tensors or on another device")
+
+
+def _need_aligned(ws: torch.Tensor) -> None:
+    if ws.data_ptr() & 255:
+        raise ValueError("the workspace must start on a 256-byte boundary")
 
 
 def key_means(k: torch.Tensor, block: int, kv_len: Optional[torch.Tensor] = None,
@@ -295,17 +342,25 @@ def key_means(k: torch.Tensor, block: int, kv_len: Optional[torch.Tensor] = None
     """Mean key of every block of ``block`` keys: [batch, heads, ceil(rows / block), d] fp32.
     With ``kv_start`` [batch] int32 only the blocks holding keys [kv_start, kv_len) are renewed
     in ``out`` (at most ``max_new`` keys per sequence were appended)."""
+    c = _prepared(("means", block, _signature(k, kv_len, kv_start, out)), _means_call, k, block, kv_len, kv_start, out)
+    means = torch.empty(c.shape, dtype=torch.float32, device=k.device) if out is None else out
+    c.k.data, c.p.kv_len = k.data_ptr(), _ptr(kv_len)
+    c.run(c.p_ref, c.k_ref, _ptr(kv_start), max_new, means.data_ptr())
+    return means
+
+
+def _means_call(k, block, kv_len, kv_start, out) -> _Call:
     _need_rows("k", k)
     bt, h, n, d = k.shape
     _lengths(bt, k.device, kv_len, kv_start)
     if kv_start is not None and out is None:
         raise ValueError("kv_start renews blocks of an existing tensor: give out")
-    shape = (bt, h, -(-n // block) if block > 0 else 0, d)
-    means = torch.empty(shape, dtype=torch.float32, device=k.device) if out is None else out
-    _need_flat("out", means, shape, torch.float32, k.device)
-    p = _problem(k, bt, h, h, 1, n, d, SelectConfig(block=block, top=1), kv_len, None)
-    _run(k.device, "sparsepr_key_means", ctypes.byref(p), _view(k), _s._p(kv_start), max_new, _s._p(means))
-    return means
+    c = _Call("sparsepr_key_means", k.device)
+    c.shape = (bt, h, -(-n // block) if block > 0 else 0, d)
+    _need_flat("out", out, c.shape, torch.float32, k.device)
+    c.p, c.k = _problem(k, bt, h, h, 1, n, d, SelectConfig(block=block, top=1)), _view(k)
+    c.p_ref, c.k_ref = ctypes.byref(c.p), ctypes.byref(c.k)
+    return c
 
 
 def select_blocks(q: torch.Tensor, means: torch.Tensor, keys: int, cfg: SelectConfig, ws: torch.Tensor,
@@ -313,29 +368,58 @@ def select_blocks(q: torch.Tensor, means: torch.Tensor, keys: int, cfg: SelectCo
                   out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Blocks of the ``keys`` keys that each query attends to: [batch, key heads, rows, top]
     int32, ascending, then -1 (ties to the lower block; the scores are compared in 64 bits)."""
+    key = ("select", keys, cfg, ws.numel(), _signature(q, means, ws, kv_len, q_start, out))
+    c = _prepared(key, _select_call, q, means, keys, cfg, ws, kv_len, q_start, out)
+    _need_aligned(ws)
+    sel = torch.empty(c.shape, dtype=torch.int32, device=q.device) if out is None else out
+    c.q.data, c.p.kv_len, c.p.q_start = q.data_ptr(), _ptr(kv_len), _ptr(q_start)
+    c.run(c.p_ref, c.q_ref, means.data_ptr(), sel.data_ptr(), ws.data_ptr())
+    return sel
+
+
+def _select_call(q, means, keys, cfg, ws, kv_len, q_start, out) -> _Call:
     _need_rows("q", q)
     bt, hq, n, d = q.shape
     hk = means.shape[1] if means.dim() == 4 else 0
     _need_flat("means", means, (bt, hk, -(-keys // cfg.block) if cfg.block > 0 else 0, d), torch.float32, q.device)
     _lengths(bt, q.device, kv_len, q_start)
-    p = _problem(q, bt, hq, hk, n, keys, d, cfg, kv_len, q_start)
-    _need_ws(ws, p, cfg, q.device, False)
-    sel = torch.empty(bt, hk, n, cfg.top, dtype=torch.int32, device=q.device) if out is None else out
-    _need_flat("out", sel, (bt, hk, n, cfg.top), torch.int32, q.device)
-    _run(q.device, "sparsepr_select_blocks", ctypes.byref(p), _view(q), _s._p(means), _s._p(sel), _s._p(ws))
-    return sel
+    c = _Call("sparsepr_select_blocks", q.device)
+    c.p, c.q, c.shape = _problem(q, bt, hq, hk, n, keys, d, cfg), _view(q), (bt, hk, n, cfg.top)
+    _need_ws(ws, c.p, cfg, q.device, False)
+    _need_flat("out", out, c.shape, torch.int32, q.device)
+    c.p_ref, c.q_ref = ctypes.byref(c.p), ctypes.byref(c.q)
+    return c
 
 
-def _attention_problem(q, k, v, sel, cfg, ws, kv_len, q_start, backward) -> _CSelected:
+def _attention_call(name, backward, cfg, ws, sel, kv_len, q_start, lse, q, k, v, others) -> _Call:
+    """Checks of both attention calls; ``others``: (name, tensor or None where the call makes it,
+    the tensor whose shape it has, whether it is an output)."""
     _need_rows("q", q)
     bt, hq, n, d = q.shape
     _need_rows("k", k, (bt, k.shape[1], k.shape[2], d), q)
     _need_rows("v", v, k.shape, q)
     _need_flat("sel", sel, (bt, k.shape[1], n, cfg.top), torch.int32, q.device)
+    _need_flat("lse", lse, q.shape[:3], torch.float32, q.device)
     _lengths(bt, q.device, kv_len, q_start)
-    p = _problem(q, bt, hq, k.shape[1], n, k.shape[2], d, cfg, kv_len, q_start)
-    _need_ws(ws, p, cfg, q.device, backward)
-    return p
+    c = _Call(name, q.device)
+    c.p = _problem(q, bt, hq, k.shape[1], n, k.shape[2], d, cfg)
+    _need_ws(ws, c.p, cfg, q.device, backward)
+    c.views = [_view(q), _view(k), _view(v)]
+    for what, t, like, is_out in others:
+        if t is not None:
+            _need_rows(what, t, like.shape, q)
+            if is_out:
+                _need_out(what, t)
+        c.views.append(_view(_rows_like(like) if t is None else t))
+    c.refs = [ctypes.byref(x) for x in c.views]
+    c.p_ref, c.lse_shape = ctypes.byref(c.p), q.shape[:3]
+    return c
+
+
+def _fill(c: _Call, kv_len, q_start, *tensors) -> None:
+    c.p.kv_len, c.p.q_start = _ptr(kv_len), _ptr(q_start)
+    for view, t in zip(c.views, tensors):
+        view.data = t.data_ptr()
 
 
 def selected_attn(q, k, v, sel: torch.Tensor, cfg: SelectConfig, ws: torch.Tensor,
@@ -343,35 +427,39 @@ def selected_attn(q, k, v, sel: torch.Tensor, cfg: SelectConfig, ws: torch.Tenso
                   out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
     """Softmax attention of every query over the keys of its selected blocks: (out, lse), out
     like q and lse [batch, heads, rows] fp32 (natural log; -inf and a zero row without keys)."""
-    p = _attention_problem(q, k, v, sel, cfg, ws, kv_len, q_start, False)
-    o = _rows_like(q) if out is None else out
-    _need_rows("out", o, q.shape, q)
-    _need_out("out", o)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device) if lse is None else lse
-    _need_flat("lse", lse, q.shape[:3], torch.float32, q.device)
-    _run(q.device, "sparsepr_selected_attn", ctypes.byref(p), _view(q), _view(k), _view(v), _s._p(sel), _view(o), _s._p(lse),
-         _s._p(ws))
-    return o, lse
+    key = ("attn", cfg, _signature(q, k, v, sel, ws, kv_len, q_start, out, lse))
+    c = _prepared(key, _attention_call, "sparsepr_selected_attn", False, cfg, ws, sel, kv_len, q_start, lse, q, k, v,
+                  (("out", out, q, True),))
+    _need_aligned(ws)
+    out = _rows_like(q) if out is None else out
+    lse = torch.empty(c.lse_shape, dtype=torch.float32, device=q.device) if lse is None else lse
+    _fill(c, kv_len, q_start, q, k, v, out)
+    r = c.refs
+    c.run(c.p_ref, r[0], r[1], r[2], sel.data_ptr(), r[3], lse.data_ptr(), ws.data_ptr())
+    return out, lse
 
 
 def selected_attn_backward(dout, q, k, v, out, lse, sel: torch.Tensor, cfg: SelectConfig, ws: torch.Tensor,
                            kv_len: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None, dq=None,
                            dk=None, dv=None):
     """(dq, dk, dv) of ``selected_attn`` for the gradient of its output; the selection is fixed.
-    ``ws`` was made with ``backward=True``."""
-    p = _attention_problem(q, k, v, sel, cfg, ws, kv_len, q_start, True)
-    _need_rows("dout", dout, q.shape, q)
-    _need_rows("out", out, q.shape, q)
-    _need_flat("lse", lse, q.shape[:3], torch.float32, q.device)
-    res = []
-    for name, g, t in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        g = _rows_like(t) if g is None else g
-        _need_rows(name, g, t.shape, q)
-        _need_out(name, g)
-        res.append(g)
-    _run(q.device, "sparsepr_selected_attn_backward", ctypes.byref(p), _view(dout), _view(q), _view(k), _view(v), _view(out),
-         _s._p(lse), _s._p(sel), *(_view(g) for g in res), _s._p(ws))
-    return tuple(res)
+    ``ws`` was made with ``backward=True``.  An expanded k or v gets the gradient of every repeated
+    head (add them up); the heads of a group are added already.  The row sums of dout * out are
+    formed from ``out`` as it is stored, so bf16 gradients carry its rounding."""
+    if lse is None:
+        raise ValueError("lse of the forward call is needed")
+    key = ("grad", cfg, _signature(dout, q, k, v, out, lse, sel, ws, kv_len, q_start, dq, dk, dv))
+    c = _prepared(key, _attention_call, "sparsepr_selected_attn_backward", True, cfg, ws, sel, kv_len, q_start, lse, q, k, v,
+                  (("dout", dout, q, False), ("out", out, q, False), ("dq", dq, q, True), ("dk", dk, k, True),
+                   ("dv", dv, k, True)))
+    _need_aligned(ws)
+    dq = _rows_like(q) if dq is None else dq
+    dk = _rows_like(k) if dk is None else dk
+    dv = _rows_like(k) if dv is None else dv
+    _fill(c, kv_len, q_start, q, k, v, dout, out, dq, dk, dv)
+    r = c.refs
+    c.run(c.p_ref, r[3], r[0], r[1], r[2], r[4], lse.data_ptr(), sel.data_ptr(), r[5], r[6], r[7], ws.data_ptr())
+    return dq, dk, dv
 
 
 def block_attention(q, k, v, cfg: SelectConfig, ws: Optional[torch.Tensor] = None,
