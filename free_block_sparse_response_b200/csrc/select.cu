@@ -302,7 +302,8 @@ __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs
     // scores above hi are in, scores in [lo, hi] open; bit j of `chosen`: the j-th open block is in
     float lo = __builtin_huge_valf(), hi = __builtin_huge_valf();
     unsigned chosen = 0;
-    bool slow = split && !(e2 < 0x1p100f);  // not finite
+    // the bound holds where nothing in it or in the products overflows or drops out of the normal range
+    bool slow = split && !(e2 < 0x1p100f && qn[r] > 0x1p-60f && mnorm > 0x1p-60f && e2 > 0x1p-90f);
     if (split && !slow) {
       // the scores to choose from (-inf: not one; the finite bound above rules out others), in
       // registers where they fit

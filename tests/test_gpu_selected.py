@@ -180,6 +180,21 @@ def test_near_ties_are_decided_in_64_bits():
     assert torch.equal(sel, R.select(q, mean, nb * 64, 64, top, lens, torch.zeros_like(lens), False, 0, 0))
 
 
+@pytest.mark.parametrize("qs,ms,group", [(1e-23, 1.0, 1), (1.0, 1e-23, 1), (1e-30, 1e-18, 2), (1e-22, 1e22, 4), (1e30, 1e-30, 2)])
+def test_near_ties_of_very_small_and_large_values(qs, ms, group):
+    """Sizes whose squares leave the range of 32 bits."""
+    n, d, nb, top = 700, 128, 96, 7
+    gen = gen_of(61)
+    mean = (rnd(gen, 1, 1, 1, d, dtype=F) + 1e-6 * rnd(gen, 1, 1, nb, d, dtype=F)) * ms
+    q = (rnd(gen, 1, group, n, d).float() * qs).to(BF)
+    cfg = spr.SelectConfig(block=64, top=top)
+    ws = spr.selected_workspace(q, torch.zeros(1, 1, nb * 64, d, dtype=BF, device=DEV), cfg)
+    sel = spr.select_blocks(q, mean.contiguous(), nb * 64, cfg, ws)
+    spr.check(ws)
+    lens = torch.tensor([nb * 64], device=DEV)
+    assert torch.equal(sel, R.select(q, mean, nb * 64, 64, top, lens, torch.zeros_like(lens), False, 0, 0))
+
+
 def test_nan_scores_rank_lowest_and_are_reported():
     q = torch.ones(1, 1, 4, 64, device=DEV, dtype=BF)
     mean = torch.arange(6, device=DEV, dtype=F).view(1, 1, 6, 1).expand(1, 1, 6, 64).contiguous()
