@@ -81,7 +81,8 @@ __device__ __forceinline__ Scope scope_of(const SelArgs& a, int b, int t) {
   const int pos = q_start_of(a, b) + t;
   int last = kv_len_of(a, b) - 1;
   if (a.causal) last = min(last, pos);
-  return Scope{last < 0 ? 0 : last / a.block + 1, a.causal && pos >= 0 ? pos / a.block : -1};
+  const int sh = a.block == 128 ? 7 : 6;
+  return Scope{last < 0 ? 0 : (last >> sh) + 1, a.causal && pos >= 0 ? pos >> sh : -1};
 }
 __device__ __forceinline__ bool is_forced(const SelArgs& a, const Scope& s, int g) {
   return g < a.n_first || (a.causal && g <= s.mine && g > s.mine - a.n_local);
@@ -166,13 +167,49 @@ __global__ void __launch_bounds__(256) select_row_kernel(const SelArgs a, int* _
   }
 }
 
+__device__ __forceinline__ float warp_min_f(float x) {
+  float y;
+  asm("redux.sync.min.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float warp_max_f(float x) {
+  float y;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The means' hi and lo parts, [rows][2][D], and their norms squared (infinite for a NaN), for the
+// tiles, which would each split them again.  Eight values a thread.
+template <int D>
+__global__ void __launch_bounds__(256) split_means_kernel(const SelArgs a, int rows) {
+  constexpr int kPer = D / 8;
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const int row = static_cast<int>(min(i / kPer, static_cast<long long>(rows) - 1)), c = static_cast<int>(i % kPer) * 8;
+  const float4* p = reinterpret_cast<const float4*>(a.means + static_cast<size_t>(row) * D + c);
+  const float4 u = __ldg(p), v = __ldg(p + 1);
+  const float x[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+  uint32_t h[4], l[4];
+  float y = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) split_bf16x2(x[2 * k], x[2 * k + 1], h[k], l[k]);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y = fmaf(x[k], x[k], y);
+#pragma unroll
+  for (int o = kPer / 2; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
+  if (i / kPer >= rows) return;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.mean_parts) + static_cast<size_t>(row) * 2 * D + c;
+  *reinterpret_cast<uint4*>(out) = make_uint4(h[0], h[1], h[2], h[3]);
+  *reinterpret_cast<uint4*>(out + D) = make_uint4(l[0], l[1], l[2], l[3]);
+  if (c == 0) a.mean_norm2[row] = y != y ? __builtin_huge_valf() : y;
+}
+
 // Tiles of ROWS tokens of one (batch, key head) against 64 blocks at a time.
 constexpr int kChunk = 64, kTileWarps = 16, kTileThreads = 32 * kTileWarps;
 
-template <int D, int ROWS>
+template <int D, int ROWS, bool QLO = true>
 size_t tile_smem(int nb) {
   const int ld = (nb + kChunk - 1) / kChunk * kChunk + 4;
-  return 2 * 2 * static_cast<size_t>(D) * (ROWS + kChunk) + sizeof(float) * ld * ROWS + sizeof(float) * ROWS +
+  return 2 * static_cast<size_t>(D) * ((QLO ? 2 : 1) * ROWS + 2 * kChunk) + sizeof(float) * ld * ROWS + sizeof(float) * ROWS +
          kTileWarps * 32 * sizeof(int) + 16;
 }
 
@@ -180,34 +217,47 @@ size_t tile_smem(int nb) {
 template <typename T, int D, int ROWS, int VPL, bool QLO>
 __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs a, int* __restrict__ sel, int* __restrict__ list) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kTileQ = ROWS * D * 2, kTileM = kChunk * D * 2;
+  constexpr int kTileQ = ROWS * D * 2, kTileM = kChunk * D * 2, kQ = QLO ? 2 * kTileQ : kTileQ;
   constexpr int RG = ROWS / 16, CG = kTileWarps / RG < 8 ? kTileWarps / RG : 8, NT = kChunk / CG / 8;  // warps over rows, columns; column tiles a warp
+  constexpr float kInf = __builtin_huge_valf();
   const int ld = ceil_div(a.nb, kChunk) * kChunk + 4;
-  const uint32_t sqh = smem_u32(smem), sql = sqh + kTileQ, smh = sql + kTileQ, sml = smh + kTileM;
-  float* score = reinterpret_cast<float*>(smem + 2 * kTileQ + 2 * kTileM);  // [ROWS][ld]
+  const uint32_t sqh = smem_u32(smem), sql = sqh + kTileQ, smh = sqh + kQ, sml = smh + kTileM;
+  float* score = reinterpret_cast<float*>(smem + kQ + 2 * kTileM);  // [ROWS][ld]
   float* qn = score + static_cast<size_t>(ROWS) * ld;
-  int* open = reinterpret_cast<int*>(qn + ROWS);                            // [warp][32]
-  int* mmax = open + kTileWarps * 32;                                                // bits of the largest mean norm squared
+  int* open = reinterpret_cast<int*>(qn + ROWS);                    // [warp][32]
+  int* mmax = open + kTileWarps * 32;                               // bits of the largest mean norm squared
   const int z = blockIdx.y, b = z / a.Hk, kh = z % a.Hk, t0 = blockIdx.x * ROWS;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // the tile's last token sees the most
   const int most = scope_of(a, b, min(t0 + ROWS, a.n) - 1).cand;
-  if (tid == 0) *mmax = 0;
-  auto put = [&](uint32_t hi_tile, uint32_t lo_tile, int r, int c, const float (&x)[8]) {  // 8 values at column c
-    uint32_t h[4], l[4];
+  const __nv_bfloat16* parts = static_cast<const __nv_bfloat16*>(a.mean_parts) + static_cast<size_t>(z) * a.nb * 2 * D;
+  auto load_chunk = [&](int g0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) split_bf16x2(x[2 * i], x[2 * i + 1], h[i], l[i]);
-    const uint32_t at = swz<D>(r, c / 8);
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(hi_tile + at), "r"(h[0]), "r"(h[1]), "r"(h[2]), "r"(h[3]) : "memory");
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(lo_tile + at), "r"(l[0]), "r"(l[1]), "r"(l[2]), "r"(l[3]) : "memory");
+    for (int i = tid; i < 2 * kChunk * (D / 8); i += kTileThreads) {
+      const int c = i % (2 * D / 8), r = i / (2 * D / 8);  // hi, then lo columns of a mean
+      const bool in = g0 + r < a.nb;
+      cp_async_16((c < D / 8 ? smh : sml) + swz<D>(r, c % (D / 8)), parts + static_cast<size_t>(in ? g0 + r : 0) * 2 * D + c * 8,
+                  in ? 16 : 0);
+    }
+    cp_async_commit();
   };
+  if (most > 0) load_chunk(0);
+  if (tid == 0) *mmax = 0;
+  __syncthreads();
+  {
+    float y = 0.f;
+    for (int g = tid; g < most; g += kTileThreads) y = fmaxf(y, __ldg(a.mean_norm2 + static_cast<size_t>(z) * a.nb + g));
+    y = warp_max_f(y);
+    if (lane == 0 && y > 0.f) atomicMax(mmax, __float_as_int(y));  // order of nonnegative floats
+  }
   // the group's query sums and the norms of their sums of magnitudes: D / 8 threads a row
+#pragma unroll 1
   for (int i = tid; i < ROWS * (D / 8); i += kTileThreads) {
     const int r = i / (D / 8), c = i % (D / 8) * 8;
     float x[8] = {}, y = 0.f, mag[8] = {};
     if (t0 + r < a.n) {
-      for (int h = 0; h < a.group; ++h) {
-        const T* p = static_cast<const T*>(a.q.p) + b * a.q.sb + (kh * a.group + h) * a.q.sh + (t0 + r) * a.q.sn + c;
+      const T* p = static_cast<const T*>(a.q.p) + b * a.q.sb + static_cast<long long>(kh * a.group) * a.q.sh + (t0 + r) * a.q.sn + c;
+      for (int h = 0; h < a.group; ++h, p += a.q.sh) {
         uint4 v[sizeof(T) / 2];
 #pragma unroll
         for (int k = 0; k < static_cast<int>(sizeof(T) / 2); ++k) v[k] = reinterpret_cast<const uint4*>(p)[k];
@@ -224,62 +274,56 @@ __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs
 #pragma unroll
     for (int o = D / 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
     if (c == 0) qn[r] = sqrtf(y);
-    put(sqh, sql, r, c, x);
+    uint32_t hi[4], lo[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) split_bf16x2(x[2 * k], x[2 * k + 1], hi[k], lo[k]);
+    const uint32_t at = swz<D>(r, c / 8);
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sqh + at), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
+    if (QLO)
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sql + at), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
   }
   const int rg = warp % RG, cg = warp / RG;
   for (int g0 = 0; g0 < most; g0 += kChunk) {
-    __syncthreads();  // the chunk before is read
-    for (int i = tid; i < kChunk * (D / 8); i += kTileThreads) {
-      const int r = i / (D / 8), c = i % (D / 8) * 8, g = g0 + r;
-      float x[8] = {}, y = 0.f;
-      if (g < most) {
-        const float4* p = reinterpret_cast<const float4*>(a.means + (static_cast<size_t>(z) * a.nb + g) * D + c);
-        const float4 u = __ldg(p), v = __ldg(p + 1);
-        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w, x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) y = fmaf(x[k], x[k], y);
-#pragma unroll
-      for (int o = D / 16; o > 0; o >>= 1) y += __shfl_xor_sync(0xffffffffu, y, o);
-      if (c == 0) atomicMax(mmax, __float_as_int(y != y ? __builtin_huge_valf() : y));  // order of nonnegative floats
-      put(smh, sml, r, c, x);
-    }
+    cp_async_wait<0>();
     __syncthreads();
-    if (cg >= CG) continue;  // more warps than 8-column strips
-    float hh[NT][4], rest[NT][4];
+    if (cg < CG) {  // (more warps than 8-column strips)
+      float hh[NT][4], rest[NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) hh[n][k] = rest[n][k] = 0.f;
+        for (int k = 0; k < 4; ++k) hh[n][k] = rest[n][k] = 0.f;
 #pragma unroll
-    for (int k2 = 0; k2 < D / 32; ++k2) {  // two 16-column steps
-      uint32_t ah[2][4], al[2][4];
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const uint32_t at = swz<D>(rg * 16 + (lane & 15), (2 * k2 + s) * 2 + (lane >> 4));
-        ldmatrix_x4(ah[s], sqh + at);
-        if (QLO) ldmatrix_x4(al[s], sql + at);
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        uint32_t bh[4], bl[4];
-        const uint32_t at = swz<D>((cg * NT + n) * 8 + (lane & 7), 4 * k2 + (lane >> 3));
-        ldmatrix_x4(bh, smh + at);
-        ldmatrix_x4(bl, sml + at);
+      for (int k2 = 0; k2 < D / 32; ++k2) {  // two 16-column steps
+        uint32_t ah[2][4], al[2][4];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          mma_bf16_16816(hh[n], ah[s], bh + 2 * s);
-          mma_bf16_16816(rest[n], ah[s], bl + 2 * s);
-          if (QLO) mma_bf16_16816(rest[n], al[s], bh + 2 * s);
+          const uint32_t at = swz<D>(rg * 16 + (lane & 15), (2 * k2 + s) * 2 + (lane >> 4));
+          ldmatrix_x4(ah[s], sqh + at);
+          if (QLO) ldmatrix_x4(al[s], sql + at);
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint32_t bh[4], bl[4];
+          const uint32_t at = swz<D>((cg * NT + n) * 8 + (lane & 7), 4 * k2 + (lane >> 3));
+          ldmatrix_x4(bh, smh + at);
+          ldmatrix_x4(bl, sml + at);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            mma_bf16_16816(hh[n], ah[s], bh + 2 * s);
+            mma_bf16_16816(rest[n], ah[s], bl + 2 * s);
+            if (QLO) mma_bf16_16816(rest[n], al[s], bh + 2 * s);
+          }
         }
       }
-    }
-    float* out = score + static_cast<size_t>(rg * 16 + (lane >> 2)) * ld + g0 + cg * NT * 8 + (lane & 3) * 2;
+      float* out = score + static_cast<size_t>(rg * 16 + (lane >> 2)) * ld + g0 + cg * NT * 8 + (lane & 3) * 2;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      *reinterpret_cast<float2*>(out + n * 8) = make_float2(hh[n][0] + rest[n][0], hh[n][1] + rest[n][1]);
-      *reinterpret_cast<float2*>(out + 8 * ld + n * 8) = make_float2(hh[n][2] + rest[n][2], hh[n][3] + rest[n][3]);
+      for (int n = 0; n < NT; ++n) {
+        *reinterpret_cast<float2*>(out + n * 8) = make_float2(hh[n][0] + rest[n][0], hh[n][1] + rest[n][1]);
+        *reinterpret_cast<float2*>(out + 8 * ld + n * 8) = make_float2(hh[n][2] + rest[n][2], hh[n][3] + rest[n][3]);
+      }
     }
+    __syncthreads();  // the chunk is read
+    if (g0 + kChunk < most) load_chunk(g0 + kChunk);
   }
   __syncthreads();
   const float mnorm = sqrtf(__int_as_float(*mmax));
@@ -288,55 +332,55 @@ __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs
     const long long w = static_cast<long long>(z) * a.n + t0 + r;
     int* out = sel + w * a.top;
     const Scope sc = scope_of(a, b, t0 + r);
-    const float* sr = score + static_cast<size_t>(r) * ld;
+    const float* sr = score + r * ld;
     const float e2 = (QLO ? 0x1p-15f : 0x1p-16f) * qn[r] * mnorm;  // 2e
-    int forced = 0;
-    if (sc.cand > 0) {
-      const int f0 = min(a.n_first, sc.cand);  // [0, f0) and [l0, l1)
-      const int l1 = a.causal ? min(sc.mine + 1, sc.cand) : 0, l0 = max(f0, sc.mine - a.n_local + 1);
-      forced = f0 + (a.causal ? max(0, l1 - l0) : 0);
-    }
-    const int want = min(a.top, sc.cand) - forced;  // of the blocks that are not forced
-    const int pool = sc.cand - forced;
-    const bool split = want > 0 && want < pool;  // some of them, not all
-    // scores above hi are in, scores in [lo, hi] open; bit j of `chosen`: the j-th open block is in
-    float lo = __builtin_huge_valf(), hi = __builtin_huge_valf();
-    unsigned chosen = 0;
+    // forced: [0, f0) and [l0, l0 + local)
+    const int f0 = min(a.n_first, sc.cand), l0 = max(f0, sc.mine - a.n_local + 1);
+    const int local = max(0, min(sc.mine + 1, sc.cand) - l0), forced = f0 + local;
+    const int want = min(a.top, sc.cand);
+    const bool split = forced < want && want < sc.cand;  // some of the others, not all or none
     // the bound holds where nothing in it or in the products overflows or drops out of the normal range
-    bool slow = split && !(e2 < 0x1p100f && qn[r] > 0x1p-60f && mnorm > 0x1p-60f && e2 > 0x1p-90f);
-    if (split && !slow) {
-      // the scores to choose from (-inf: not one; the finite bound above rules out others), in
-      // registers where they fit
-      auto score_of = [&](int g) { return g < sc.cand && !is_forced(a, sc, g) ? sr[g] : -__builtin_huge_valf(); };
-      float val[VPL > 0 ? VPL : 1];
+    if (split && !(e2 < 0x1p100f && qn[r] > 0x1p-60f && mnorm > 0x1p-60f && e2 > 0x1p-90f)) {
+      if (lane == 0) list[atomicAdd(list - 1, 1)] = static_cast<int>(w);
+      continue;
+    }
+    // What to choose from: infinite where a block is in, -infinite where it is out (the finite
+    // bound rules out such scores); in registers where they fit.
+    auto score_of = [&](int g) {
+      const bool in = g < f0 || static_cast<unsigned>(g - l0) < static_cast<unsigned>(local) || (!split && want == sc.cand);
+      return g >= sc.cand ? -kInf : in ? kInf : split ? sr[g] : -kInf;
+    };
+    float val[VPL > 0 ? VPL : 1];
 #pragma unroll
-      for (int i = 0; i < VPL; ++i) val[i] = score_of(32 * i + lane);
-      auto each_score = [&](auto f) {
-        if (VPL > 0) {
+    for (int i = 0; i < VPL; ++i) val[i] = score_of(32 * i + lane);
+    auto each_score = [&](auto f) {  // f(x, first block of the 32)
+      if (VPL > 0) {
 #pragma unroll
-          for (int i = 0; i < VPL; ++i) f(val[i]);
-        } else {
-          for (int g = lane; g < sc.cand; g += 32) f(score_of(g));
-        }
-      };
+        for (int i = 0; i < VPL; ++i) f(val[i], 32 * i);
+      } else {
+        for (int g0 = 0; g0 < sc.cand; g0 += 32) f(score_of(g0 + lane), g0);
+      }
+    };
+    // scores above hi are in, scores in [lo, hi] open; bit j of `chosen`: the j-th open block is in
+    float lo = kInf, hi = 0.f;
+    unsigned chosen = 0;
+    if (split) {
       auto count = [&](float v) {
         int c = 0;
-        each_score([&](float x) { c += x >= v; });
+        each_score([&](float x, int) { c += x >= v; });
         return __reduce_add_sync(0xffffffffu, c);
       };
-      auto least = [&](float x) { return float_from_order_key(__reduce_min_sync(0xffffffffu, float_order_key(x))); };
-      auto most = [&](float x) { return float_from_order_key(__reduce_max_sync(0xffffffffu, float_order_key(x))); };
       // Halving the range of the values finds a threshold between the want-th and the next one in
       // about log2(range / gap) steps (seven for 16 of 128 normal scores; over the keys' bits the
       // sign and exponent alone take nine).
-      float vlo = __builtin_huge_valf(), vhi = -__builtin_huge_valf();
-      each_score([&](float x) {
-        vhi = fmaxf(vhi, x);
-        vlo = fminf(vlo, x == -__builtin_huge_valf() ? vlo : x);
+      float vlo = kInf, vhi = -kInf;
+      each_score([&](float x, int) {
+        vhi = fmaxf(vhi, x == kInf ? vhi : x);
+        vlo = fminf(vlo, x == -kInf ? vlo : x);
       });
-      vlo = least(vlo), vhi = most(vhi);
+      vlo = warp_min_f(vlo), vhi = warp_max_f(vhi);
       float v = vlo;
-      int have = pool;  // scores >= v
+      int have = sc.cand;  // scores >= v
       for (int step = 0; step < 24 && have != want; ++step) {
         const float mid = 0.5f * vlo + 0.5f * vhi;
         if (!(mid > vlo && mid < vhi)) break;
@@ -348,89 +392,83 @@ __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs
       }
       if (have != want) {  // (nearly) equal scores: the exact one by its bits
         uint32_t bits = 0;
-        have = pool;
+        have = sc.cand;
         for (int bit = 31; bit >= 0 && have != want; --bit) {
           const uint32_t next = bits | (1u << bit);
           int c = 0;
-          each_score([&](float x) { c += x > -__builtin_huge_valf() && float_order_key(x) >= next; });
+          each_score([&](float x, int) { c += x > -kInf && float_order_key(x) >= next; });
           c = __reduce_add_sync(0xffffffffu, c);
           if (c >= want) bits = next, have = c;
         }
         v = float_from_order_key(bits);
       }
       // the want-th largest, and the one after it
-      float fa = __builtin_huge_valf(), fb = -__builtin_huge_valf();
-      each_score([&](float x) {
+      float fa = kInf, fb = -kInf;
+      each_score([&](float x, int) {
         if (x >= v)
           fa = fminf(fa, x);
         else
           fb = fmaxf(fb, x);
       });
-      fa = least(fa);
-      fb = have > want ? fa : most(fb);
-      if (fa - fb > e2) {
-        hi = fb;
-      } else {
+      fa = warp_min_f(fa);
+      fb = have > want ? fa : warp_max_f(fb);
+      hi = fb;
+      if (!(fa - fb > e2)) {
         lo = fa - e2, hi = fb + e2;
         int in = 0, mid = 0;
-        for (int g0 = 0; g0 < sc.cand; g0 += 32) {
-          const int g = g0 + lane;
-          const bool live = g < sc.cand && !is_forced(a, sc, g);
-          const float s = live ? sr[g] : 0.f;
-          in += __popc(__ballot_sync(0xffffffffu, live && s > hi));
-          const bool o = live && s >= lo && s <= hi;
+        each_score([&](float x, int g0) {
+          in += __popc(__ballot_sync(0xffffffffu, x > hi));
+          const bool o = x >= lo && x <= hi;
           const unsigned om = __ballot_sync(0xffffffffu, o);
           const int at = mid + __popc(om & ((1u << lane) - 1u));
-          if (o && at < 32) my_open[at] = g;
+          if (o && at < 32) my_open[at] = g0 + lane;
           mid += __popc(om);
-        }
+        });
         __syncwarp();
-        slow = mid > 32;
-        if (!slow) {  // the open blocks' scores in 64 bits: lane j keeps the j-th's
-          constexpr int C = D / 32;
-          double q[C] = {};
-          for (int h = 0; h < a.group; ++h) {
-            const T* p = static_cast<const T*>(a.q.p) + b * a.q.sb + (kh * a.group + h) * a.q.sh + (t0 + r) * a.q.sn + lane * C;
-#pragma unroll
-            for (int c = 0; c < C; ++c) q[c] += static_cast<double>(to_f32<T>(p[c]));
-          }
-          double mine = 0.0;
-          for (int j = 0; j < mid; ++j) {
-            const float* m = a.means + (static_cast<size_t>(z) * a.nb + my_open[j]) * D + lane * C;
-            double s = 0.0;
-#pragma unroll
-            for (int c = 0; c < C; ++c) s = fma(q[c], static_cast<double>(__ldg(m + c)), s);
-            s = warp_sum_d(s);
-            if (lane == j) mine = s;
-          }
-          int before = 0;  // open blocks that come before this lane's
-          for (int j = 0; j < mid; ++j) {
-            const double s = __shfl_sync(0xffffffffu, mine, j);
-            before += s > mine || (s == mine && j < lane);
-          }
-          chosen = __ballot_sync(0xffffffffu, lane < mid && before < want - in);
+        if (mid > 32) {
+          if (lane == 0) list[atomicAdd(list - 1, 1)] = static_cast<int>(w);
+          continue;
         }
+        // the open blocks' scores in 64 bits: lane j keeps the j-th's
+        constexpr int C = D / 32;
+        double q[C] = {};
+        for (int h = 0; h < a.group; ++h) {
+          const T* p = static_cast<const T*>(a.q.p) + b * a.q.sb + (kh * a.group + h) * a.q.sh + (t0 + r) * a.q.sn + lane * C;
+#pragma unroll
+          for (int c = 0; c < C; ++c) q[c] += static_cast<double>(to_f32<T>(p[c]));
+        }
+        double mine = 0.0;
+        for (int j = 0; j < mid; ++j) {
+          const float* m = a.means + (static_cast<size_t>(z) * a.nb + my_open[j]) * D + lane * C;
+          double s = 0.0;
+#pragma unroll
+          for (int c = 0; c < C; ++c) s = fma(q[c], static_cast<double>(__ldg(m + c)), s);
+          s = warp_sum_d(s);
+          if (lane == j) mine = s;
+        }
+        int before = 0;  // open blocks that come before this lane's
+        for (int j = 0; j < mid; ++j) {
+          const double s = __shfl_sync(0xffffffffu, mine, j);
+          before += s > mine || (s == mine && j < lane);
+        }
+        chosen = __ballot_sync(0xffffffffu, lane < mid && before < want - in);
         __syncwarp();
       }
     }
-    if (slow) {
-      if (lane == 0) list[atomicAdd(list - 1, 1)] = static_cast<int>(w);
-      continue;
-    }
     int n_out = 0, n_open = 0;
-    for (int g0 = 0; g0 < sc.cand; g0 += 32) {
-      const int g = g0 + lane;
-      const bool live = g < sc.cand, f = live && is_forced(a, sc, g);
-      const float s = live ? sr[g] : 0.f;
-      const bool o = split && live && !f && s >= lo && s <= hi;
-      const unsigned om = __ballot_sync(0xffffffffu, o);
-      bool take = f || (live && want >= pool);
-      if (split && live && !f) take = o ? (chosen >> (n_open + __popc(om & ((1u << lane) - 1u)))) & 1u : s > hi;
-      n_open += __popc(om);
+    const unsigned below = (1u << lane) - 1u;
+    each_score([&](float x, int g0) {
+      bool take = x > hi;
+      if (chosen != 0) {
+        const bool o = x >= lo && x <= hi;
+        const unsigned om = __ballot_sync(0xffffffffu, o);
+        if (o) take = (chosen >> (n_open + __popc(om & below))) & 1u;
+        n_open += __popc(om);
+      }
       const unsigned tm = __ballot_sync(0xffffffffu, take);
-      if (take) out[n_out + __popc(tm & ((1u << lane) - 1u))] = g;
+      if (take) out[n_out + __popc(tm & below)] = g0 + lane;
       n_out += __popc(tm);
-    }
+    });
     for (int j = n_out + lane; j < a.top; j += 32) out[j] = -1;
   }
 }
@@ -448,7 +486,10 @@ template <typename T, int D, int ROWS, int VPL, bool QLO>
 cudaError_t tile_select(const SelArgs& a, int* sel, cudaStream_t st) {
   cudaError_t e = cudaMemsetAsync(a.slow, 0, sizeof(int), st);
   if (e != cudaSuccess) return e;
-  const size_t smem = tile_smem<D, ROWS>(a.nb);
+  const int means = a.Bt * a.Hk * a.nb;
+  split_means_kernel<D><<<static_cast<unsigned>((static_cast<long long>(means) * (D / 8) + 255) / 256), 256, 0, st>>>(a, means);
+  if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
+  const size_t smem = tile_smem<D, ROWS, QLO>(a.nb);
   auto kern = select_tile_kernel<T, D, ROWS, VPL, QLO>;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;

@@ -63,6 +63,8 @@ struct SelArgs {
   const float* means;    // [Bt, Hk, nb, d]
   int* status;
   int* slow;             // select: number of rows left to select_row_kernel, then the rows
+  void* mean_parts;      // select: bf16 [Bt, Hk, nb][2][d], the means' hi and lo parts
+  float* mean_norm2;     // select: [Bt, Hk, nb] squared norms of the means
   // lists: per region (batch, key head, slice of `slice` tokens), `slices` regions per head
   int slice, slices;
   int subs;              // sub-slices of a slice

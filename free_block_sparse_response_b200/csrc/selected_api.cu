@@ -99,7 +99,7 @@ constexpr size_t kPartialBytes = 1ull << 30;
 // status header).
 struct Plan {
   int regions, chunk;  // chunk: regions per launch
-  size_t slow, vexp, offs, list, inv, units, n_units, blk, part, ml, delta, seg, total;
+  size_t slow, mean_parts, mean_norm2, vexp, offs, list, inv, units, n_units, blk, part, ml, delta, seg, total;
 };
 
 Plan make_plan(SelArgs& a, bool backward) {
@@ -141,8 +141,10 @@ Plan make_plan(SelArgs& a, bool backward) {
     return at;
   };
   const size_t R = L.regions;
-  // the selection's list comes first: its place depends on nothing else
   L.slow = take(sizeof(int) * (static_cast<size_t>(a.Bt) * a.Hk * a.n + 1));
+  const size_t means = static_cast<size_t>(a.Bt) * a.Hk * a.nb;
+  L.mean_parts = take(backward ? 0 : 2 * 2 * means * a.d);
+  L.mean_norm2 = take(backward ? 0 : sizeof(float) * means);
   L.vexp = take(backward || a.f32 ? 0 : sizeof(float) * static_cast<size_t>(a.Bt) * a.Hk * a.nb);
   L.offs = take(sizeof(int) * R * a.nb * a.subs);
   L.list = take(sizeof(int) * R * entries);
@@ -167,6 +169,8 @@ T* at(void* ws, size_t off) {
 void bind(SelArgs& a, const Plan& L, void* ws) {
   a.status = at<int>(ws, 0);
   a.slow = at<int>(ws, L.slow);
+  a.mean_parts = at<char>(ws, L.mean_parts);
+  a.mean_norm2 = at<float>(ws, L.mean_norm2);
   a.offs = at<int>(ws, L.offs);
   a.list = at<int>(ws, L.list);
   a.inv = at<int>(ws, L.inv);
