@@ -524,7 +524,8 @@ cudaError_t select_blocks(const SelArgs& a, int* sel, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_key_means(const SelArgs& a, const int* kv_start, int max_new, float* means, cudaStream_t st) {
-  const int blocks = kv_start == nullptr ? a.nb : min(a.nb, (max_new + a.block - 2) / a.block + 1);
+  // max_new keys from any place in a block touch at most this many
+  const int blocks = kv_start == nullptr ? a.nb : min(a.nb, (min(max_new, a.nk) + a.block - 2) / a.block + 1);
   if (a.Hk > 65535 || a.Bt > 65535) return cudaErrorInvalidValue;
   const dim3 grid(blocks, a.Hk, a.Bt);
   if (a.f32)

@@ -328,6 +328,20 @@ def test_decode_over_a_growing_cache_matches_the_prompt():
     close(out, prompt[:, :, -1:].double(), 2 * U[BF] * want.abs() + 2 * (U[BF] + E) * size, "last token")
 
 
+@pytest.mark.parametrize("max_new", [150, 10 ** 6, 2 ** 31 - 1])
+def test_means_of_appended_keys_with_any_bound_on_them(max_new):
+    """max_new is an upper bound: one far past the cache renews the same blocks and no others."""
+    k = rnd(gen_of(22), 2, 3, 400, 64)
+    lens = torch.tensor([400, 210], dtype=torch.int32, device=DEV)
+    start = torch.tensor([250, 209], dtype=torch.int32, device=DEV)
+    means = torch.full((2, 3, 7, 64), 5.0, device=DEV)
+    spr.key_means(k, 64, kv_len=lens, kv_start=start, max_new=max_new, out=means)
+    want = torch.full_like(means, 5.0)
+    full = spr.key_means(k, 64, kv_len=lens)
+    want[0, :, 3:], want[1, :, 3] = full[0, :, 3:], full[1, :, 3]
+    assert torch.equal(means, want)
+
+
 def test_long_offsets_past_32_bits():
     """A cache view whose last rows lie past 2^32 elements of its start (strides of a wider buffer)."""
     rows, d = 1024, 128
