@@ -140,25 +140,35 @@ __global__ void __launch_bounds__(256) select_row_kernel(const SelArgs a, int* _
       for (int c = 0; c < C; ++c) q[c] += static_cast<double>(to_f32<T>(p[(c / 4) * 32 + part * 4 + c % 4]));
     }
     const float* m = a.means + static_cast<size_t>(z) * a.nb * D + part * 4;
-    for (int g0 = 0; g0 < sc.cand; g0 += 32) {
-      const int g = g0 + grp;
-      double s = 0.0;
-      if (g < sc.cand) {
+    // the means of kBatch blocks a lane under way
+    constexpr int kBatch = 4;
+    for (int g0 = 0; g0 < sc.cand; g0 += 32 * kBatch) {
+      float4 x[kBatch][C / 4];
 #pragma unroll
-        for (int c = 0; c < C; c += 4) {
-          const float4 x = __ldg(reinterpret_cast<const float4*>(m + static_cast<size_t>(g) * D + c * 8));
-          s = fma(q[c], static_cast<double>(x.x), s);
-          s = fma(q[c + 1], static_cast<double>(x.y), s);
-          s = fma(q[c + 2], static_cast<double>(x.z), s);
-          s = fma(q[c + 3], static_cast<double>(x.w), s);
-        }
+      for (int k = 0; k < kBatch; ++k) {
+        const int g = min(g0 + 32 * k + grp, sc.cand - 1);
+#pragma unroll
+        for (int c = 0; c < C; c += 4)
+          x[k][c / 4] = __ldg(reinterpret_cast<const float4*>(m + static_cast<size_t>(g) * D + c * 8));
       }
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (part == 0 && g < sc.cand) {
-        const bool forced = is_forced(a, sc, g);
-        if (!forced && s != s) record_error(a.status, kErrNonFinite);
-        keys[g] = forced ? ~0ull : score_key(s);
+      for (int k = 0; k < kBatch; ++k) {
+        const int g = g0 + 32 * k + grp;
+        double s = 0.0;
+#pragma unroll
+        for (int c = 0; c < C; c += 4) {
+          s = fma(q[c], static_cast<double>(x[k][c / 4].x), s);
+          s = fma(q[c + 1], static_cast<double>(x[k][c / 4].y), s);
+          s = fma(q[c + 2], static_cast<double>(x[k][c / 4].z), s);
+          s = fma(q[c + 3], static_cast<double>(x[k][c / 4].w), s);
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (part == 0 && g < sc.cand) {
+          const bool forced = is_forced(a, sc, g);
+          if (!forced && s != s) record_error(a.status, kErrNonFinite);
+          keys[g] = forced ? ~0ull : score_key(s);
+        }
       }
     }
     __syncthreads();
