@@ -147,11 +147,20 @@ __global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
   // sub-slices of this region that hold tokens
   const int live = min(a.subs, ceil_div(a.n - s * a.slice, kSub));
   int* offs = a.offs + static_cast<size_t>(region) * a.nb * a.subs;
-  for (int g = warp; g < a.nb; g += 16) {
-    int cnt = 0;
-    for (int i = lane; i < live; i += 32) cnt += offs[static_cast<size_t>(g) * a.subs + i];
-    cnt = __reduce_add_sync(0xffffffffu, cnt);
-    if (lane == 0) s_blk[g].x = cnt;
+  // (eight blocks' counts under way: one at a time each costs a memory latency)
+  constexpr int kBatch = 8;
+  for (int g0 = warp; g0 < a.nb; g0 += 16 * kBatch) {
+    int cnt[kBatch] = {};
+    for (int i = lane; i < live; i += 32) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (g0 + 16 * k < a.nb) cnt[k] += offs[static_cast<size_t>(g0 + 16 * k) * a.subs + i];
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int sum = __reduce_add_sync(0xffffffffu, cnt[k]);
+      if (lane == 0 && g0 + 16 * k < a.nb) s_blk[g0 + 16 * k].x = sum;
+    }
   }
   __syncthreads();
   int entry0 = 0, unit0 = 0, slot0 = 0;
@@ -172,22 +181,31 @@ __global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
     }
   }
   __syncthreads();
-  for (int g = warp; g < a.nb; g += 16) {
-    const int4 k = s_blk[g];
-    int off = k.x;
+  for (int g0 = warp; g0 < a.nb; g0 += 16 * kBatch) {
+    int off[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) off[k] = g0 + 16 * k < a.nb ? s_blk[g0 + 16 * k].x : 0;
     for (int i0 = 0; i0 < live; i0 += 32) {
       const int i = i0 + lane;
-      int* at = offs + static_cast<size_t>(g) * a.subs + i;
-      const int c = i < live ? *at : 0;
-      int x = c;
+      int c[kBatch];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+      for (int k = 0; k < kBatch; ++k)
+        c[k] = i < live && g0 + 16 * k < a.nb ? offs[static_cast<size_t>(g0 + 16 * k) * a.subs + i] : 0;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        int x = c[k];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, o);
+          if (lane >= o) x += y;
+        }
+        if (i < live && g0 + 16 * k < a.nb) offs[static_cast<size_t>(g0 + 16 * k) * a.subs + i] = off[k] + x - c[k];
+        off[k] += __shfl_sync(0xffffffffu, x, 31);
       }
-      if (i < live) *at = off + x - c;
-      off += __shfl_sync(0xffffffffu, x, 31);
     }
+  }
+  for (int g = warp; g < a.nb; g += 16) {
+    const int4 k = s_blk[g];
     const int rows = k.y * a.group, nu = ceil_div(rows, a.unit_rows);
     for (int i = lane; i < nu; i += 32)
       a.units[static_cast<size_t>(region) * a.unit_cap + k.w + i] =
