@@ -75,10 +75,9 @@ struct SelArgs {
   Unit* units;           // [regions][unit_cap], the last ones empty
   int* n_units;          // [regions]
   int4* blk;             // [regions][nb] {units, first slot of their sums where there are more, first unit, -}
-  // partial rows of one chunk of regions: fp32 [chunk regions][slice * top * group][d], or fp16
-  // in planes of 64 columns (selected_tc.cu)
+  // partial rows of one chunk of regions, [chunk regions][slice * top * group][d]: fp32, or fp16
+  // with the columns of part_column() (selected_tc.cuh)
   float* part;
-  long long plane;       // rows of a plane
   // statistics of each partial row.  fp32: its maximum (log2 units) and sum; fp16 forward: its
   // log-sum-exp and the exponent that its values are to be multiplied by 2^ of; fp16 dQ: -, scale
   float2* ml;

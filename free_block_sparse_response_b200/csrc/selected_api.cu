@@ -120,8 +120,9 @@ Plan make_plan(SelArgs& a, bool backward) {
   if (a.slices == 1) a.slice = a.n;
   L.regions = a.Bt * a.Hk * a.slices;
   const long long entries = static_cast<long long>(a.slice) * a.top, rows = entries * a.group;
-  L.chunk = static_cast<int>(std::min<long long>(L.regions, std::max<long long>(1, kPartialBytes / (row * rows))));
-  a.plane = rows * L.chunk;
+  // equal chunks, so that the last one fills the SMs too
+  const long long most = std::min<long long>(L.regions, std::max<long long>(1, kPartialBytes / (row * rows)));
+  L.chunk = spr::ceil_div(L.regions, spr::ceil_div(L.regions, static_cast<int>(most)));
   // The tensor-core kernels work tile by tile.  On the fp32 pipes a unit is one CTA: long units
   // load K and V seldom (and, backward, leave few sums), short ones fill the SMs when there are
   // few rows: the longest that still gives four units per SM.

@@ -12,7 +12,7 @@
 // Every CTA takes an equal, contiguous share of the tiles in the order region, block, row.  A
 // block inside one share is written directly; a block that a share's end cuts leaves one fp32
 // sum per CTA (two slots each), added in order by join_kv_tc_kernel: the same in every run.
-// dQ parts go out as in the forward pass (fp16 with a power of two per row, planes of 64).
+// dQ parts go out as in the forward pass (fp16 with a power of two per row, whole rows).
 //
 // Work of a tile (B = D = 128): 21 MFLOP, 16K exponentials, 64 KB gathered, 32 KB written.
 // Shared memory (7 tiles of 32 KB) holds K, V, P, dS, one dO and two Q; TMEM is full (S, dP, dV^T,
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float one[2] = {1.f, 1.f};
         float up[2];
-        store_part<D>(o, one, lane0 + q, un.rows, part + 32 * i, a.plane, out0, up);
+        store_part<D>(o, one, lane0 + q, un.rows, part + 32 * i, out0, up);
         if (i == 0) {
 #pragma unroll
           for (int k = 0; k < 2; ++k)

@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------------------- output
     tc::setmaxnreg_inc<kRegOut>();
     // A quad of lanes holds rows q and q + 8 of 16 TMEM lanes, lane i of it columns 8 j + 2 i
-    // and + 1; each lane's 16 columns of a 64-column plane go out as 32 contiguous bytes, a
+    // and + 1; each lane's 16 columns of a 64-column line go out as 32 contiguous bytes, a
     // row's quad as one 128-byte line (part_column() is the order inside the line).
     const int w4 = warp & 3, q = lane >> 2, i = lane & 3;
     uint8_t* const part = static_cast<uint8_t*>(static_cast<void*>(a.part));
@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < D / 2; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
           }
-          store_part_as_is<D>(o, lane0 + q, un.rows, part + 32 * i, a.plane, out0);
+          store_part_as_is<D>(o, lane0 + q, un.rows, part + 32 * i, out0);
         }
         tc::fence_before_sync();
         tc::mbar_arrive(bar(kOFree + x));
@@ -409,9 +409,8 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
   const int b = z / a.Hk, kh = z % a.Hk;
   const int* inv = a.inv + (static_cast<size_t>(z) * a.n + (live ? t : 0)) * a.top;
   const size_t row0 = ci * static_cast<size_t>(a.slice) * a.top * a.group + h;
-  // the lane's 16 bytes of a part: chunk ch % 8 of a line in plane ch / 8
-  const uint8_t* part =
-      static_cast<const uint8_t*>(static_cast<const void*>(a.part)) + (ch / 8) * a.plane * 128 + (ch % 8) * 16;
+  // the lane's 16 bytes of a part
+  const uint8_t* part = static_cast<const uint8_t*>(static_cast<const void*>(a.part)) + ch * 16;
   float m = -kInf, l = 0.f, acc[8] = {};
   for (int j0 = 0; j0 < a.top; j0 += kPer) {
     const int e = live && j0 + ch < a.top ? __ldg(inv + j0 + ch) : -1;
@@ -439,7 +438,7 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
       for (int i = 0; i < 8; ++i) {
         const int ej = __shfl_sync(0xffffffffu, e, j + i, kPer);
         fj[i] = __shfl_sync(0xffffffffu, f, j + i, kPer);
-        v[i] = ej >= 0 ? __ldcs(reinterpret_cast<const uint4*>(part + (row0 + static_cast<size_t>(ej) * a.group) * 128))
+        v[i] = ej >= 0 ? __ldcs(reinterpret_cast<const uint4*>(part + (row0 + static_cast<size_t>(ej) * a.group) * (2 * D)))
                        : make_uint4(0, 0, 0, 0);
       }
 #pragma unroll

@@ -96,8 +96,8 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32])
       : "r"(taddr));
 }
 
-// Partial rows: planes of 64 columns, rows of 128 bytes.  First column of the c-th pair of
-// 16-byte chunk `ch` of a row (8 chunks a plane): the four lanes of a quad, which hold columns
+// Partial rows of 2 D bytes, 128-byte lines of 64 columns.  First column of the c-th pair of
+// 16-byte chunk `ch` of a row (8 chunks a line): the four lanes of a quad, which hold columns
 // 2 i, 2 i + 1 of every eight, write 32 bytes each.
 __device__ __forceinline__ int part_column(int ch, int c) {
   return (ch >> 3) * 64 + ((ch & 1) * 4 + c) * 8 + ((ch & 7) >> 1) * 2;
@@ -220,7 +220,7 @@ __device__ __forceinline__ bool each_tile(const SelArgs& a, int first, const int
 // by side, since this is bound by its latencies.  `part` is the lane's 32 bytes of row 0.
 template <int D>
 __device__ __forceinline__ void store_part(const uint32_t (&o)[D / 2], const float (&f)[2], int r, int rows, uint8_t* part,
-                                           long long plane, long long out0, float (&up)[2]) {
+                                           long long out0, float (&up)[2]) {
   float big[2][2] = {}, mx[2], g[2];
 #pragma unroll
   for (int c = 0; c < D / 2; c += 8)
@@ -251,14 +251,14 @@ __device__ __forceinline__ void store_part(const uint32_t (&o)[D / 2], const flo
                                             __uint_as_float(o[c / 2 + 4 * j + 2 * k + 1]) * g[k]);
         h[j] = *reinterpret_cast<const uint32_t*>(&v);
       }
-      st_global_32(part + ((c / 64) * plane + out0 + r + 8 * k) * 128, h);
+      st_global_32(part + (out0 + r + 8 * k) * (2 * D) + c * 2, h);
     }
   }
 }
 
 // The same without a scale: the values are inside fp16.
 template <int D>
-__device__ __forceinline__ void store_part_as_is(const uint32_t (&o)[D / 2], int r, int rows, uint8_t* part, long long plane,
+__device__ __forceinline__ void store_part_as_is(const uint32_t (&o)[D / 2], int r, int rows, uint8_t* part,
                                                  long long out0) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -271,7 +271,7 @@ __device__ __forceinline__ void store_part_as_is(const uint32_t (&o)[D / 2], int
         const __half2 v = __floats2half2_rn(__uint_as_float(o[c / 2 + 4 * j + 2 * k]), __uint_as_float(o[c / 2 + 4 * j + 2 * k + 1]));
         h[j] = *reinterpret_cast<const uint32_t*>(&v);
       }
-      st_global_32(part + ((c / 64) * plane + out0 + r + 8 * k) * 128, h);
+      st_global_32(part + (out0 + r + 8 * k) * (2 * D) + c * 2, h);
     }
   }
 }
