@@ -83,6 +83,7 @@ struct SelArgs {
   float2* ml;
   float* vexp;           // [Bt * Hk][nb] Unit::k of each block (fp16 forward parts), or null
   float* delta;          // backward: sum of o * go per query row
+  __nv_bfloat16* rest;   // [Bt, Hq, n, d] what the rounding of o left off, or null
   float* seg;            // backward: [chunk regions][seg_cap][2][block][d] sums of split blocks
   int seg_cap;
 };

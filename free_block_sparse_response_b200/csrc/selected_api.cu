@@ -50,6 +50,13 @@ int check_keys(const sparsepr_view* v, int32_t Nk) {
   return SPARSEPR_OK;
 }
 
+int check_rest(const sparsepr_selected* p) {
+  if (p->out_rest == nullptr) return SPARSEPR_OK;
+  if (p->dtype != SPARSEPR_BF16) return bad("out_rest goes with bf16 results");
+  if ((reinterpret_cast<uintptr_t>(p->out_rest) & 15u) != 0) return bad("out_rest must start on a 16-byte boundary");
+  return SPARSEPR_OK;
+}
+
 View view(const sparsepr_view* v) { return View{v->data, v->stride_b, v->stride_h, v->stride_n}; }
 
 int check_problem(const sparsepr_selected* p) {
@@ -88,6 +95,7 @@ SelArgs base_args(const sparsepr_selected* p) {
   a.n_first = p->n_first, a.n_local = p->n_local;
   a.q_start0 = p->Nk - p->Nq;
   a.kv_len = p->kv_len, a.q_start = p->q_start;
+  a.rest = static_cast<__nv_bfloat16*>(p->out_rest);
   a.scale = p->scale > 0.f ? p->scale : 1.0f / std::sqrt(static_cast<float>(p->d));
   return a;
 }
@@ -271,7 +279,7 @@ int sparsepr_selected_attn(const sparsepr_selected* p, const sparsepr_view* Q, c
                            const sparsepr_view* V, const int32_t* sel, const sparsepr_view* O, float* lse, void* ws,
                            sparsepr_stream_t stream) {
   int rc;
-  if ((rc = check_problem(p))) return rc;
+  if ((rc = check_problem(p)) || (rc = check_rest(p))) return rc;
   const int elem = p->dtype == SPARSEPR_F32 ? 4 : 2;
   for (const sparsepr_view* v : {Q, K, V, O})
     if ((rc = check_view(v, elem, true))) return rc;
@@ -299,7 +307,7 @@ int sparsepr_selected_attn_backward(const sparsepr_selected* p, const sparsepr_v
                                     const float* lse, const int32_t* sel, const sparsepr_view* dQ, const sparsepr_view* dK,
                                     const sparsepr_view* dV, void* ws, sparsepr_stream_t stream) {
   int rc;
-  if ((rc = check_problem(p))) return rc;
+  if ((rc = check_problem(p)) || (rc = check_rest(p))) return rc;
   const int elem = p->dtype == SPARSEPR_F32 ? 4 : 2;
   for (const sparsepr_view* v : {dO, Q, K, V, O, dQ, dK, dV})
     if ((rc = check_view(v, elem, true))) return rc;

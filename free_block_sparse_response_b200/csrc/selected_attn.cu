@@ -233,19 +233,23 @@ __global__ void __launch_bounds__(256) join_kernel(const SelArgs a, int first, i
 // ------------------------------------------------------------------------------ backward
 
 // delta_i = sum_c O_ic dO_ic: D / V lanes a row with 16-byte loads, four rows under way per lane.
-template <typename T, int D>
+// Its error is common to a row's dS, so it does not average out over the keys as the rounding of dS
+// does: a bf16 O alone makes it the largest error of dQ (16 heads x 32,760 tokens, 8 blocks: 2.9e-3
+// of dQ's norm, 1.7e-3 with REST, what O's rounding left off; dQ's own rounding is 1.7e-3).
+template <typename T, int D, bool REST>
 __global__ void __launch_bounds__(256) delta_kernel(const SelArgs a) {
   constexpr int V = 16 / sizeof(T), kPer = D / V, kRowsW = 32 / kPer, kBatch = 4;
   const int lane = threadIdx.x & 31, ch = lane % kPer;
   const long long rows = static_cast<long long>(a.Bt) * a.Hq * a.n;
   const long long w0 = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kRowsW * kBatch + lane / kPer;
-  uint4 o[kBatch], g[kBatch];
+  uint4 o[kBatch], g[kBatch], r[kBatch];
 #pragma unroll
   for (int i = 0; i < kBatch; ++i) {
     const long long w = min(w0 + i * kRowsW, rows - 1);
     const int t = static_cast<int>(w % a.n), h = static_cast<int>(w / a.n % a.Hq), b = static_cast<int>(w / a.n / a.Hq);
     o[i] = *reinterpret_cast<const uint4*>(row_ptr<const T>(a.o, b, h, t) + ch * V);
     g[i] = *reinterpret_cast<const uint4*>(row_ptr<const T>(a.go, b, h, t) + ch * V);
+    if (REST) r[i] = *reinterpret_cast<const uint4*>(a.rest + static_cast<size_t>(w) * D + ch * V);
   }
 #pragma unroll
   for (int i = 0; i < kBatch; ++i) {
@@ -253,6 +257,11 @@ __global__ void __launch_bounds__(256) delta_kernel(const SelArgs a) {
 #pragma unroll
     for (int c = 0; c < V; ++c)
       s = fmaf(to_f32<T>(reinterpret_cast<const T*>(&o[i])[c]), to_f32<T>(reinterpret_cast<const T*>(&g[i])[c]), s);
+    if (REST) {
+#pragma unroll
+      for (int c = 0; c < V; ++c)
+        s = fmaf(to_f32<T>(reinterpret_cast<const T*>(&r[i])[c]), to_f32<T>(reinterpret_cast<const T*>(&g[i])[c]), s);
+    }
 #pragma unroll
     for (int k = kPer / 2; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
     if (ch == 0 && w0 + i * kRowsW < rows) a.delta[w0 + i * kRowsW] = s;
@@ -483,15 +492,15 @@ cudaError_t backward(const SelArgs& a, int first, int count, cudaStream_t st) {
   return counted(cudaGetLastError(), 1);
 }
 
-template <typename T>
+template <typename T, bool REST>
 cudaError_t delta(const SelArgs& a, cudaStream_t st) {
   const long long rows = static_cast<long long>(a.Bt) * a.Hq * a.n;
   const int per_cta = 8 * 4 * (32 / (a.d * static_cast<int>(sizeof(T)) / 16));
   const unsigned grid = static_cast<unsigned>((rows + per_cta - 1) / per_cta);
   if (a.d == 128)
-    delta_kernel<T, 128><<<grid, 256, 0, st>>>(a);
+    delta_kernel<T, 128, REST><<<grid, 256, 0, st>>>(a);
   else
-    delta_kernel<T, 64><<<grid, 256, 0, st>>>(a);
+    delta_kernel<T, 64, REST><<<grid, 256, 0, st>>>(a);
   return counted(cudaGetLastError(), 1);
 }
 
@@ -512,7 +521,8 @@ cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cud
 }
 
 cudaError_t launch_delta(const SelArgs& a, cudaStream_t st) {
-  return a.f32 ? delta<float>(a, st) : delta<__nv_bfloat16>(a, st);
+  if (a.f32) return delta<float, false>(a, st);
+  return a.rest != nullptr ? delta<__nv_bfloat16, true>(a, st) : delta<__nv_bfloat16, false>(a, st);
 }
 
 }  // namespace spr

@@ -242,8 +242,11 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_kernel(const SelArgs a,
       x = fmaf(f, *((splits > 1 ? cluster.map_shared_rank(&s_co[0][0], w) : &s_co[0][0]) + i), x);
     }
     const int hq = kh * a.group + h0 + h;
-    static_cast<__nv_bfloat16*>(a.o.p)[b * a.o.sb + hq * a.o.sh + t * a.o.sn + c] =
-        __float2bfloat16_rn(sum > 0.f ? x / sum : sum != sum ? sum : 0.f);
+    const float y = sum > 0.f ? x / sum : sum != sum ? sum : 0.f;
+    const __nv_bfloat16 v = __float2bfloat16_rn(y);
+    static_cast<__nv_bfloat16*>(a.o.p)[b * a.o.sb + hq * a.o.sh + t * a.o.sn + c] = v;
+    if (a.rest != nullptr)
+      a.rest[((static_cast<size_t>(b) * a.Hq + hq) * a.n + t) * D + c] = __float2bfloat16_rn(y - __bfloat162float(v));
     if (c == 0)
       a.lse[(static_cast<size_t>(b) * a.Hq + hq) * a.n + t] = sum > 0.f || sum != sum ? (mx + log2f(sum)) * kLn2 : -kInf;
   }

@@ -459,9 +459,18 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
   const float inv_l = GRAD ? 1.f : l > 0.f ? 1.f / l : l != l ? l : 0.f;
   const View& out = GRAD ? a.gq : a.o;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out.p) + b * out.sb + (kh * a.group + h) * out.sh + t * out.sn;
+  __nv_bfloat16* rest = GRAD || a.rest == nullptr
+                            ? nullptr
+                            : a.rest + ((static_cast<size_t>(b) * a.Hq + kh * a.group + h) * a.n + t) * D;
 #pragma unroll
-  for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint32_t*>(o + part_column(ch, c)) = pack_bf16x2(acc[2 * c] * inv_l, acc[2 * c + 1] * inv_l);
+  for (int c = 0; c < 4; ++c) {
+    const float x = acc[2 * c] * inv_l, y = acc[2 * c + 1] * inv_l;
+    const uint32_t v = pack_bf16x2(x, y);
+    *reinterpret_cast<uint32_t*>(o + part_column(ch, c)) = v;
+    if (rest != nullptr)
+      *reinterpret_cast<uint32_t*>(rest + part_column(ch, c)) =
+          pack_bf16x2(x - __uint_as_float(v << 16), y - __uint_as_float(v & 0xffff0000u));
+  }
   if (!GRAD && ch == 0)
     a.lse[(static_cast<size_t>(b) * a.Hq + kh * a.group + h) * a.n + t] =
         l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -kInf;

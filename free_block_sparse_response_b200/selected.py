@@ -15,8 +15,9 @@ or, call by call, with a workspace that the caller keeps:
     ws = spr.selected_workspace(q, k, cfg, backward=True)
     means = spr.key_means(k, cfg.block)
     sel = spr.select_blocks(q, means, k.shape[2], cfg, ws)
-    out, lse = spr.selected_attn(q, k, v, sel, cfg, ws)
-    dq, dk, dv = spr.selected_attn_backward(dout, q, k, v, out, lse, sel, cfg, ws)
+    rest = torch.empty(q.shape, dtype=q.dtype, device=q.device)   # bf16 training: what out's rounding leaves off
+    out, lse = spr.selected_attn(q, k, v, sel, cfg, ws, rest=rest)
+    dq, dk, dv = spr.selected_attn_backward(dout, q, k, v, out, lse, sel, cfg, ws, rest=rest)
 
 For a cache, ``kv_len`` [batch] holds each sequence's length and ``q_start`` [batch] the key
 position of its first query; after appending keys, ``key_means(..., kv_start=, max_new=,
@@ -52,7 +53,8 @@ class _CRotary(ctypes.Structure):
 class _CSelected(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("dtype", "Bt", "Hq", "Hkv", "Nq", "Nk", "d", "block", "top", "causal",
                                               "n_first", "n_local")] + \
-               [("scale", ctypes.c_float), ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p)]
+               [("scale", ctypes.c_float), ("kv_len", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("out_rest", ctypes.c_void_p)]
 
 
 def signatures():
@@ -296,7 +298,7 @@ class SelectConfig:
 
 def _problem(dtype_of, bt, hq, hk, nq, nk, d, cfg: SelectConfig) -> _CSelected:
     return _CSelected(_s._dtype_code(dtype_of), bt, hq, hk, nq, nk, d, cfg.block, cfg.top, int(bool(cfg.causal)),
-                      cfg.n_first, cfg.n_local, cfg.scale, None, None)
+                      cfg.n_first, cfg.n_local, cfg.scale, None, None, None)
 
 
 def _lengths(bt: int, device, kv_len, q_start) -> None:
@@ -322,7 +324,7 @@ def selected_workspace(q: torch.Tensor, k: torch.Tensor, cfg: SelectConfig, back
 def _ws_size(dtype, bt, hq, hk, nq, nk, d, cfg: SelectConfig, backward: bool) -> int:
     """Workspace bytes of a problem: a function of its sizes alone."""
     p = _CSelected(dtype, bt, hq, hk, nq, nk, d, cfg.block, cfg.top, int(bool(cfg.causal)), cfg.n_first, cfg.n_local,
-                   cfg.scale, None, None)
+                   cfg.scale, None, None, None)
     return int(_s.lib().sparsepr_selected_workspace_size(ctypes.byref(p), 1 if backward else 0))
 
 
@@ -391,7 +393,7 @@ def _select_call(q, means, keys, cfg, ws, kv_len, q_start, out) -> _Call:
     return c
 
 
-def _attention_call(name, backward, cfg, ws, sel, kv_len, q_start, lse, q, k, v, others) -> _Call:
+def _attention_call(name, backward, cfg, ws, sel, kv_len, q_start, lse, rest, q, k, v, others) -> _Call:
     """Checks of both attention calls; ``others``: (name, tensor or None where the call makes it,
     the tensor whose shape it has, whether it is an output)."""
     _need_rows("q", q)
@@ -400,6 +402,9 @@ def _attention_call(name, backward, cfg, ws, sel, kv_len, q_start, lse, q, k, v,
     _need_rows("v", v, k.shape, q)
     _need_flat("sel", sel, (bt, k.shape[1], n, cfg.top), torch.int32, q.device)
     _need_flat("lse", lse, q.shape[:3], torch.float32, q.device)
+    if rest is not None and q.dtype != torch.bfloat16:
+        raise ValueError("rest goes with bf16 tensors")
+    _need_flat("rest", rest, q.shape, torch.bfloat16, q.device)
     _lengths(bt, q.device, kv_len, q_start)
     c = _Call(name, q.device)
     c.p = _problem(q, bt, hq, k.shape[1], n, k.shape[2], d, cfg)
@@ -416,24 +421,27 @@ def _attention_call(name, backward, cfg, ws, sel, kv_len, q_start, lse, q, k, v,
     return c
 
 
-def _fill(c: _Call, kv_len, q_start, *tensors) -> None:
-    c.p.kv_len, c.p.q_start = _ptr(kv_len), _ptr(q_start)
+def _fill(c: _Call, kv_len, q_start, rest, *tensors) -> None:
+    c.p.kv_len, c.p.q_start, c.p.out_rest = _ptr(kv_len), _ptr(q_start), _ptr(rest)
     for view, t in zip(c.views, tensors):
         view.data = t.data_ptr()
 
 
 def selected_attn(q, k, v, sel: torch.Tensor, cfg: SelectConfig, ws: torch.Tensor,
                   kv_len: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
-                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+                  out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                  rest: Optional[torch.Tensor] = None):
     """Softmax attention of every query over the keys of its selected blocks: (out, lse), out
-    like q and lse [batch, heads, rows] fp32 (natural log; -inf and a zero row without keys)."""
-    key = ("attn", cfg, _signature(q, k, v, sel, ws, kv_len, q_start, out, lse))
-    c = _prepared(key, _attention_call, "sparsepr_selected_attn", False, cfg, ws, sel, kv_len, q_start, lse, q, k, v,
+    like q and lse [batch, heads, rows] fp32 (natural log; -inf and a zero row without keys).
+    ``rest``: a contiguous bf16 tensor of q's shape that gets what the rounding of out left off,
+    for the backward call."""
+    key = ("attn", cfg, _signature(q, k, v, sel, ws, kv_len, q_start, out, lse, rest))
+    c = _prepared(key, _attention_call, "sparsepr_selected_attn", False, cfg, ws, sel, kv_len, q_start, lse, rest, q, k, v,
                   (("out", out, q, True),))
     _need_aligned(ws)
     out = _rows_like(q) if out is None else out
     lse = torch.empty(c.lse_shape, dtype=torch.float32, device=q.device) if lse is None else lse
-    _fill(c, kv_len, q_start, q, k, v, out)
+    _fill(c, kv_len, q_start, rest, q, k, v, out)
     r = c.refs
     c.run(c.p_ref, r[0], r[1], r[2], sel.data_ptr(), r[3], lse.data_ptr(), ws.data_ptr())
     return out, lse
@@ -441,22 +449,23 @@ def selected_attn(q, k, v, sel: torch.Tensor, cfg: SelectConfig, ws: torch.Tenso
 
 def selected_attn_backward(dout, q, k, v, out, lse, sel: torch.Tensor, cfg: SelectConfig, ws: torch.Tensor,
                            kv_len: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None, dq=None,
-                           dk=None, dv=None):
+                           dk=None, dv=None, rest: Optional[torch.Tensor] = None):
     """(dq, dk, dv) of ``selected_attn`` for the gradient of its output; the selection is fixed.
     ``ws`` was made with ``backward=True``.  An expanded k or v gets the gradient of every repeated
     head (add them up); the heads of a group are added already.  The row sums of dout * out are
-    formed from ``out`` as it is stored, so bf16 gradients carry its rounding."""
+    formed from ``out`` as it is stored, so bf16 gradients carry its rounding (it is dq's largest
+    error), unless ``rest`` of the forward call is given."""
     if lse is None:
         raise ValueError("lse of the forward call is needed")
-    key = ("grad", cfg, _signature(dout, q, k, v, out, lse, sel, ws, kv_len, q_start, dq, dk, dv))
-    c = _prepared(key, _attention_call, "sparsepr_selected_attn_backward", True, cfg, ws, sel, kv_len, q_start, lse, q, k, v,
-                  (("dout", dout, q, False), ("out", out, q, False), ("dq", dq, q, True), ("dk", dk, k, True),
-                   ("dv", dv, k, True)))
+    key = ("grad", cfg, _signature(dout, q, k, v, out, lse, sel, ws, kv_len, q_start, dq, dk, dv, rest))
+    c = _prepared(key, _attention_call, "sparsepr_selected_attn_backward", True, cfg, ws, sel, kv_len, q_start, lse, rest,
+                  q, k, v, (("dout", dout, q, False), ("out", out, q, False), ("dq", dq, q, True), ("dk", dk, k, True),
+                            ("dv", dv, k, True)))
     _need_aligned(ws)
     dq = _rows_like(q) if dq is None else dq
     dk = _rows_like(k) if dk is None else dk
     dv = _rows_like(k) if dv is None else dv
-    _fill(c, kv_len, q_start, q, k, v, dout, out, dq, dk, dv)
+    _fill(c, kv_len, q_start, rest, q, k, v, dout, out, dq, dk, dv)
     r = c.refs
     c.run(c.p_ref, r[3], r[0], r[1], r[2], r[4], lse.data_ptr(), sel.data_ptr(), r[5], r[6], r[7], ws.data_ptr())
     return dq, dk, dv

@@ -371,6 +371,9 @@ typedef struct sparsepr_selected {
   float scale;                       /* softmax scale; <= 0 selects 1/sqrt(d)           */
   const int32_t* kv_len;             /* [Bt] device, or NULL (Nk); clamped to [0, Nk]   */
   const int32_t* q_start;            /* [Bt] device, or NULL                            */
+  void* out_rest;                    /* [Bt, Hq, Nq, d] device, bf16, or NULL: what the
+                                        rounding of O left off.  The attention call writes it,
+                                        the backward call adds it to O (bf16 only)      */
 } sparsepr_selected;
 
 /* Bytes of workspace of the calls below on this problem (0 on invalid sizes); `backward`
@@ -404,7 +407,8 @@ SPARSEPR_API int sparsepr_selected_attn(const sparsepr_selected* p, const sparse
 
 /* Its backward pass for a fixed selection: dQ, dK, dV (all rows written, zero where nothing
  * contributes) from dO and the forward call's inputs, O and lse.  Sums over a block's
- * queries run in token order: the result is the same in every run. */
+ * queries run in token order: the result is the same in every run.  The row sums of dO * O
+ * take O as it is stored and, where it is given, out_rest. */
 SPARSEPR_API int sparsepr_selected_attn_backward(const sparsepr_selected* p, const sparsepr_view* dO,
                                                  const sparsepr_view* Q, const sparsepr_view* K, const sparsepr_view* V,
                                                  const sparsepr_view* O, const float* lse, const int32_t* sel,

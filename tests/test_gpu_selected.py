@@ -131,6 +131,68 @@ def test_backward_matches_the_formula(shape):
         close(g, w, U[dt] * w.abs() + U[dt] * s * 1.01 + E * e + 1e-30, name)
 
 
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[-1] is BF], ids=lambda s: "-".join(str(x) for x in s[:9]))
+def test_backward_with_the_rest_of_out(shape):
+    """out + rest holds the result past its rounding, and dq and dk lose that rounding: with delta from
+    out + rest the reference's delta is that of the exact out, off by u^2 + (u + e) of sum P |v| |dout|
+    (the rest's own rounding; the weights' rounding and fp32 sums of the forward pass)."""
+    q, k, v, lens, starts, cfg = problem(shape, 5)
+    bt, hq, n, d = q.shape
+    keys = k.shape[2]
+    dout = rnd(gen_of(6), *q.shape)
+    ws = spr.selected_workspace(q, k, cfg, backward=True)
+    sel = spr.select_blocks(q, spr.key_means(k, cfg.block, kv_len=lens), keys, cfg, ws, kv_len=lens, q_start=starts)
+    plain, _ = spr.selected_attn(q, k, v, sel, cfg, ws, kv_len=lens, q_start=starts)
+    rest = torch.full(q.shape, math.nan, dtype=BF, device=DEV)
+    out, lse = spr.selected_attn(q, k, v, sel, cfg, ws, kv_len=lens, q_start=starts, rest=rest)
+    got = spr.selected_attn_backward(dout, q, k, v, out, lse, sel, cfg, ws, kv_len=lens, q_start=starts, rest=rest)
+    spr.check(ws)
+    assert torch.equal(out, plain)
+    ok = R.mask(sel, n, keys, cfg.block, lens, starts, cfg.causal)
+    whole = out.double() + rest.double()
+    # at most half a step of out, itself rounded
+    assert (rest.double().abs() <= U[BF] * (1 + U[BF]) * out.double().abs() + 1e-38).all()
+    want, _, p = R.attention(q, k, v, ok, d ** -0.5)
+    size = p @ torch.where(ok.any(2)[..., None], v.double(), 0.0).abs().repeat_interleave(hq // k.shape[1], 1)
+    close(whole, want, U[BF] ** 2 * want.abs() + (U[BF] + E) * size + 1e-30, "out + rest")
+    # the rows that the backward pass forms delta from are these
+    grads, sizes, noise = R.backward(dout, q, k, v, ok, d ** -0.5, out=whole)
+    for name, g, w, s, e in zip(("dq", "dk", "dv"), got, grads, sizes, noise):
+        close(g, w, U[BF] * w.abs() + U[BF] * s * 1.01 + E * e + 1e-30, name)
+
+
+def test_the_rest_of_out_takes_its_rounding_from_dq():
+    """Rows whose values share a large part: delta of the rounded out is off by up to u |dout . out|, for
+    every key alike.  Here out is near 4, its rounding 0.009 rms, delta's error 0.009 sqrt(128) = 0.1, dq's
+    0.1 tau |sum P k| = 0.1 * 0.088 * 2 = 0.018 an element; with the rest what is left is the weights' rounding
+    in out (4.1 / 22 * 1.1e-3 = 2e-4, so 4e-4 of dq) and dS's (1e-4): a factor of 40, of which 10 are asked."""
+    q, k, v, lens, starts, cfg = problem((1, 2, 2, 600, 1024, 128, 128, 4, False, 0, 0, None, BF), 23)
+    v, k = (v.float() + 4).to(BF), (k.float() + 2).to(BF)
+    dout = rnd(gen_of(24), *q.shape)
+    ws = spr.selected_workspace(q, k, cfg, backward=True)
+    sel = spr.select_blocks(q, spr.key_means(k, 128), 1024, cfg, ws)
+    rest = torch.empty(q.shape, dtype=BF, device=DEV)
+    out, lse = spr.selected_attn(q, k, v, sel, cfg, ws, rest=rest)
+    want = R.backward(dout, q, k, v, R.mask(sel, 600, 1024, 128, lens, starts, False), 128 ** -0.5)[0][0]
+    dqs = (spr.selected_attn_backward(dout, q, k, v, out, lse, sel, cfg, ws, rest=r)[0] for r in (rest, None))
+    with_rest, without = (float((dq.double() - want).norm()) for dq in dqs)
+    assert with_rest < without / 10
+
+
+def test_the_rest_is_checked():
+    q, k, v, lens, starts, cfg = problem((1, 2, 2, 40, 200, 64, 64, 2, False, 0, 0, None, BF), 25)
+    ws = spr.selected_workspace(q, k, cfg)
+    sel = spr.select_blocks(q, spr.key_means(k, 64), 200, cfg, ws)
+    for bad in (torch.empty(1, 2, 40, 64, device=DEV), torch.empty(1, 2, 39, 64, dtype=BF, device=DEV),
+                torch.empty(1, 40, 2, 64, dtype=BF, device=DEV).transpose(1, 2)):
+        with pytest.raises(ValueError, match="rest"):
+            spr.selected_attn(q, k, v, sel, cfg, ws, rest=bad)
+    with pytest.raises(spr.SparsePRError, match="out_rest"):
+        spr.selected_attn(q, k, v, sel, cfg, ws, rest=torch.empty(2 * 40 * 64 + 1, dtype=BF, device=DEV)[1:].view(1, 2, 40, 64))
+    with pytest.raises(ValueError, match="bf16"):
+        spr.selected_attn(q.float(), k.float(), v.float(), sel, cfg, ws, rest=torch.empty(1, 2, 40, 64, device=DEV))
+
+
 def test_gradients_match_differences():
     """Central differences of the 64-bit loss along random directions, selection fixed."""
     q, k, v, lens, starts, cfg = problem((1, 4, 2, 200, 200, 64, 64, 2, True, 0, 1, None, F), 8)

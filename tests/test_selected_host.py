@@ -84,6 +84,16 @@ def test_null_and_misaligned_tensors_are_refused(L):
     assert L.sparsepr_selected_attn(p, ok, ok, ok, FAKE, ok, FAKE, None, None) == spr.ERR_INVALID_ARG
 
 
+def test_the_rest_of_out_is_checked(L):
+    v = view()
+    for kw, word in ((dict(dtype=spr.F32), b"bf16"), (dict(out_rest=4096 + 8), b"16-byte")):
+        p = problem(**{"out_rest": 4096, **kw})
+        assert L.sparsepr_selected_attn(p, v, v, v, FAKE, v, FAKE, FAKE, None) == spr.ERR_INVALID_ARG
+        assert word in L.sparsepr_last_error()
+        assert L.sparsepr_selected_attn_backward(p, v, v, v, v, v, FAKE, FAKE, v, v, v, FAKE, None) == spr.ERR_INVALID_ARG
+        assert word in L.sparsepr_last_error()
+
+
 def test_rows_that_repeat_are_refused_where_they_cannot_be(L):
     p, ok, flat = problem(Bt=2, Nq=10, Nk=300), view(b=1 << 20, h=1 << 16), view(b=1 << 20, h=1 << 16, n=0)
     one = view(b=0, h=1 << 16)
