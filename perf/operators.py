@@ -274,11 +274,13 @@ def _run_attend(s):
 
 
 def _run_train(s):
-    if own:
-        out, lse = s["spr"].selected_attn(s["q"], s["k"], s["v"], s["sel"], s["cfg"], s["ws"], kv_len=s["lens"],
-                                          q_start=s["starts"])
-        dq, dk, dv = s["spr"].selected_attn_backward(s["grad"], s["q"], s["k"], s["v"], out, lse, s["sel"], s["cfg"],
-                                                     s["ws"], kv_len=s["lens"], q_start=s["starts"])
+    if own:  # bf16: with what the rounding of out left off, which dq needs
+        q = s["q"]
+        rest = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q.dtype == torch.bfloat16 else None
+        out, lse = s["spr"].selected_attn(q, s["k"], s["v"], s["sel"], s["cfg"], s["ws"], kv_len=s["lens"],
+                                          q_start=s["starts"], rest=rest)
+        dq, dk, dv = s["spr"].selected_attn_backward(s["grad"], q, s["k"], s["v"], out, lse, s["sel"], s["cfg"],
+                                                     s["ws"], kv_len=s["lens"], q_start=s["starts"], rest=rest)
     else:
         out, dq, dk, dv = _plain_train(s["case"], s["q"], s["k"], s["v"], s["sel"], s["lens"], s["starts"], s["grad"])
     return {"out": out, "dq": dq, "dk": dk, "dv": dv}
