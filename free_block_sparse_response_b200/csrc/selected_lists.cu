@@ -220,10 +220,15 @@ __global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
 }
 
 __global__ void __launch_bounds__(512) scatter_kernel(const SelArgs a) {
-  extern __shared__ uint32_t mask[];  // [nb][kWords], then the words' first entries [nb][kWords]
+  // bits [nb][kWords], the blocks' first entries [nb], and from those the words' [nb][kWords]
+  extern __shared__ uint32_t mask[];
   const int z = blockIdx.y, s = blockIdx.x, t0 = s * kSub;
+  const int region = z * a.slices + s / a.subs, ls = s % a.subs;
+  int* first = reinterpret_cast<int*>(mask + a.nb * kWords);
+  uint16_t* before = reinterpret_cast<uint16_t*>(first + a.nb);
+  const int* offs = a.offs + static_cast<size_t>(region) * a.nb * a.subs + ls;
+  for (int g = threadIdx.x; g < a.nb; g += blockDim.x) first[g] = __ldg(offs + static_cast<size_t>(g) * a.subs);
   set_bits(a, mask, z, t0);
-  uint16_t* before = reinterpret_cast<uint16_t*>(mask + a.nb * kWords);
   for (int g = threadIdx.x; g < a.nb; g += blockDim.x) {
     int c = 0;
 #pragma unroll
@@ -233,14 +238,12 @@ __global__ void __launch_bounds__(512) scatter_kernel(const SelArgs a) {
     }
   }
   __syncthreads();
-  const int region = z * a.slices + s / a.subs, ls = s % a.subs;
   int* list = a.list + static_cast<size_t>(region) * a.slice * a.top;
-  const int* offs = a.offs + static_cast<size_t>(region) * a.nb * a.subs + ls;
   each_selected(a, z, t0, [&](int i, size_t at, int g) {
     int e = -1;
     if (g >= 0) {
       const int w = g * kWords + (i >> 5);
-      e = __ldg(offs + static_cast<size_t>(g) * a.subs) + before[w] + __popc(mask[w] & ((1u << (i & 31)) - 1u));
+      e = first[g] + before[w] + __popc(mask[w] & ((1u << (i & 31)) - 1u));
       list[e] = t0 + i;
     }
     a.inv[at] = e;
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(512) scatter_kernel(const SelArgs a) {
 cudaError_t launch_lists(const SelArgs& a, cudaStream_t st) {
   const int heads = a.Bt * a.Hk, subs = ceil_div(a.n, kSub);
   if (heads > 65535) return cudaErrorInvalidValue;
-  const size_t mask = sizeof(uint32_t) * a.nb * kWords, both = mask + sizeof(uint16_t) * a.nb * kWords;
+  const size_t mask = sizeof(uint32_t) * a.nb * kWords, both = mask + sizeof(int) * a.nb + sizeof(uint16_t) * a.nb * kWords;
   if (both > 227 * 1024) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(scatter_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
