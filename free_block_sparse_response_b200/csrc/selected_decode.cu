@@ -4,7 +4,7 @@
 // or a few per key head there is nothing to share a key tile with but the token's own group.
 // What bounds it: HBM, one read of the selected blocks' K and V; for a single sequence, latency.
 // 32 sequences x 8 key heads, 32 blocks of 64 keys: 268 MB in 71 us, 3.8 TB/s; one sequence, 16
-// blocks of 128: 10 us.
+// blocks of 128: 9 us.
 //
 // One cluster per (batch, key head, token, 16 query heads of the group); the keys of the
 // selected blocks are cut into pieces of 32, dealt to the cluster's warps.  A warp takes 16 keys
@@ -256,11 +256,15 @@ __global__ void __launch_bounds__(32 * kWarps, 2) decode_kernel(const SelArgs a,
 template <int D>
 cudaError_t decode(const SelArgs& a, cudaStream_t st) {
   const long long units = static_cast<long long>(a.Bt) * a.Hk * a.n * ceil_div(a.group, 16);
-  // Three CTAs fit an SM: the smallest cluster that gives four per SM, up to eight CTAs and to a
-  // warp for each piece.
+  // CTAs that the SMs hold at once: two an SM (three at d = 64).  The largest cluster that stays
+  // within that, up to eight CTAs and to a warp for each piece: a second wave costs its start and
+  // join again.  Measured, us at 1, 2, 4, 8 CTAs a cluster where tried (32 blocks of 64, 16 of 128,
+  // 16 of 64 keys): 256 clusters of d 128 53, 59, 68, 91; 192 53, 58, 54, 69; 64 -, -, 18, 23;
+  // 96 of d 64 -, 13.6, 10.8, 16.
+  constexpr int kSlots = (D == 128 ? 2 : 3) * 148;
   const int pieces = std::min(a.top, a.nb) * (a.block / kPiece);
   int splits = 1;
-  while (splits < 8 && units * splits < 4 * 148 && 2 * splits * kWarps <= pieces) splits *= 2;
+  while (splits < 8 && 2 * units * splits <= kSlots && 2 * splits * kWarps <= pieces) splits *= 2;
   if (units * splits > 0x7fffffffLL) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(units * splits));
