@@ -3,7 +3,7 @@
 // Mathematics as in selected_attn.cu, without the detour over the blocks' lists: with a token
 // or a few per key head there is nothing to share a key tile with but the token's own group.
 // What bounds it: HBM, one read of the selected blocks' K and V; for a single sequence, latency.
-// 32 sequences x 8 key heads, 32 blocks of 64 keys: 268 MB in 71 us, 3.8 TB/s; one sequence, 16
+// 32 sequences x 8 key heads, 32 blocks of 64 keys: 268 MB in 52 us, 5.1 TB/s; one sequence, 16
 // blocks of 128: 9 us.
 //
 // One cluster per (batch, key head, token, 16 query heads of the group); the keys of the
@@ -283,14 +283,15 @@ cudaError_t decode(const SelArgs& a, cudaStream_t st) {
 
 // Few tokens read the selected blocks once each and straight; the lists share a block's tile
 // between the tokens that selected it, at the price of five more launches and of tiles of 128 rows.
-// Direct up to 12 tokens, and while a block has at most two tokens on average (n top / nb).
-// Measured, direct and lists in us (replayed graphs, d 128; batch x key heads x group):
-//   1 x 8 x 4, 16 of 64 blocks of 128:  n = 1 11, 34;  8 23, 39;  16 43, 39;  64 92, 43
-//   8 x 8 x 1, 16 of 64 blocks of 128:  n = 1 27, 70;  8 98, 119;  16 156, 127
-//   1 x 8 x 8, 32 of 512 blocks of 64:  n = 1 13, 75;  32 67, 134;  64 105, 147;  128 164, 165
+// Direct up to 12 tokens, and while a block has at most three tokens on average (n top / nb).
+// Measured, direct and lists in us (replayed graphs; batch x key heads x group):
+//   1 x 8 x 4, d 128, 16 of 64 blocks of 128:  n = 1 9, 31;  8 15, 38;  16 24, 39;  32 39, 40
+//   8 x 8 x 1, d 128, 16 of 64 blocks of 128:  n = 1 18, 70;  8 84, 117;  12 119, 122;  16 154, 125
+//   1 x 8 x 8, d 128, 32 of 512 blocks of 64:  n = 1 10, 60;  32 47, 116;  64 87, 134;  128 163, 146
+//   4 x 4 x 2, d 64, 16 of 256 blocks of 64:   n = 1 7, 42;  32 34, 74;  64 52, 82;  128 87, 91
 bool use_decode(const SelArgs& a) {
   const long long n = static_cast<long long>(a.n) * ceil_div(a.group, 16);
-  return !a.f32 && n <= std::max<long long>(12, 2ll * a.nb / a.top);
+  return !a.f32 && n <= std::max<long long>(12, 3ll * a.nb / a.top);
 }
 
 cudaError_t launch_decode(const SelArgs& a, cudaStream_t st) {
