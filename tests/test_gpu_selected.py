@@ -596,6 +596,52 @@ def test_repeated_heads_and_batches_by_stride_zero():
     assert torch.equal(one, spr.block_attention(q[:, :, :1], k.contiguous(), v.contiguous(), cfg))
 
 
+def test_gradients_of_repeated_inputs():
+    """Queries, keys and output gradients that repeat in memory: what their copies give."""
+    gen = gen_of(48)
+    q = rnd(gen, 1, 4, 1, 64).expand(2, 4, 150, 64)
+    k, v = (rnd(gen, 1, 1, 300, 64).expand(2, 2, 300, 64) for _ in range(2))
+    dout = rnd(gen, 2, 1, 1, 64).expand(2, 4, 150, 64)
+    cfg = spr.SelectConfig(block=64, top=3)
+    res = []
+    for ins in ((q, k, v, dout), [t.contiguous() for t in (q, k, v, dout)]):
+        a, b, c, g = ins
+        ws = spr.selected_workspace(a, b, cfg, backward=True)
+        sel = spr.select_blocks(a, spr.key_means(b, 64), 300, cfg, ws)
+        out, lse = spr.selected_attn(a, b, c, sel, cfg, ws)
+        res.append((sel, out, lse) + spr.selected_attn_backward(g, a, b, c, out, lse, sel, cfg, ws))
+        spr.check(ws)
+    for x, y in zip(*res):
+        assert torch.equal(x, y)
+
+
+def test_given_outputs_are_written_whole_and_nothing_beside_them():
+    """out, lse, rest and the gradients into parts of wider buffers, selection and means in place."""
+    q, k, v, lens, starts, cfg = problem((2, 4, 2, 140, 300, 64, 64, 3, True, 0, 1, (300, 200), BF), 49)
+    dout = rnd(gen_of(50), *q.shape)
+    ws = spr.selected_workspace(q, k, cfg, backward=True)
+    means = spr.key_means(k, 64, kv_len=lens)
+    sel = spr.select_blocks(q, means, 300, cfg, ws, kv_len=lens, q_start=starts)
+    out, lse = spr.selected_attn(q, k, v, sel, cfg, ws, kv_len=lens, q_start=starts)
+    want = (out,) + spr.selected_attn_backward(dout, q, k, v, out, lse, sel, cfg, ws, kv_len=lens, q_start=starts)
+    sel2, means2 = torch.full_like(sel, 77), torch.full_like(means, 7.0)
+    spr.key_means(k, 64, kv_len=lens, out=means2)
+    spr.select_blocks(q, means2, 300, cfg, ws, kv_len=lens, q_start=starts, out=sel2)
+    assert torch.equal(means2, means) and torch.equal(sel2, sel)
+    wide = [torch.full((t.shape[0], t.shape[2] + 2, t.shape[1], 80), 3.0, dtype=BF, device=DEV) for t in want]
+    parts = [w[:, 1:-1, :, 8:72].transpose(1, 2) for w in wide]
+    lse2 = torch.full_like(lse, 7.0)
+    spr.selected_attn(q, k, v, sel, cfg, ws, kv_len=lens, q_start=starts, out=parts[0], lse=lse2)
+    spr.selected_attn_backward(dout, q, k, v, parts[0], lse2, sel, cfg, ws, kv_len=lens, q_start=starts, dq=parts[1],
+                               dk=parts[2], dv=parts[3])
+    spr.check(ws)
+    assert torch.equal(lse2, lse)
+    for t, p, w in zip(want, parts, wide):
+        assert torch.equal(t, p)
+        p.fill_(3.0)
+        assert (w == 3.0).all()
+
+
 def test_token_slices_of_a_large_call():
     """A head whose partial rows pass the workspace's chunk is worked off slice by slice: the same as
     calls on parts of the tokens."""
