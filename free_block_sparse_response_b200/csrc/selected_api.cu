@@ -92,7 +92,9 @@ SelArgs base_args(const sparsepr_selected* p) {
   a.Bt = p->Bt, a.Hq = p->Hq, a.Hk = p->Hkv, a.group = p->Hq / p->Hkv;
   a.n = p->Nq, a.nk = p->Nk, a.d = p->d;
   a.block = p->block, a.nb = spr::ceil_div(p->Nk, p->block), a.top = p->top;
-  a.n_first = p->n_first, a.n_local = p->n_local;
+  // A causal query's own block holds keys past the query: by its mean, later keys would decide about
+  // it.  So it is in whatever n_local says, unless the first blocks leave no room for a score at all.
+  a.n_first = p->n_first, a.n_local = p->causal && p->n_first < p->top ? std::max(p->n_local, 1) : p->n_local;
   a.q_start0 = p->Nk - p->Nq;
   a.kv_len = p->kv_len, a.q_start = p->q_start;
   a.rest = static_cast<__nv_bfloat16*>(p->out_rest);

@@ -287,7 +287,8 @@ def _rotary_call(plan, positions, q, k, inverse, qo, ko) -> _Call:
 class SelectConfig:
     """Attention over selected key blocks: keys per block (64 or 128), blocks per query, causal
     masking, blocks that are always selected (the first ``n_first``; causal: the query's own
-    block and the ``n_local`` - 1 before it) and the softmax scale (<= 0: 1/sqrt(d))."""
+    block, unless ``n_first`` = ``top``, and the ``n_local`` - 1 before it) and the softmax scale
+    (<= 0: 1/sqrt(d))."""
     block: int = 128
     top: int = 16
     causal: bool = False

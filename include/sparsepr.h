@@ -367,7 +367,9 @@ typedef struct sparsepr_selected {
   int32_t causal;
   int32_t n_first;                   /* the first n_first blocks are always selected    */
   int32_t n_local;                   /* causal: so are the query's own block and the
-                                        n_local - 1 before it; n_first + n_local <= top */
+                                        n_local - 1 before it; n_first + n_local <= top.
+                                        0 counts as 1 where n_first < top: the mean of the
+                                        own block would let later keys select it        */
   float scale;                       /* softmax scale; <= 0 selects 1/sqrt(d)           */
   const int32_t* kv_len;             /* [Bt] device, or NULL (Nk); clamped to [0, Nk]   */
   const int32_t* q_start;            /* [Bt] device, or NULL                            */
