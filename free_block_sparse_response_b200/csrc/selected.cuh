@@ -41,11 +41,9 @@ constexpr int kTcShares = 148;
 // One work item of the attention kernels: rows [r0, r0 + rows) of the entries of key block g,
 // whose first entry is `off` of its region's list; row r is query head r % group of entry r / group.
 // rows = 0: none.  live, qs: the length and the position of query 0, both from the block's first
-// key on.  total: the block's rows in this region.  k: power of two that the forward parts of
-// the block are divided by.
+// key on.  total: the block's rows in this region.  wide: a.wide of the block.
 struct __align__(16) Unit {
-  int g, off, r0, rows, live, qs, b, kh, total;
-  float k;
+  int g, off, r0, rows, live, qs, b, kh, total, wide;
   int pad[2];
 };
 
@@ -62,7 +60,9 @@ struct SelArgs {
   float* lse;            // [Bt, Hq, n]
   const float* means;    // [Bt, Hk, nb, d]
   int* status;
-  int* slow;             // select: number of rows left to select_row_kernel, then the rows
+  // number of rows that a call leaves to a second kernel, then the rows: select, [Bt, Hk, n] to
+  // select_row_kernel; attention in bf16, [Bt, Hq, n] to mend_kernel
+  int* slow;
   void* mean_parts;      // select: bf16 [Bt, Hk, nb][2][d], the means' hi and lo parts
   float* mean_norm2;     // select: [Bt, Hk, nb] squared norms of the means
   // lists: per region (batch, key head, slice of `slice` tokens), `slices` regions per head
@@ -78,10 +78,12 @@ struct SelArgs {
   // partial rows of one chunk of regions, [chunk regions][slice * top * group][d]: fp32, or fp16
   // with the columns of part_column() (selected_tc.cuh)
   float* part;
-  // statistics of each partial row.  fp32: its maximum (log2 units) and sum; fp16 forward: its
-  // log-sum-exp and the exponent that its values are to be multiplied by 2^ of; fp16 dQ: -, scale
+  // statistics of each partial row.  fp32: its maximum (log2 units) and sum; fp16 dQ: -, scale
   float2* ml;
-  float* vexp;           // [Bt * Hk][nb] Unit::k of each block (fp16 forward parts), or null
+  // fp16 forward: log-sum-exp (log2 units), the exponent and the factor that its values are to be
+  // multiplied by (2^ of the one, times the other), -
+  float4* stat;
+  int* wide;             // [Bt * Hk][nb] whether a block's parts take store_wide (bf16)
   float* delta;          // backward: sum of o * go per query row
   __nv_bfloat16* rest;   // [Bt, Hq, n, d] what the rounding of o left off, or null
   float* seg;            // backward: [chunk regions][seg_cap][2][block][d] sums of split blocks
@@ -99,8 +101,8 @@ __device__ __forceinline__ int q_start_of(const SelArgs& a, int b) {
 cudaError_t launch_key_means(const SelArgs& a, const int* kv_start, int max_new, float* means, cudaStream_t st);
 cudaError_t launch_select(const SelArgs& a, int* sel, cudaStream_t st);
 cudaError_t launch_lists(const SelArgs& a, cudaStream_t st);
-// Unit::k of every block into a.vexp, before the lists.
-cudaError_t launch_value_exponents(const SelArgs& a, cudaStream_t st);
+// a.wide from the blocks of v (whose sums the parts are), before the lists.
+cudaError_t launch_wide_blocks(const SelArgs& a, const View& v, cudaStream_t st);
 // One chunk of `count` regions starting at region `first`.
 cudaError_t launch_selected_forward(const SelArgs& a, int first, int count, cudaStream_t st);
 cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cudaStream_t st);
@@ -108,5 +110,7 @@ cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cud
 bool use_decode(const SelArgs& a);
 cudaError_t launch_decode(const SelArgs& a, cudaStream_t st);
 cudaError_t launch_delta(const SelArgs& a, cudaStream_t st);
+// The elements of the listed rows of a.o, or (grad) a.gq, that their parts could not hold.
+cudaError_t launch_mend(const SelArgs& a, bool grad, cudaStream_t st);
 
 }  // namespace spr

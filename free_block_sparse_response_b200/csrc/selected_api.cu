@@ -109,7 +109,7 @@ constexpr size_t kPartialBytes = 1ull << 30;
 // status header).
 struct Plan {
   int regions, chunk;  // chunk: regions per launch
-  size_t slow, mean_parts, mean_norm2, vexp, offs, list, inv, units, n_units, blk, part, ml, delta, seg, total;
+  size_t slow, mean_parts, mean_norm2, wide, offs, list, inv, units, n_units, blk, part, ml, delta, seg, total;
 };
 
 Plan make_plan(SelArgs& a, bool backward) {
@@ -117,7 +117,8 @@ Plan make_plan(SelArgs& a, bool backward) {
   const long long subs = spr::ceil_div(a.n, spr::kSub);
   // the tensor-core kernels keep their partial rows in fp16
   const size_t val = a.f32 ? sizeof(float) : 2;
-  const size_t row = val * a.d + sizeof(float2);
+  const size_t stats = a.f32 || backward ? sizeof(float2) : sizeof(float4);
+  const size_t row = val * a.d + stats;
   const size_t sub_bytes = row * spr::kSub * a.top * a.group;
   // A backward region is a head's whole token range, so that a key block's gradient is
   // formed by one region; a forward region is cut where its partial rows pass the chunk.
@@ -152,11 +153,11 @@ Plan make_plan(SelArgs& a, bool backward) {
     return at;
   };
   const size_t R = L.regions;
-  L.slow = take(sizeof(int) * (static_cast<size_t>(a.Bt) * a.Hk * a.n + 1));
+  L.slow = take(sizeof(int) * (static_cast<size_t>(a.Bt) * a.Hq * a.n + 1));
   const size_t means = static_cast<size_t>(a.Bt) * a.Hk * a.nb;
   L.mean_parts = take(backward ? 0 : 2 * 2 * means * a.d);
   L.mean_norm2 = take(backward ? 0 : sizeof(float) * means);
-  L.vexp = take(backward || a.f32 ? 0 : sizeof(float) * static_cast<size_t>(a.Bt) * a.Hk * a.nb);
+  L.wide = take(a.f32 ? 0 : sizeof(int) * means);
   L.offs = take(sizeof(int) * R * a.nb * a.subs);
   L.list = take(sizeof(int) * R * entries);
   L.inv = take(sizeof(int) * static_cast<size_t>(a.Bt) * a.Hk * a.n * a.top);
@@ -164,7 +165,7 @@ Plan make_plan(SelArgs& a, bool backward) {
   L.n_units = take(sizeof(int) * R);
   L.blk = take(sizeof(int4) * R * a.nb);
   L.part = take(val * a.d * rows * L.chunk);
-  L.ml = take(backward && a.f32 ? 0 : sizeof(float2) * rows * L.chunk);
+  L.ml = take(backward && a.f32 ? 0 : stats * rows * L.chunk);
   L.delta = take(backward ? sizeof(float) * static_cast<size_t>(a.Bt) * a.Hq * a.n : 0);
   L.seg = take(sizeof(float) * 2 * a.block * a.d *
                (!backward ? 0 : a.f32 ? static_cast<size_t>(a.seg_cap) * L.chunk : 2 * size_t{spr::kTcShares}));
@@ -182,6 +183,7 @@ void bind(SelArgs& a, const Plan& L, void* ws) {
   a.slow = at<int>(ws, L.slow);
   a.mean_parts = at<char>(ws, L.mean_parts);
   a.mean_norm2 = at<float>(ws, L.mean_norm2);
+  a.wide = at<int>(ws, L.wide);
   a.offs = at<int>(ws, L.offs);
   a.list = at<int>(ws, L.list);
   a.inv = at<int>(ws, L.inv);
@@ -190,6 +192,7 @@ void bind(SelArgs& a, const Plan& L, void* ws) {
   a.blk = at<int4>(ws, L.blk);
   a.part = at<float>(ws, L.part);
   a.ml = at<float2>(ws, L.ml);
+  a.stat = at<float4>(ws, L.ml);
   a.delta = at<float>(ws, L.delta);
   a.seg = at<float>(ws, L.seg);
 }
@@ -293,15 +296,13 @@ int sparsepr_selected_attn(const sparsepr_selected* p, const sparsepr_view* Q, c
   bind(a, L, ws);
   a.q = view(Q), a.k = view(K), a.v = view(V), a.o = view(O), a.sel = sel, a.lse = lse;
   if (spr::use_decode(a)) return cuda_status(spr::launch_decode(a, st), "selected attention: few tokens");
-  if (!a.f32) {
-    a.vexp = at<float>(ws, L.vexp);
-    if ((rc = cuda_status(spr::launch_value_exponents(a, st), "selected attention: value exponents"))) return rc;
-  }
+  if (!a.f32 && (rc = cuda_status(spr::launch_wide_blocks(a, a.v, st), "selected attention: ranges"))) return rc;
   if ((rc = cuda_status(spr::launch_lists(a, st), "selected attention: lists"))) return rc;
   for (int r = 0; r < L.regions; r += L.chunk)
     if ((rc = cuda_status(spr::launch_selected_forward(a, r, std::min(L.chunk, L.regions - r), st), "selected attention")))
       return rc;
-  return SPARSEPR_OK;
+  if (a.f32) return SPARSEPR_OK;
+  return cuda_status(spr::launch_mend(a, false, st), "selected attention: values outside the parts' range");
 }
 
 int sparsepr_selected_attn_backward(const sparsepr_selected* p, const sparsepr_view* dO, const sparsepr_view* Q,
@@ -325,12 +326,14 @@ int sparsepr_selected_attn_backward(const sparsepr_selected* p, const sparsepr_v
   a.gq = view(dQ), a.gk = view(dK), a.gv = view(dV);
   a.sel = sel, a.lse = const_cast<float*>(lse);
   if ((rc = cuda_status(spr::launch_delta(a, st), "selected attention backward: row sums"))) return rc;
+  if (!a.f32 && (rc = cuda_status(spr::launch_wide_blocks(a, a.k, st), "selected attention backward: ranges"))) return rc;
   if ((rc = cuda_status(spr::launch_lists(a, st), "selected attention backward: lists"))) return rc;
   for (int r = 0; r < L.regions; r += L.chunk)
     if ((rc = cuda_status(spr::launch_selected_backward(a, r, std::min(L.chunk, L.regions - r), st),
                           "selected attention backward")))
       return rc;
-  return SPARSEPR_OK;
+  if (a.f32) return SPARSEPR_OK;
+  return cuda_status(spr::launch_mend(a, true, st), "selected attention backward: values outside the parts' range");
 }
 
 }  // extern "C"

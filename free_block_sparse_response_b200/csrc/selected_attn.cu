@@ -56,6 +56,122 @@ __device__ __forceinline__ void load_block(float* dst, const View& v, int b, int
   }
 }
 
+// ------------------------------------------------------------------------------ rows formed again
+
+// A query row straight from the inputs in fp32:
+//   sum_j P_j v_j, or (GRAD) sum_j dS_j k_j, over the visible keys of its selected blocks.
+// Keys that the row does not see are not touched, so that whatever they hold (a NaN times a weight of
+// 0 is a NaN) does not reach it.  D / V lanes take a key, V columns each; warp `warp` of `warps` takes
+// its share of the keys, kBatch at a time in flight, and x gets its sums of columns V (lane % (D / V)) ..
+template <typename T, int D, bool GRAD>
+__device__ __noinline__ void sum_again(const SelArgs& a, int z, int t, int h, float lse2, float delta, int warp, int warps,
+                                       float* x) {
+  constexpr int V = 16 / sizeof(T), L = D / V, kKeys = 32 / L, kBatch = 4;
+  const int lane = threadIdx.x & 31, ch = lane % L, b = z / a.Hk, kh = z % a.Hk, hq = kh * a.group + h;
+  auto piece = [&](const View& v, int hv, int j) { return *reinterpret_cast<const uint4*>(row_ptr<const T>(v, b, hv, j) + ch * V); };
+  auto at = [](const uint4& v, int c) { return to_f32<T>(reinterpret_cast<const T*>(&v)[c]); };
+  const uint4 q = piece(a.q, hq, t), go = GRAD ? piece(a.go, hq, t) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int c = 0; c < V; ++c) x[c] = 0.f;
+  const size_t slots = (static_cast<size_t>(z) * a.n + t) * a.top;
+  const int last = a.causal ? min(kv_len_of(a, b) - 1, q_start_of(a, b) + t) : kv_len_of(a, b) - 1;
+  const int keys = lse2 == -__builtin_huge_valf() ? 0 : a.top * a.block;  // (a zero row of the forward pass)
+  const float scale2 = a.scale * kLog2e;
+  for (int i0 = warp * kKeys * kBatch; i0 < keys; i0 += warps * kKeys * kBatch) {
+    uint4 k[kBatch], v[kBatch];
+    bool live[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kKeys + lane / L, s = i / a.block;
+      const int j = i < keys && a.inv[slots + s] >= 0 ? a.sel[slots + s] * a.block + i % a.block : last + 1;
+      live[u] = j <= last;
+      k[u] = live[u] ? piece(a.k, kh, j) : make_uint4(0, 0, 0, 0);
+      v[u] = live[u] ? piece(a.v, kh, j) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      float s = 0.f, dp = 0.f;
+#pragma unroll
+      for (int c = 0; c < V; ++c) {
+        s = fmaf(at(q, c), at(k[u], c), s);
+        if (GRAD) dp = fmaf(at(go, c), at(v[u], c), dp);
+      }
+#pragma unroll
+      for (int o = L / 2; o > 0; o >>= 1) {
+        s += __shfl_xor_sync(0xffffffffu, s, o);
+        if (GRAD) dp += __shfl_xor_sync(0xffffffffu, dp, o);
+      }
+      if (!live[u]) continue;
+      const float p = exp2f(fmaf(s, scale2, -lse2)), w = GRAD ? p * (dp - delta) * a.scale : p;
+#pragma unroll
+      for (int c = 0; c < V; ++c) x[c] = fmaf(w, GRAD ? at(k[u], c) : at(v[u], c), x[c]);
+    }
+  }
+#pragma unroll
+  for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+    for (int c = 0; c < V; ++c) x[c] += __shfl_xor_sync(0xffffffffu, x[c], o);
+}
+
+// fp32: the NaNs of a row (columns D / 32 lane ..) in place of which it has a value, by the row's warp.
+template <int D, bool GRAD>
+__device__ __forceinline__ void mend_row(const SelArgs& a, int z, int t, int h, float lse2, float delta, float (&y)[D / 32]) {
+  bool open = false;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) open = open || y[c] != y[c];
+  if (!__any_sync(0xffffffffu, open)) return;
+  const int lane = threadIdx.x & 31;
+  float x[4];
+  sum_again<float, D, GRAD>(a, z, t, h, lse2, delta, 0, 1, x);
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c) {
+    float w = x[c];
+    if (D == 64) {  // four columns a lane there, two here
+      const float u = __shfl_sync(0xffffffffu, x[c], lane / 2), v = __shfl_sync(0xffffffffu, x[c + 2], lane / 2);
+      w = lane & 1 ? v : u;
+    }
+    if (y[c] != y[c]) y[c] = w;
+  }
+}
+
+// bf16: the rows that the joins listed, a CTA each: rows of blocks that are wide (wide_blocks_kernel) with a
+// value that fp16 cannot hold beside the row's largest, hidden NaNs and infinities among them.  (In the
+// joins themselves, as in fp32, this would take twice their registers, and they live from the warps
+// under way.)
+constexpr int kMendWarps = 16;
+
+template <int D, bool GRAD>
+__global__ void __launch_bounds__(32 * kMendWarps) mend_kernel(const __grid_constant__ SelArgs a) {
+  __shared__ float s_x[kMendWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rows = __ldg(a.slow);
+  for (int i = blockIdx.x; i < rows; i += gridDim.x) {
+    const int row = __ldg(a.slow + 1 + i), t = row % a.n, hq = row / a.n % a.Hq, b = row / a.n / a.Hq;
+    const float lse = a.lse[row];
+    if (lse != lse) continue;  // a NaN that the row sees
+    float x[8];
+    sum_again<__nv_bfloat16, D, GRAD>(a, b * a.Hk + hq / a.group, t, hq % a.group, lse * kLog2e, GRAD ? a.delta[row] : 0.f, warp,
+                                      kMendWarps, x);
+    if (lane < D / 8) {
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s_x[warp][lane * 8 + c] = x[c];
+    }
+    __syncthreads();
+    if (threadIdx.x < D) {
+      const int c = threadIdx.x;
+      float y = 0.f;
+#pragma unroll
+      for (int w = 0; w < kMendWarps; ++w) y += s_x[w][c];
+      __nv_bfloat16* o = row_ptr<__nv_bfloat16>(GRAD ? a.gq : a.o, b, hq, t) + c;
+      if (__hisnan(*o)) {
+        *o = __float2bfloat16_rn(y);
+        if (!GRAD && a.rest != nullptr)
+          a.rest[static_cast<size_t>(row) * D + c] = __float2bfloat16_rn(y - __bfloat162float(*o));
+      }
+    }
+    __syncthreads();
+  }
+}
+
 // ------------------------------------------------------------------------------ forward
 
 constexpr int kFwdThreads = 128, kFwdRows = 64;
@@ -177,7 +293,7 @@ __global__ void __launch_bounds__(kFwdThreads) forward_kernel(const SelArgs a, i
 // One warp per query row: joins the row's parts.  Lane s holds slot s's statistics; then
 // the lanes cover the row's columns and walk the parts.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) join_kernel(const SelArgs a, int first, int count) {
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ SelArgs a, int first, int count) {
   constexpr int C = D / 32;
   const int lane = threadIdx.x & 31;
   const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -221,10 +337,13 @@ __global__ void __launch_bounds__(256) join_kernel(const SelArgs a, int first, i
     }
   }
   l = warp_sum(l);
-  const float inv_l = l > 0.f ? 1.f / l : 0.f;
+  const float inv_l = l > 0.f ? 1.f / l : l == l ? 0.f : l;
+#pragma unroll
+  for (int c = 0; c < C; ++c) acc[c] *= inv_l;
+  if (l == l) mend_row<D, false>(a, z, t, h, ms + log2f(l), 0.f, acc);
   T* o = row_ptr<T>(a.o, b, kh * a.group + h, t) + lane * C;
 #pragma unroll
-  for (int c = 0; c < C; ++c) o[c] = from_f32<T>(acc[c] * (l == l ? inv_l : l));
+  for (int c = 0; c < C; ++c) o[c] = from_f32<T>(acc[c]);
   if (lane == 0)
     a.lse[(static_cast<size_t>(b) * a.Hq + kh * a.group + h) * a.n + t] =
         l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -__builtin_huge_valf();
@@ -441,7 +560,7 @@ __global__ void __launch_bounds__(256) join_kv_kernel(const SelArgs a, int first
 
 // One warp per query row: dQ is the sum of the row's partial rows, slot by slot.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) join_q_kernel(const SelArgs a, int first, int count) {
+__global__ void __launch_bounds__(256) join_q_kernel(const __grid_constant__ SelArgs a, int first, int count) {
   constexpr int C = D / 32;
   const int lane = threadIdx.x & 31;
   const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
@@ -461,6 +580,8 @@ __global__ void __launch_bounds__(256) join_q_kernel(const SelArgs a, int first,
 #pragma unroll
     for (int c = 0; c < C; ++c) acc[c] += p[c];
   }
+  const size_t at = (static_cast<size_t>(z / a.Hk) * a.Hq + z % a.Hk * a.group + h) * a.n + t;
+  if (a.lse[at] == a.lse[at]) mend_row<D, true>(a, z, t, h, a.lse[at] * kLog2e, a.delta[at], acc);
   T* o = row_ptr<T>(a.gq, z / a.Hk, z % a.Hk * a.group + h, t) + lane * C;
 #pragma unroll
   for (int c = 0; c < C; ++c) o[c] = from_f32<T>(acc[c]);
@@ -518,6 +639,14 @@ cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cud
   if (a.d == 128)
     return a.block == 128 ? backward<float, 128, 128>(a, first, count, st) : backward<float, 128, 64>(a, first, count, st);
   return a.block == 128 ? backward<float, 64, 128>(a, first, count, st) : backward<float, 64, 64>(a, first, count, st);
+}
+
+cudaError_t launch_mend(const SelArgs& a, bool grad, cudaStream_t st) {
+  if (a.d == 128)
+    grad ? mend_kernel<128, true><<<2 * 148, 32 * kMendWarps, 0, st>>>(a) : mend_kernel<128, false><<<2 * 148, 32 * kMendWarps, 0, st>>>(a);
+  else
+    grad ? mend_kernel<64, true><<<2 * 148, 32 * kMendWarps, 0, st>>>(a) : mend_kernel<64, false><<<2 * 148, 32 * kMendWarps, 0, st>>>(a);
+  return counted(cudaGetLastError(), 1);
 }
 
 cudaError_t launch_delta(const SelArgs& a, cudaStream_t st) {

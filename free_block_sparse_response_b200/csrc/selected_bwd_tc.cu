@@ -216,18 +216,25 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         const int lane0 = 32 * w4 + 16 * half;
-        uint32_t o[D / 2];
-#pragma unroll
-        for (int c = 0; c < D; c += 64)
-          tmem_ld_16x64(tDp + (static_cast<uint32_t>(lane0) << 16) + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c / 2]));
-        tc::tmem_wait_ld();
-        if (half == 1) {
-          tc::fence_before_sync();
-          tc::mbar_arrive(bar(kDqFree));
-        }
-        const float one[2] = {1.f, 1.f};
+        const uint32_t tRow = tDp + (static_cast<uint32_t>(lane0) << 16);
         float up[2];
-        store_part<D>(o, one, lane0 + q, un.rows, part + 32 * i, out0, up);
+        if (un.wide) {
+          store_wide<D>(tRow, lane0 + q, un.rows, part + 32 * i, out0, up);
+          if (half == 1) {
+            tc::fence_before_sync();
+            tc::mbar_arrive(bar(kDqFree));
+          }
+        } else {
+          uint32_t o[D / 2];
+#pragma unroll
+          for (int c = 0; c < D; c += 64) tmem_ld_16x64(tRow + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c / 2]));
+          tc::tmem_wait_ld();
+          if (half == 1) {
+            tc::fence_before_sync();
+            tc::mbar_arrive(bar(kDqFree));
+          }
+          store_part<D>(o, lane0 + q, un.rows, part + 32 * i, out0, up);
+        }
         if (i == 0) {
 #pragma unroll
           for (int k = 0; k < 2; ++k)

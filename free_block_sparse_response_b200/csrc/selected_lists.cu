@@ -215,9 +215,10 @@ __global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
     for (int i = lane; i < nu; i += 32)
       a.units[static_cast<size_t>(region) * a.unit_cap + k.w + i] =
           Unit{g, k.x, i * a.unit_rows, min(a.unit_rows, rows - i * a.unit_rows), len - g * a.block, qs - g * a.block, b,
-               z % a.Hk, rows, a.vexp == nullptr ? 0.f : __ldg(a.vexp + static_cast<size_t>(z) * a.nb + g), {}};
+               z % a.Hk, rows, a.f32 ? 0 : __ldg(a.wide + static_cast<size_t>(z) * a.nb + g), {}};
   }
   if (threadIdx.x == 0) a.n_units[region] = unit0;
+  if (threadIdx.x == 0 && region == 0) *a.slow = 0;
   // the kernels on the fp32 pipes launch a CTA for every unit there may be
   if (a.f32)
     for (int u = unit0 + threadIdx.x; u < a.unit_cap; u += 512)

@@ -4,11 +4,12 @@
 // query rows that selected it.  K and V of the block stay in shared memory; 128 rows at a time
 //   S = Q K^T (128 x B),  P = exp(S - row max),  O = P V (128 x D)
 // need no running maximum, since one tile holds all the keys of the row's part.  The part goes
-// out in fp16, with its log-sum-exp; join_half_kernel adds a row's parts.  So that O needs no
-// scaling on its way out, P is formed as exp(S - row max) 2^-k: with |V| < 2^e in the block
-// (value_exponents_kernel), k = e + log2 B - 15 keeps |O| <= 2^15, inside fp16, and leaves its 11
-// bits to everything down to 2^-29 of that bound.  A part's rounding, 2^-12, is 16 times finer
-// than the result's bf16; fp32 parts would double the traffic of the output and the join.
+// out in fp16 with a power of two and its log-sum-exp; join_half_kernel adds a row's parts.  A
+// part's rounding, 2^-12, is 16 times finer than the result's bf16; fp32 parts would double the
+// traffic of the output and the join.  The power of two is the row's own (store_part), so that a row
+// is the same to the bit whatever the keys hold that it does not see.  Blocks of V that span too much for
+// fp16 (wide_blocks_kernel) are watched on their way out (store_wide), and what does not fit is
+// formed again from the inputs in fp32 (mend_kernel).
 //
 // Work of a tile (B = D = 128): 8.4 MFLOP, 16K exponentials, 32 KB of Q gathered, 32 KB written.
 // A tile passes through five stages of ~1 us (gather, S, softmax, O, output), so one persistent
@@ -48,7 +49,7 @@ constexpr float kInf = __builtin_huge_valf();
 constexpr int kThreads = 640, kLoaders = 128;
 constexpr int kRegSoftmax = 112, kRegOut = 136, kRegRest = 56;
 constexpr int kOutWarp = 8, kLoadWarp = 12, kMmaWarp = 16, kKvWarp = 18;
-constexpr float kFold = 60.f;  // the part of k that P takes; the rest (values above 2^68) the output
+constexpr float kRoom = 8.f;  // P is 2^-8 at most, so that O, 128 terms, stays below the largest |V|
 
 template <int D, int B>
 struct Fwd {
@@ -157,8 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (cut) mask_from(s, nv - c0);
           max_into(mx, s);
         }
-        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2, kf = fminf(un.k, kFold);
-        const float shift = (m == -kInf ? 0.f : m) + kf;
+        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2, shift = (m == -kInf ? 0.f : m) + kRoom;
         const uint64_t sc2 = f32x2(scale2, scale2), nm2 = f32x2(-shift, -shift);
         uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
         const uint32_t sP = sSlot + (t % R) * F::kSlot;  // over Q, which S has read
@@ -188,8 +188,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         f32x2_split(sum[1], l2, l3);
         const float l = (l0 + l1) + (l2 + l3);  // not above 0: no visible key (or a NaN, which stays one)
         if (row < un.rows)
-          a.ml[(ci * cap + un.off) * a.group + un.r0 + row] =
-              l > 0.f || l != l ? make_float2(shift + __log2f(l), shift + (un.k - kf)) : make_float2(-kInf, -kInf);
+          *reinterpret_cast<float2*>(a.stat + (ci * cap + un.off) * a.group + un.r0 + row) =
+              l > 0.f || l != l ? make_float2(shift + __log2f(l), shift) : make_float2(-kInf, -kInf);
         return true;
     });
   } else if (warp < kLoadWarp) {
@@ -209,20 +209,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const int lane0 = 32 * w4 + 16 * half;
-          uint32_t o[D / 2];
+          const uint32_t tRow = tO + (static_cast<uint32_t>(lane0) << 16);
+          float up[2];
+          if (un.wide) {
+            store_wide<D>(tRow, lane0 + q, un.rows, part + 32 * i, out0, up);
+            if (half == 1) {
+              tc::fence_before_sync();
+              tc::mbar_arrive(bar(kOFree + x));
+            }
+          } else {
+            uint32_t o[D / 2];
 #pragma unroll
-          for (int c = 0; c < D; c += 64)
-            tmem_ld_16x64(tO + (static_cast<uint32_t>(lane0) << 16) + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c / 2]));
-          tc::tmem_wait_ld();
-          if (un.k > kFold) {
-            const float f = exp2f(kFold - un.k);
-#pragma unroll
-            for (int c = 0; c < D / 2; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            for (int c = 0; c < D; c += 64) tmem_ld_16x64(tRow + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c / 2]));
+            tc::tmem_wait_ld();
+            if (half == 1) {
+              tc::fence_before_sync();
+              tc::mbar_arrive(bar(kOFree + x));
+            }
+            store_part<D>(o, lane0 + q, un.rows, part + 32 * i, out0, up);
           }
-          store_part_as_is<D>(o, lane0 + q, un.rows, part + 32 * i, out0);
+          if (i == 0) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              if (lane0 + q + 8 * k < un.rows) a.stat[out0 + lane0 + q + 8 * k].z = up[k];
+          }
         }
-        tc::fence_before_sync();
-        tc::mbar_arrive(bar(kOFree + x));
         return true;
     });
   } else if (warp < kMmaWarp) {
@@ -402,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // the parts' bytes, pieces of 256 in the tokens' order: 4.2 to 5.1 TB/s.  (Walking eight rows a
 // group of lanes, with weights and entries asked for ahead, was slower: 186 against 175 us.)
 template <int D, bool GRAD>
-__global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int first, int count) {
+__global__ void __launch_bounds__(256, 6) join_half_kernel(const SelArgs a, int first, int count) {
   constexpr int kPer = D / 8, kRowsW = 32 / kPer;
   const int lane = threadIdx.x & 31, ch = lane % kPer;
   const long long w = (static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5)) * kRowsW + lane / kPer;
@@ -419,7 +430,13 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
   float m = -kInf, l = 0.f, acc[8] = {};
   for (int j0 = 0; j0 < a.top; j0 += kPer) {
     const int e = live && j0 + ch < a.top ? __ldg(inv + j0 + ch) : -1;
-    const float2 st = e >= 0 ? __ldcs(a.ml + row0 + static_cast<size_t>(e) * a.group) : make_float2(-kInf, GRAD ? 0.f : -kInf);
+    float4 st = make_float4(-kInf, GRAD ? 0.f : -kInf, 0.f, 0.f);
+    if (e >= 0) {
+      if (GRAD)
+        st.y = __ldcs(a.ml + row0 + static_cast<size_t>(e) * a.group).y;
+      else
+        st = __ldcs(a.stat + row0 + static_cast<size_t>(e) * a.group);
+    }
     float f = st.y;
     if (!GRAD) {
       float mx = st.x;
@@ -429,7 +446,7 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
       const float ms = mx == -kInf ? 0.f : mx, old = exp2f(m - ms), wt = exp2f(st.x - ms);
       m = mx;
       l = fmaf(l, old, wt);
-      f = exp2f(st.y - ms);
+      f = exp2f(st.y - ms) * st.z;
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] *= old;
     }
@@ -460,7 +477,13 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
   }
 #pragma unroll
   for (int o = kPer / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  // a part could not hold some of its row (a NaN): on the list for mend_kernel
+  float any = 0.f;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) any += acc[c];
+  const unsigned open = __ballot_sync(0xffffffffu, live && any != any) >> (lane - ch);
   if (!live) return;
+  if ((open & ((1u << kPer) - 1u)) != 0 && ch == 0) a.slow[1 + atomicAdd(a.slow, 1)] = (b * a.Hq + kh * a.group + h) * a.n + t;
   const float inv_l = GRAD ? 1.f : l > 0.f ? 1.f / l : l != l ? l : 0.f;
   const View& out = GRAD ? a.gq : a.o;
   __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out.p) + b * out.sb + (kh * a.group + h) * out.sh + t * out.sn;
@@ -481,36 +504,52 @@ __global__ void __launch_bounds__(256) join_half_kernel(const SelArgs a, int fir
         l > 0.f || l != l ? (m + log2f(l)) * kLn2 : -kInf;
 }
 
-// Unit::k of each block: e + log2 B - 15 with |V| < 2^e over the block's finite values.
+// Larger magnitudes of pairs of bf16 values (signs of no meaning); a NaN is the largest.
+__device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Which blocks are wide: they hold a value that is not finite, or columns whose largest magnitudes'
+// exponents are more than 24 apart (columns of zeros aside).  What the parts of the others may lose, 2^-39
+// of a row's largest value, is at most 2^-14 of any column's largest.  One CTA a block, bound by
+// the read of the tensor.
 template <int D>
-__global__ void __launch_bounds__(256) value_exponents_kernel(const SelArgs a) {
-  constexpr int kPer = D / 8, kRows = 256 / kPer;
-  __shared__ int s_max;
-  const int g = blockIdx.x, kh = blockIdx.y, b = blockIdx.z;
-  const int rows = min(a.block, kv_len_of(a, b) - g * a.block);
-  if (threadIdx.x == 0) s_max = 0;
-  __syncthreads();
-  const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.v.p) + b * a.v.sb + kh * a.v.sh +
-                           static_cast<long long>(g) * a.block * a.v.sn + threadIdx.x % kPer * 8;
-  int mx = 0;  // largest magnitude's bits: ordered as integers, without sign
+__global__ void __launch_bounds__(256) wide_blocks_kernel(const SelArgs a, const View x) {
+  constexpr int L = D / 8, kRows = 256 / L;
+  __shared__ uint4 s_mx[8][L];
+  const int g = blockIdx.x, kh = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rows = min(a.block, kv_len_of(a, b) - g * a.block), ch = threadIdx.x % L;
+  const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(x.p) + b * x.sb + kh * x.sh +
+                           static_cast<long long>(g) * a.block * x.sn + ch * 8;
+  uint32_t mx[4] = {};  // by column
+  auto add = [&](const uint4& v) {
+    mx[0] = max_abs_bf16x2(mx[0], v.x), mx[1] = max_abs_bf16x2(mx[1], v.y);
+    mx[2] = max_abs_bf16x2(mx[2], v.z), mx[3] = max_abs_bf16x2(mx[3], v.w);
+  };
 #pragma unroll 4
-  for (int r = threadIdx.x / kPer; r < rows; r += kRows) {
-    const uint4 x = *reinterpret_cast<const uint4*>(v + r * a.v.sn);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  for (int r = threadIdx.x / L; r < rows; r += kRows) add(*reinterpret_cast<const uint4*>(p + r * x.sn));
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int lo = static_cast<int>(w[i] & 0x7fffu), hi = static_cast<int>(w[i] >> 16 & 0x7fffu);
-      mx = max(mx, max(lo < 0x7f80 ? lo : 0, hi < 0x7f80 ? hi : 0));
-    }
-  }
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  if ((threadIdx.x & 31) == 0) atomicMax(&s_max, mx);
+  for (int o = L; o < 32; o <<= 1)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mx[w] = max_abs_bf16x2(mx[w], __shfl_xor_sync(0xffffffffu, mx[w], o));
+  if (lane < L) s_mx[warp][lane] = make_uint4(mx[0], mx[1], mx[2], mx[3]);
   __syncthreads();
-  if (threadIdx.x == 0) {
-    const int e = (s_max >> 7) - 126;  // |V| < 2^e
-    a.vexp[(static_cast<size_t>(b) * a.Hk + kh) * a.nb + g] =
-        s_max == 0 ? 0.f : static_cast<float>(max(e + (a.block == 128 ? 7 : 6) - 15, -100));
-  }
+  if (warp > 0) return;
+#pragma unroll
+  for (int w = 1; w < 8; ++w) add(s_mx[w][ch]);
+  uint32_t top = 0, low = 0x7fffu;
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+#pragma unroll
+    for (int k = 0; k < 32; k += 16) {
+      const uint32_t u = mx[w] >> k & 0x7fffu;
+      top = max(top, u);
+      if (u != 0) low = min(low, u);
+    }
+  top = __reduce_max_sync(0xffffffffu, top), low = __reduce_min_sync(0xffffffffu, low);
+  if (lane == 0) a.wide[(static_cast<size_t>(b) * a.Hk + kh) * a.nb + g] = top >= 0x7f80u || (top >> 7) > (low >> 7) + 24;
 }
 
 template <int D, int B>
@@ -533,9 +572,9 @@ cudaError_t forward(const SelArgs& a, int first, int count, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_value_exponents(const SelArgs& a, cudaStream_t st) {
+cudaError_t launch_wide_blocks(const SelArgs& a, const View& v, cudaStream_t st) {
   const dim3 grid(a.nb, a.Hk, a.Bt);
-  a.d == 128 ? value_exponents_kernel<128><<<grid, 256, 0, st>>>(a) : value_exponents_kernel<64><<<grid, 256, 0, st>>>(a);
+  a.d == 128 ? wide_blocks_kernel<128><<<grid, 256, 0, st>>>(a, v) : wide_blocks_kernel<64><<<grid, 256, 0, st>>>(a, v);
   return counted(cudaGetLastError(), 1);
 }
 

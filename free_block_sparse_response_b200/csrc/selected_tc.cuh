@@ -96,6 +96,13 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&r)[32])
       : "r"(taddr));
 }
 
+// The same for 8 columns.
+__device__ __forceinline__ void tmem_ld_16x8(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x1.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(taddr));
+}
+
 // Partial rows of 2 D bytes, 128-byte lines of 64 columns.  First column of the c-th pair of
 // 16-byte chunk `ch` of a row (8 chunks a line): the four lanes of a quad, which hold columns
 // 2 i, 2 i + 1 of every eight, write 32 bytes each.
@@ -134,6 +141,11 @@ __device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
@@ -145,13 +157,12 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
-// Powers of two with big * down in [1/2, 1) and up * down = 1 (0 and non-finite values: as
-// the nearest exponent that has both).
-__device__ __forceinline__ void pow2_scale(float big, float& up, float& down) {
-  int e = static_cast<int>((__float_as_uint(big) >> 23) & 255u) + 1;
-  e = min(max(e, 1), 253);
-  up = __uint_as_float(static_cast<uint32_t>(e) << 23);
-  down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+// Powers of two with big * down in [2^14, 2^15), the upper end of fp16, and up * down = 1 (below
+// 2^-112: as for 2^-112).
+__device__ __forceinline__ void part_scale(float big, float& up, float& down) {
+  const uint32_t e = max(__float_as_uint(big) >> 23, 15u);
+  up = __uint_as_float((e - 14) << 23);
+  down = __uint_as_float((268 - e) << 23);
 }
 
 // The tensor-core kernels run one CTA per SM; CTA c takes tiles [sum c / shares, sum (c + 1) /
@@ -205,7 +216,7 @@ __device__ __forceinline__ bool each_tile(const SelArgs& a, int first, const int
     Unit un;
     un.g = get(rec.g), un.off = get(rec.off), un.r0 = get(rec.r0), un.rows = get(rec.rows), un.live = get(rec.live);
     un.qs = get(rec.qs), un.b = get(rec.b), un.kh = get(rec.kh), un.total = get(rec.total);
-    un.k = __int_as_float(get(__float_as_int(rec.k)));
+    un.wide = get(rec.wide);
     const bool closes = (ends >> src) & 1u;
     if (!f(un, get(rec_ci), t, u, opens, closes)) return false;
     opens = closes;
@@ -214,13 +225,17 @@ __device__ __forceinline__ bool each_tile(const SelArgs& a, int first, const int
   return true;
 }
 
+constexpr float kSmallestHalf = 0x1p-14f;  // the smallest normal fp16
+
 // Rows r and r + 8 of a tile, held by the quad's lanes as tmem_ld_16x64 leaves them (D / 2
-// registers), times f[k], to the partial rows out0 + r of a chunk: fp16 with the row's largest
-// magnitude scaled to [1/2, 1); up[k] is the power of two that undoes it.  The two rows go side
-// by side, since this is bound by its latencies.  `part` is the lane's 32 bytes of row 0.
+// registers), to the partial rows out0 + r of a chunk: fp16, the row's largest magnitude scaled to
+// [2^14, 2^15), so that 11 bits are left to everything down to 2^-29 of it and the rest is off by at
+// most 2^-39 of it; up[k] is the power of two that undoes it.  The scale is the row's own, so that what a row cannot see does not reach it.  The
+// two rows go side by side, since this is bound by its latencies.  `part` is the lane's 32 bytes
+// of row 0.  For blocks that are not wide (wide_blocks_kernel).
 template <int D>
-__device__ __forceinline__ void store_part(const uint32_t (&o)[D / 2], const float (&f)[2], int r, int rows, uint8_t* part,
-                                           long long out0, float (&up)[2]) {
+__device__ __forceinline__ void store_part(const uint32_t (&o)[D / 2], int r, int rows, uint8_t* part, long long out0,
+                                           float (&up)[2]) {
   float big[2][2] = {}, mx[2], g[2];
 #pragma unroll
   for (int c = 0; c < D / 2; c += 8)
@@ -234,21 +249,19 @@ __device__ __forceinline__ void store_part(const uint32_t (&o)[D / 2], const flo
 #pragma unroll
     for (int k = 0; k < 2; ++k) mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], m));
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    float down;
-    pow2_scale(mx[k] * f[k], up[k], down);
-    g[k] = f[k] * down;
-  }
+  for (int k = 0; k < 2; ++k) part_scale(mx[k], up[k], g[k]);
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     if (r + 8 * k >= rows) continue;
+    const uint64_t g2 = f32x2(g[k], g[k]);
 #pragma unroll
     for (int c = 0; c < D; c += 64) {
       uint32_t h[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const __half2 v = __floats2half2_rn(__uint_as_float(o[c / 2 + 4 * j + 2 * k]) * g[k],
-                                            __uint_as_float(o[c / 2 + 4 * j + 2 * k + 1]) * g[k]);
+        float x, y;
+        f32x2_split(fmul2(f32x2(__uint_as_float(o[c / 2 + 4 * j + 2 * k]), __uint_as_float(o[c / 2 + 4 * j + 2 * k + 1])), g2), x, y);
+        const __half2 v = __floats2half2_rn(x, y);
         h[j] = *reinterpret_cast<const uint32_t*>(&v);
       }
       st_global_32(part + (out0 + r + 8 * k) * (2 * D) + c * 2, h);
@@ -256,22 +269,47 @@ __device__ __forceinline__ void store_part(const uint32_t (&o)[D / 2], const flo
   }
 }
 
-// The same without a scale: the values are inside fp16.
+// The same straight from TMEM for any values.  One that fp16 cannot hold beside the row's largest (smaller
+// than 2^-29 of it, infinite, or a NaN, as 0 times a hidden NaN is) goes out as a NaN, which the
+// row's sum keeps; mend_kernel then forms it again from the inputs.  Eight columns at a time, twice
+// (the largest first): ~10 us a tile, but small.  Wider or unrolled code here, though never run,
+// took the kernels from 850 to 880 us and more (16 heads x 32,760 tokens, 16 of 256 blocks).
 template <int D>
-__device__ __forceinline__ void store_part_as_is(const uint32_t (&o)[D / 2], int r, int rows, uint8_t* part,
-                                                 long long out0) {
+__device__ __forceinline__ void store_wide(uint32_t taddr, int r, int rows, uint8_t* part, long long out0, float (&up)[2]) {
+  float mx[2] = {}, g[2];
+  uint32_t o[4];
+#pragma unroll 1
+  for (int j = 0; j < D / 8; ++j) {
+    tmem_ld_16x8(taddr + 8 * j, o);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float x = fabsf(__uint_as_float(o[c]));
+      mx[c >> 1] = fmaxf(mx[c >> 1], x < __builtin_huge_valf() ? x : 0.f);
+    }
+  }
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    if (r + 8 * k >= rows) continue;
+    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+    part_scale(mx[k], up[k], g[k]);
+  }
+#pragma unroll 1
+  for (int j = 0; j < D / 8; ++j) {
+    tmem_ld_16x8(taddr + 8 * j, o);
+    tc::tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < D; c += 64) {
-      uint32_t h[8];
+    for (int k = 0; k < 2; ++k) {
+      float y[2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const __half2 v = __floats2half2_rn(__uint_as_float(o[c / 2 + 4 * j + 2 * k]), __uint_as_float(o[c / 2 + 4 * j + 2 * k + 1]));
-        h[j] = *reinterpret_cast<const uint32_t*>(&v);
+      for (int c = 0; c < 2; ++c) {
+        const float x = __uint_as_float(o[2 * k + c]);
+        y[c] = x * g[k];
+        if (x != 0.f && !(fabsf(y[c]) >= 0x1p-14f && fabsf(y[c]) < 0x1p16f)) y[c] = __builtin_nanf("");
       }
-      st_global_32(part + (out0 + r + 8 * k) * (2 * D) + c * 2, h);
+      if (r + 8 * k < rows)
+        *reinterpret_cast<__half2*>(part + (out0 + r + 8 * k) * (2 * D) + (j >> 3) * 128 + (j & 7) * 4) =
+            __floats2half2_rn(y[0], y[1]);
     }
   }
 }

@@ -357,8 +357,9 @@ SPARSEPR_API int sparsepr_rotary(const sparsepr_rotary_params* p, const double* 
  * key head and one selection.  Keys at or past kv_len[b] do not exist: their K and V rows
  * are not read (they may hold anything).  causal: query i sits at key position
  * q_start[b] + i and sees keys up to it; q_start NULL: Nk - Nq (the queries are the last
- * ones).  A NaN or infinity in a key or value row that exists reaches every query that
- * selected its block, causally hidden rows of the query's own block included. */
+ * ones).  Keys that a query does not see, causally hidden ones of its own block too, reach neither
+ * its output and log-sum-exp nor its dQ, whatever they hold; a NaN or infinity in a query or in dO
+ * reaches dK and dV of every key of the blocks that it selected. */
 typedef struct sparsepr_selected {
   int32_t dtype;                     /* of Q, K, V and the results                      */
   int32_t Bt, Hq, Hkv, Nq, Nk, d;    /* d 64 or 128                                     */

@@ -2,13 +2,14 @@
 
 Tolerances as counted in test_gpu_selected.py, from which the helpers come.
 """
+import math
 
 import pytest
 import torch
 
 import free_block_sparse_response_b200 as spr
 import selected_reference as R
-from test_gpu_selected import _built, DEV, gen_of, rnd  # noqa: F401
+from test_gpu_selected import _built, BF, close, DEV, E, F, gen_of, problem, rnd, U  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +67,128 @@ def test_a_selection_of_first_blocks_alone_takes_nothing_else():
     want = torch.tensor([0, 1], dtype=torch.int32, device=DEV).expand(1, 2, n, 2).clone()
     want[:, :, :64, 1] = -1
     assert torch.equal(sel, want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+@pytest.mark.parametrize("times", [0.1, 3.0, 100.0])
+def test_causal_rows_are_the_same_to_the_bit_whatever_comes_later(times, dtype):
+    """The whole call on two inputs that differ from a key on: the rows before it."""
+    gen = gen_of(83)
+    n, at = 500, 333
+    q, k, v = (rnd(gen, 2, h, n, 128, dtype=dtype) for h in (4, 2, 2))
+    cfg = spr.SelectConfig(block=128, top=3, causal=True)
+    res = []
+    for later in (False, True):
+        if later:
+            k[:, :, at:], v[:, :, at:] = (times * rnd(gen, 2, 2, n - at, 128, dtype=dtype) for _ in range(2))
+        res.append(spr.block_attention(q, k, v, cfg)[:, :, :at].clone())
+    assert torch.equal(*res)
+
+
+HIDDEN = [(1e30, BF), (-1e38, BF), (math.nan, BF), (math.inf, BF), (1e30, F), (math.nan, F), (-math.inf, F)]
+
+
+@pytest.mark.parametrize("d,block", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("what", ["k", "v"])
+@pytest.mark.parametrize("value,dtype", HIDDEN, ids=str)
+def test_hidden_keys_of_the_own_block_do_not_reach_a_query(d, block, what, value, dtype):
+    """Rows before the keys that hold `value` are as without them: output, log-sum-exp and dq, through
+    the lists; to the bit where the value is finite."""
+    n, at = 300, 200
+    q, k, v, lens, starts, cfg = problem((1, 4, 2, n, n, d, block, 2, True, 0, 1, None, dtype), 73)
+    dout = rnd(gen_of(74), *q.shape, dtype=dtype)
+    ws = spr.selected_workspace(q, k, cfg, backward=True)
+    sel = spr.select_blocks(q, spr.key_means(k, block), n, cfg, ws)
+    bad = {"k": k.clone(), "v": v.clone()}
+    bad[what][:, :, at:] = value
+    res = []
+    for kk, vv in ((k, v), (bad["k"], bad["v"])):
+        out, lse = spr.selected_attn(q, kk, vv, sel, cfg, ws)
+        dq = spr.selected_attn_backward(dout, q, kk, vv, out, lse, sel, cfg, ws)[0]
+        res.append([t[:, :, :at].clone() for t in (out, lse, dq)])
+    spr.check(ws)
+    if math.isfinite(value):
+        assert all(torch.equal(a, b) for a, b in zip(*res))
+    ok = R.mask(sel, n, n, block, lens, starts, True)
+    want, wlse, p = R.attention(q, k, v, ok, d ** -0.5)
+    size = p @ v.double().abs().repeat_interleave(2, 1)
+    out, lse, dq = res[1]
+    close(out, want[:, :, :at], (U[dtype] * want.abs() + (U[dtype] + E) * size)[:, :, :at], "out")
+    close(lse, wlse[:, :, :at], 1e-5 * (1 + wlse[:, :, :at].abs()), "lse")
+    whole = torch.cat([out, want[:, :, at:].to(dtype)], 2)
+    grads, sizes, noise = R.backward(dout, q, k, v, ok, d ** -0.5, out=whole)
+    bound = U[dtype] * grads[0].abs() + U[dtype] * sizes[0] * 1.01 + E * noise[0]
+    close(dq, grads[0][:, :, :at], bound[:, :, :at], "dq")
+
+
+@pytest.mark.parametrize("n", [1, 3, 11])
+@pytest.mark.parametrize("value", [1e30, math.nan, -math.inf])
+def test_hidden_keys_do_not_reach_a_query_of_a_few_tokens(n, value):
+    """The same for a few tokens inside a longer cache: keys past a token's own position."""
+    q, k, v, lens, starts, cfg = problem((1, 4, 2, n, 300, 128, 64, 2, True, 0, 1, None, BF), 75)
+    starts = torch.full_like(starts, 200 - n)
+    bad = {"k": k.clone(), "v": v.clone()}
+    bad["k"][:, :, 200:], bad["v"][:, :, 200:] = value, value
+    ws = spr.selected_workspace(q, k, cfg)
+    sel = spr.select_blocks(q, spr.key_means(k, 64, kv_len=starts + n), 300, cfg, ws, q_start=starts)
+    want = spr.selected_attn(q, k, v, sel, cfg, ws, q_start=starts)
+    got = spr.selected_attn(q, bad["k"], bad["v"], sel, cfg, ws, q_start=starts)
+    spr.check(ws)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+# ------------------------------------------------------------------- ranges
+
+@pytest.mark.parametrize("n,d,block", [(3, 128, 64), (200, 128, 64), (300, 128, 128), (200, 64, 64), (333, 64, 128)])
+@pytest.mark.parametrize("size", [1e3, 1e8, 1e30])
+def test_one_large_column_leaves_the_others(size, n, d, block):
+    """Columns of very different sizes: each is as exact as its own values allow."""
+    q, k, v, lens, starts, cfg = problem((1, 4, 2, n, 640, d, block, 4, False, 0, 0, None, BF), 76)
+    v[..., 7] = (v[..., 7].float() * size).to(BF)
+    v[..., 9] = (v[..., 9].float() / size).to(BF)
+    v[..., 11] = 0
+    ws = spr.selected_workspace(q, k, cfg)
+    sel = spr.select_blocks(q, spr.key_means(k, block), 640, cfg, ws)
+    rest = torch.empty_like(q)
+    out, _ = spr.selected_attn(q, k, v, sel, cfg, ws, rest=rest)
+    spr.check(ws)
+    want, _, p = R.attention(q, k, v, R.mask(sel, n, 640, block, lens, starts, False), d ** -0.5)
+    wide = p @ v.double().abs().repeat_interleave(2, 1)
+    close(out, want, U[BF] * want.abs() + (U[BF] + E) * wide + 1e-37, "out")
+    close(out.double() + rest.double(), want, U[BF] ** 2 * want.abs() + (U[BF] + E) * wide + 1e-37, "out + rest")
+    assert (out[..., 11] == 0).all()
+
+
+@pytest.mark.parametrize("n", [3, 200])
+@pytest.mark.parametrize("size", [1e6, 1e20, 1e38])
+def test_a_value_of_no_weight_leaves_the_others(size, n):
+    """A key whose weight is exp(-250) and less, beside which its value is very large."""
+    q, k, v, lens, starts, cfg = problem((1, 2, 2, n, 512, 128, 128, 3, False, 0, 0, None, BF), 84)
+    q = q.abs()
+    k[:, :, 70], v[:, :, 70] = -40, size
+    ws = spr.selected_workspace(q, k, cfg)
+    sel = torch.tensor([0, 1, 3], dtype=torch.int32, device=DEV).expand(1, 2, n, 3).contiguous()
+    out, _ = spr.selected_attn(q, k, v, sel, cfg, ws)
+    want, _, p = R.attention(q, k, v, R.mask(sel, n, 512, 128, lens, starts, False), 128 ** -0.5)
+    assert float(p[..., 70].max()) < 1e-100
+    wide = p @ v.double().abs()
+    close(out, want, U[BF] * want.abs() + (U[BF] + E) * wide, "out")
+
+
+@pytest.mark.parametrize("d,block", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("size", [1e3, 1e8, 1e30])
+def test_one_large_key_column_leaves_the_gradients_of_others(size, d, block):
+    """dq in the columns beside one of very large keys (where the queries hold zeros)."""
+    q, k, v, lens, starts, cfg = problem((1, 2, 2, 200, 640, d, block, 3, False, 0, 0, None, BF), 77)
+    q[..., 7] = 0
+    k[..., 7] = (k[..., 7].float() * size).to(BF)
+    dout = rnd(gen_of(78), *q.shape)
+    ws = spr.selected_workspace(q, k, cfg, backward=True)
+    sel = spr.select_blocks(q, spr.key_means(k, block), 640, cfg, ws)
+    out, lse = spr.selected_attn(q, k, v, sel, cfg, ws)
+    got = spr.selected_attn_backward(dout, q, k, v, out, lse, sel, cfg, ws)
+    spr.check(ws)
+    ok = R.mask(sel, 200, 640, block, lens, starts, False)
+    grads, sizes, noise = R.backward(dout, q, k, v, ok, d ** -0.5, out=out)
+    for name, g, w, s, e in zip(("dq", "dk", "dv"), got, grads, sizes, noise):
+        close(g, w, U[BF] * w.abs() + U[BF] * s * 1.01 + E * e + 1e-30, name)
