@@ -214,6 +214,7 @@ __global__ void __launch_bounds__(256) split_means_kernel(const SelArgs a, int r
 }
 
 // Tiles of ROWS tokens of one (batch, key head) against 64 blocks at a time.
+constexpr int kMostSmem = 227 * 1024;
 constexpr int kChunk = 64, kTileWarps = 16, kTileThreads = 32 * kTileWarps;
 
 template <int D, int ROWS, bool QLO = true>
@@ -501,7 +502,8 @@ cudaError_t tile_select(const SelArgs& a, int* sel, cudaStream_t st) {
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
   const size_t smem = tile_smem<D, ROWS, QLO>(a.nb);
   auto kern = select_tile_kernel<T, D, ROWS, VPL, QLO>;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  // (the same in every call: the limit is the kernel's, and another host thread may be about to launch it)
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
   if (e != cudaSuccess) return e;
   kern<<<dim3(ceil_div(a.n, ROWS), a.Bt * a.Hk), kTileThreads, smem, st>>>(a, sel, a.slow + 1);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
@@ -521,12 +523,11 @@ cudaError_t tile_select(const SelArgs& a, int* sel, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t select_blocks(const SelArgs& a, int* sel, cudaStream_t st) {
   if (static_cast<long long>(a.Bt) * a.Hk * a.n <= 4 * 148) return row_select<T, D>(a, sel, nullptr, st);
-  constexpr size_t kMost = 227 * 1024;
-  if (a.nb <= 640 && tile_smem<D, 64>(a.nb) <= kMost) {
+  if (a.nb <= 640 && tile_smem<D, 64>(a.nb) <= kMostSmem) {
     if (a.nb <= 128) return tile_select<T, D, 64, 4>(a, sel, st);
     return a.nb <= 256 ? tile_select<T, D, 64, 8>(a, sel, st) : tile_select<T, D, 64, 20>(a, sel, st);
   }
-  if (tile_smem<D, 32>(a.nb) <= kMost)
+  if (tile_smem<D, 32>(a.nb) <= kMostSmem)
     return a.nb <= 640 ? tile_select<T, D, 32, 20>(a, sel, st) : tile_select<T, D, 32, 0>(a, sel, st);
   return tile_select<T, D, 16, 0>(a, sel, st);
 }

@@ -3,6 +3,7 @@
 Tolerances as counted in test_gpu_selected.py, from which the helpers come.
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -192,3 +193,37 @@ def test_one_large_key_column_leaves_the_gradients_of_others(size, d, block):
     grads, sizes, noise = R.backward(dout, q, k, v, ok, d ** -0.5, out=out)
     for name, g, w, s, e in zip(("dq", "dk", "dv"), got, grads, sizes, noise):
         close(g, w, U[BF] * w.abs() + U[BF] * s * 1.01 + E * e + 1e-30, name)
+
+
+# ------------------------------------------------------------------- selection
+
+def test_two_threads_select_among_different_numbers_of_blocks():
+    """Host threads with workspaces and streams of their own: neither sees the other's sizes."""
+    errors, results = [], {}
+
+    def work(i, nb):
+        try:
+            gen = gen_of(81 + i)
+            q, mean = rnd(gen, 1, 2, 640, 64), rnd(gen, 1, 2, nb, 64, dtype=F)
+            cfg = spr.SelectConfig(block=64, top=5)
+            stream = torch.cuda.Stream()
+            stream.wait_stream(torch.cuda.default_stream())
+            with torch.cuda.stream(stream):
+                ws = spr.selected_workspace(q, torch.zeros(1, 2, nb * 64, 64, device=DEV, dtype=BF), cfg)
+                for _ in range(3000):
+                    sel = spr.select_blocks(q, mean, nb * 64, cfg, ws)
+            stream.synchronize()
+            spr.check(ws)
+            results[i] = (q, mean, nb, sel)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in ((0, 20), (1, 128), (2, 64))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for q, mean, nb, sel in results.values():
+        lens = torch.tensor([nb * 64], device=DEV)
+        assert torch.equal(sel, R.select(q, mean, nb * 64, 64, 5, lens, torch.zeros_like(lens), False, 0, 0))
