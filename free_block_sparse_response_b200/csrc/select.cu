@@ -350,8 +350,10 @@ __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs
     const int local = max(0, min(sc.mine + 1, sc.cand) - l0), forced = f0 + local;
     const int want = min(a.top, sc.cand);
     const bool split = forced < want && want < sc.cand;  // some of the others, not all or none
-    // the bound holds where nothing in it or in the products overflows or drops out of the normal range
-    if (split && !(e2 < 0x1p100f && qn[r] > 0x1p-60f && mnorm > 0x1p-60f && e2 > 0x1p-90f)) {
+    // The bound holds where nothing in it or in the products overflows or drops out of the normal range.
+    // A score may be a NaN only where a norm is not finite: the row kernel looks, whether it decides or not.
+    const bool odd = forced < sc.cand && !(qn[r] < kInf && mnorm < kInf);
+    if (odd || (split && !(e2 < 0x1p100f && qn[r] > 0x1p-60f && mnorm > 0x1p-60f && e2 > 0x1p-90f))) {
       if (lane == 0) list[atomicAdd(list - 1, 1)] = static_cast<int>(w);
       continue;
     }

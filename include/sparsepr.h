@@ -394,8 +394,8 @@ SPARSEPR_API int sparsepr_key_means(const sparsepr_selected* p, const sparsepr_v
 /* Selected blocks of every query, sel [Bt, Hkv, Nq, top] int32: of the blocks that hold a
  * key the query sees, the forced ones (n_first, n_local), then those with the largest
  * (sum of the group's queries) . mean, ties to the lower block; ascending, then -1.  The
- * scores are compared as exact 64-bit values.  A NaN score ranks lowest and records
- * SPARSEPR_ERR_NONFINITE in the status word. */
+ * scores are compared as exact 64-bit values.  A NaN score of a block that is not forced ranks
+ * lowest and records SPARSEPR_ERR_NONFINITE in the status word, whether the block is selected or not. */
 SPARSEPR_API int sparsepr_select_blocks(const sparsepr_selected* p, const sparsepr_view* Q, const float* means,
                                         int32_t* sel, void* ws, sparsepr_stream_t stream);
 

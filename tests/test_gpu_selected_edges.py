@@ -197,6 +197,32 @@ def test_one_large_key_column_leaves_the_gradients_of_others(size, d, block):
 
 # ------------------------------------------------------------------- selection
 
+@pytest.mark.parametrize("n", [4, 700])
+@pytest.mark.parametrize("top", [3, 6, 9])
+@pytest.mark.parametrize("where", ["query", "mean"])
+def test_nan_scores_are_reported_by_every_path(n, top, where):
+    """A NaN score of any row is reported, also where the row takes all of its blocks."""
+    gen = gen_of(79)
+    q, mean = rnd(gen, 1, 2, n, 64), rnd(gen, 1, 2, 6, 64, dtype=F)
+    if where == "query":
+        q[0, 1, n // 2, 5] = math.nan
+    else:
+        mean[0, 1, 4, 5] = math.nan
+    cfg = spr.SelectConfig(block=64, top=top)
+    ws = spr.selected_workspace(q, torch.zeros(1, 2, 384, 64, device=DEV, dtype=BF), cfg)
+    sel = spr.select_blocks(q, mean, 384, cfg, ws)
+    with pytest.raises(spr.SparsePRError) as e:
+        spr.check(ws)
+    assert e.value.code == spr.ERR_NONFINITE
+    if where == "mean" and top < 6:
+        assert not (sel[0, 1] == 4).any()
+    # a forced block's score decides nothing and is not one
+    cfg = spr.SelectConfig(block=64, top=6, n_first=6)
+    ws = spr.selected_workspace(q, torch.zeros(1, 2, 384, 64, device=DEV, dtype=BF), cfg)
+    spr.select_blocks(q, mean, 384, cfg, ws)
+    spr.check(ws)
+
+
 def test_two_threads_select_among_different_numbers_of_blocks():
     """Host threads with workspaces and streams of their own: neither sees the other's sizes."""
     errors, results = [], {}
