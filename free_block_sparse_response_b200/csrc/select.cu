@@ -6,10 +6,14 @@
 //
 //   1. Scores s~ of a tile of queries from bf16 hi + lo parts on the tensor cores.  With
 //      x = hi + lo + r, |lo| <= 2^-9 |x| and |r| <= 2^-18 |x|, the products hi hi + hi lo + lo hi
-//      leave out at most 3 * 2^-18 sum |q||m|, and eight chained fp32 accumulations add at most
-//      2^-18 of it: |s~ - s| <= e = 2^-16 |q| max |m_g| (Cauchy-Schwarz; for a group, |q| is the
-//      norm of the sum of magnitudes, which also covers the fp32 sum over the heads).  Single
-//      bf16 queries have no lo part: two products, 2 * 2^-18, e = 2^-17 |q| max |m_g|.
+//      leave out at most 3 * 2^-18 sum |q||m| (single bf16 queries have no lo part: two products, 2 *
+//      2^-18).  A product of 16 columns adds 17 numbers in an order and with an internal rounding
+//      that are not specified; cutting each off 2^-23 below the largest, eight of them in a row lose at
+//      most 8 * 17 * 2^-23, and 2^-8 of that twice in the lo products.  In all 2.8e-5, and 2^-15 is
+//      3.05e-5.  The sum of a group's G queries in fp32 adds G - 1 roundings, 2^-24 each, of their
+//      magnitudes: |s~ - s| <= e = (2^-15 + (G - 1) 2^-23) |q| max |m_g| (Cauchy-Schwarz; |q| is the
+//      norm of the group's sum of magnitudes, the second term twice what it has to be, which covers
+//      the rounding of that sum).
 //   2. The k-th and (k+1)-th largest s~, a and b.  Scores above b + 2e are in and scores below
 //      a - 2e are out whatever the rounding; with a - b > 2e nothing is left between.
 //   3. The few blocks between are compared by their scores in 64 bits.
@@ -338,13 +342,14 @@ __global__ void __launch_bounds__(kTileThreads) select_tile_kernel(const SelArgs
   }
   __syncthreads();
   const float mnorm = sqrtf(__int_as_float(*mmax));
+  const float margin = 0x1p-14f + 0x1p-22f * static_cast<float>(a.group - 1);
   int* my_open = open + warp * 32;
   for (int r = warp; r < ROWS && t0 + r < a.n; r += kTileWarps) {
     const long long w = static_cast<long long>(z) * a.n + t0 + r;
     int* out = sel + w * a.top;
     const Scope sc = scope_of(a, b, t0 + r);
     const float* sr = score + r * ld;
-    const float e2 = (QLO ? 0x1p-15f : 0x1p-16f) * qn[r] * mnorm;  // 2e
+    const float e2 = margin * qn[r] * mnorm;  // 2e
     // forced: [0, f0) and [l0, l0 + local)
     const int f0 = min(a.n_first, sc.cand), l0 = max(f0, sc.mine - a.n_local + 1);
     const int local = max(0, min(sc.mine + 1, sc.cand) - l0), forced = f0 + local;

@@ -223,6 +223,41 @@ def test_nan_scores_are_reported_by_every_path(n, top, where):
     spr.check(ws)
 
 
+def test_the_sum_of_a_large_group_is_decided_in_64_bits():
+    """2,049 heads, the first 2^24 times the others, whose sum in 32 bits is lost beside it: the exact
+    difference of the two blocks' scores is +2048, without them -2048, and 2^-16 |q| |m| is 512."""
+    n, group, d = 600, 2049, 64
+    q = torch.zeros(1, group, n, d, dtype=BF, device=DEV)
+    q[:, 0, :, 0] = q[:, 0, :, 1] = 2.0 ** 24
+    q[:, 1:, :, 0], q[:, 1:, :, 1] = 1.0, -1.0
+    mean = torch.zeros(1, 1, 2, d, device=DEV)
+    mean[0, 0, 0, :2] = torch.tensor([-1.0, 1.0])
+    mean[0, 0, 1, :2] = torch.tensor([1.0, -1.0 - 6144 * 2.0 ** -24])
+    cfg = spr.SelectConfig(block=64, top=1)
+    ws = spr.selected_workspace(q, torch.zeros(1, 1, 128, d, dtype=BF, device=DEV), cfg)
+    sel = spr.select_blocks(q, mean, 128, cfg, ws)
+    lens = torch.tensor([128], device=DEV)
+    assert torch.equal(sel, R.select(q, mean, 128, 64, 1, lens, torch.zeros_like(lens), False, 0, 0))
+    assert (sel == 1).all()
+
+
+@pytest.mark.parametrize("group,d", [(1, 128), (3, 128), (1, 64)])
+def test_ties_of_a_dominating_dim_are_decided_by_the_rest(group, d):
+    """One dim a thousand times the others and equal in all blocks: what is left differs in the last bits
+    of a 32-bit sum."""
+    n, nb, top = 700, 96, 7
+    gen = gen_of(80)
+    q, mean = rnd(gen, 1, group, n, d), rnd(gen, 1, 1, nb, d, dtype=F) * 1e-2
+    q[..., 3] = 1000 + q[..., 3]
+    mean[..., 3] = 10
+    cfg = spr.SelectConfig(block=64, top=top)
+    ws = spr.selected_workspace(q, torch.zeros(1, 1, nb * 64, d, dtype=BF, device=DEV), cfg)
+    sel = spr.select_blocks(q, mean, nb * 64, cfg, ws)
+    spr.check(ws)
+    lens = torch.tensor([nb * 64], device=DEV)
+    assert torch.equal(sel, R.select(q, mean, nb * 64, 64, top, lens, torch.zeros_like(lens), False, 0, 0))
+
+
 def test_two_threads_select_among_different_numbers_of_blocks():
     """Host threads with workspaces and streams of their own: neither sees the other's sizes."""
     errors, results = [], {}
