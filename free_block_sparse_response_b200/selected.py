@@ -241,7 +241,7 @@ def rotary(plan: RotaryPlan, positions: torch.Tensor, q: torch.Tensor, k: Option
     is applied in both directions).  ``out``: the output tensor or pair, which may be the input
     itself or a strided view such as the new rows of a key cache."""
     qo, ko = (None, None) if out is None else tuple(out) if k is not None else (out, None)
-    key = ("rotary", plan[1:], plan.freqs.get_device(), bool(inverse), _signature(positions, q, k, qo, ko))
+    key = ("rotary", plan[1:], bool(inverse), _signature(plan.freqs, positions, q, k, qo, ko))
     c = _prepared(key, _rotary_call, plan, positions, q, k, inverse, qo, ko)
     qo = _rows_like(q) if qo is None else qo
     if k is not None:
@@ -259,6 +259,7 @@ def _rotary_call(plan, positions, q, k, inverse, qo, ko) -> _Call:
     bt, h, n, d = q.shape
     if d != plan.d or plan.freqs.device != q.device:
         raise ValueError("the plan was made for another head dim or device")
+    _need_flat("the plan's freqs", plan.freqs, (plan.rot_dim // 2,), torch.float64, q.device)
     axes = len(plan.sections)
     at = positions[..., None] if positions.dim() == 2 and axes == 1 else positions
     if at.dtype != torch.int32 or at.device != q.device or at.dim() != 3 or at.shape[0] not in (1, bt) or \

@@ -288,3 +288,18 @@ def test_two_threads_select_among_different_numbers_of_blocks():
     for q, mean, nb, sel in results.values():
         lens = torch.tensor([nb * 64], device=DEV)
         assert torch.equal(sel, R.select(q, mean, nb * 64, 64, 5, lens, torch.zeros_like(lens), False, 0, 0))
+
+
+# ------------------------------------------------------------------- rotary
+
+def test_a_plan_with_other_frequencies_is_checked():
+    """A plan is a plain tuple: its frequencies are held to its sizes, type and layout in every call."""
+    q = rnd(gen_of(85), 1, 2, 10, 64)
+    pos = torch.arange(10, dtype=torch.int32, device=DEV)[None]
+    plan = spr.rotary_plan(64, DEV)
+    want = spr.rotary(plan, pos, q)
+    wide = torch.zeros(64, dtype=torch.float64, device=DEV)
+    for bad in (plan.freqs[:31], plan.freqs.float(), wide[::2], plan.freqs.cpu(), torch.zeros(32, 2, dtype=torch.float64, device=DEV)):
+        with pytest.raises(ValueError):
+            spr.rotary(plan._replace(freqs=bad), pos, q)
+    assert torch.equal(spr.rotary(plan._replace(freqs=plan.freqs.clone()), pos, q), want)
