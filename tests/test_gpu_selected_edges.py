@@ -290,6 +290,35 @@ def test_two_threads_select_among_different_numbers_of_blocks():
         assert torch.equal(sel, R.select(q, mean, nb * 64, 64, 5, lens, torch.zeros_like(lens), False, 0, 0))
 
 
+@pytest.mark.parametrize("n", [1, 2, 3])
+@pytest.mark.parametrize("top", [4, 40])
+def test_bad_entries_of_a_few_tokens(n, top):
+    """The direct form skips and reports what the lists skip and report, and stops at a negative entry."""
+    q, k, v, lens, starts, cfg = problem((1, 4, 2, n, 64 * 50, 64, 64, top, False, 0, 0, None, BF), 82)
+
+    def rows(*entries):
+        r = torch.full((1, 2, n, top), -1, dtype=torch.int32, device=DEV)
+        pad = list(range(10, 10 + top - 4)) if top > 4 else []
+        line = pad + list(entries)
+        r[..., :len(line)] = torch.tensor(line, dtype=torch.int32, device=DEV)
+        return r
+
+    last = 10 + top - 4 if top > 4 else 1
+    ws = spr.selected_workspace(q, k, cfg)
+    want = spr.selected_attn(q, k, v, rows(last, last + 2), cfg, ws)
+    spr.check(ws)
+    for bad in ((last, last, last + 2, last + 1), (last, last + 2, 50, 1 << 30), (last, last - 1, last + 2, 0)):
+        got = spr.selected_attn(q, k, v, rows(*bad), cfg, ws)
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), bad
+        with pytest.raises(spr.SparsePRError) as e:
+            spr.check(ws)
+        assert e.value.code == spr.ERR_INVALID_ARG
+        spr.sparsepr.reset_workspace(ws)
+    got = spr.selected_attn(q, k, v, rows(last, last + 2, -7, last + 3), cfg, ws)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    spr.check(ws)
+
+
 # ------------------------------------------------------------------- rotary
 
 def test_a_plan_with_other_frequencies_is_checked():
@@ -303,3 +332,41 @@ def test_a_plan_with_other_frequencies_is_checked():
         with pytest.raises(ValueError):
             spr.rotary(plan._replace(freqs=bad), pos, q)
     assert torch.equal(spr.rotary(plan._replace(freqs=plan.freqs.clone()), pos, q), want)
+
+
+# ------------------------------------------------------------------- large calls
+
+def by_head(q, k, v, sel, dout, out, cfg, lens, starts):
+    """64-bit gradients and what bounds them (u |.| of bf16 and noise), query head by query head."""
+    hq, hk, n, keys = q.shape[1], k.shape[1], q.shape[2], k.shape[2]
+    grp, d = hq // hk, q.shape[3]
+    dq, bq = torch.empty(q.shape, dtype=torch.float64, device=DEV), torch.empty(q.shape, dtype=torch.float64, device=DEV)
+    dk, bk, dv, bv = (torch.zeros(k.shape, dtype=torch.float64, device=DEV) for _ in range(4))
+    for h in range(hq):
+        one, at = slice(h, h + 1), slice(h // grp, h // grp + 1)
+        ok = R.mask(sel[:, at], n, keys, cfg.block, lens, starts, cfg.causal)
+        grads, sizes, noise = R.backward(dout[:, one], q[:, one], k[:, at], v[:, at], ok, d ** -0.5, out=out[:, one])
+        u = U[q.dtype]
+        dq[:, one], bq[:, one] = grads[0], u * grads[0].abs() + u * sizes[0] * 1.01 + E * noise[0]
+        for total, bound, i in ((dk, bk, 1), (dv, bv, 2)):
+            total[:, at] += grads[i]
+            bound[:, at] += u * sizes[i] * 1.01 + E * noise[i]
+    return (dq, dk, dv), (bq, bk + U[q.dtype] * dk.abs(), bv + U[q.dtype] * dv.abs())
+
+
+def test_gradients_of_several_chunks_of_heads():
+    """Heads whose partial rows together pass the workspace's chunk: worked off in two."""
+    gen = gen_of(86)
+    n, h, d, top = 8192, 8, 128, 64
+    q, k, v = rnd(gen, 1, h, n, d), rnd(gen, 1, h, n, d), rnd(gen, 1, h, n, d)
+    dout = rnd(gen, 1, h, n, d)
+    cfg = spr.SelectConfig(block=64, top=top)
+    ws = spr.selected_workspace(q, k, cfg, backward=True)
+    sel = spr.select_blocks(q, spr.key_means(k, 64), n, cfg, ws)
+    out, lse = spr.selected_attn(q, k, v, sel, cfg, ws)
+    got = spr.selected_attn_backward(dout, q, k, v, out, lse, sel, cfg, ws)
+    spr.check(ws)
+    lens = torch.tensor([n], device=DEV)
+    grads, bounds = by_head(q, k, v, sel, dout, out, cfg, lens, torch.zeros_like(lens))
+    for name, g, w, b in zip(("dq", "dk", "dv"), got, grads, bounds):
+        close(g, w, b + 1e-30, name)
