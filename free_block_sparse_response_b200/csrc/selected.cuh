@@ -88,6 +88,9 @@ struct SelArgs {
   __nv_bfloat16* rest;   // [Bt, Hq, n, d] what the rounding of o left off, or null
   float* seg;            // backward: [chunk regions][seg_cap][2][block][d] sums of split blocks
   int seg_cap;
+  // backward, a head of several slices: [2][nk][d] sums of dV and of dK over the slices so
+  // far of the head at work, or null (the launches write a.gk and a.gv)
+  float* acc;
 };
 
 // Device limits of one batch element.
@@ -110,6 +113,8 @@ cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cud
 bool use_decode(const SelArgs& a);
 cudaError_t launch_decode(const SelArgs& a, cudaStream_t st);
 cudaError_t launch_delta(const SelArgs& a, cudaStream_t st);
+// a.acc to rows of a.gk and a.gv, (batch, key head) z.
+cudaError_t launch_slice_sums(const SelArgs& a, int z, cudaStream_t st);
 // The elements of the listed rows of a.o, or (grad) a.gq, that their parts could not hold.
 cudaError_t launch_mend(const SelArgs& a, bool grad, cudaStream_t st);
 

@@ -109,7 +109,7 @@ constexpr size_t kPartialBytes = 1ull << 30;
 // status header).
 struct Plan {
   int regions, chunk;  // chunk: regions per launch
-  size_t slow, mean_parts, mean_norm2, wide, offs, list, inv, units, n_units, blk, part, ml, delta, seg, total;
+  size_t slow, mean_parts, mean_norm2, wide, offs, list, inv, units, n_units, blk, part, ml, delta, seg, acc, total;
 };
 
 Plan make_plan(SelArgs& a, bool backward) {
@@ -120,10 +120,9 @@ Plan make_plan(SelArgs& a, bool backward) {
   const size_t stats = a.f32 || backward ? sizeof(float2) : sizeof(float4);
   const size_t row = val * a.d + stats;
   const size_t sub_bytes = row * spr::kSub * a.top * a.group;
-  // A backward region is a head's whole token range, so that a key block's gradient is
-  // formed by one region; a forward region is cut where its partial rows pass the chunk.
-  long long per = subs;
-  if (!backward) per = std::min<long long>(subs, std::max<long long>(1, kPartialBytes / sub_bytes));
+  // A region is cut where its partial rows pass the chunk.  A key block's gradient is then the sum of
+  // its slices', which go one after the other and add to fp32 sums of the head (acc).
+  const long long per = std::min<long long>(subs, std::max<long long>(1, kPartialBytes / sub_bytes));
   a.subs = static_cast<int>(per);
   a.slice = static_cast<int>(per) * spr::kSub;
   a.slices = static_cast<int>((subs + per - 1) / per);
@@ -133,7 +132,7 @@ Plan make_plan(SelArgs& a, bool backward) {
   const long long entries = static_cast<long long>(a.slice) * a.top, rows = entries * a.group;
   // equal chunks, so that the last one fills the SMs too
   const long long most = std::min<long long>(L.regions, std::max<long long>(1, kPartialBytes / (row * rows)));
-  L.chunk = spr::ceil_div(L.regions, spr::ceil_div(L.regions, static_cast<int>(most)));
+  L.chunk = backward && a.slices > 1 ? 1 : spr::ceil_div(L.regions, spr::ceil_div(L.regions, static_cast<int>(most)));
   // The tensor-core kernels work tile by tile.  On the fp32 pipes a unit is one CTA: long units
   // load K and V seldom (and, backward, leave few sums), short ones fill the SMs when there are
   // few rows: the longest that still gives four units per SM.
@@ -169,6 +168,7 @@ Plan make_plan(SelArgs& a, bool backward) {
   L.delta = take(backward ? sizeof(float) * static_cast<size_t>(a.Bt) * a.Hq * a.n : 0);
   L.seg = take(sizeof(float) * 2 * a.block * a.d *
                (!backward ? 0 : a.f32 ? static_cast<size_t>(a.seg_cap) * L.chunk : 2 * size_t{spr::kTcShares}));
+  L.acc = take(backward && a.slices > 1 ? sizeof(float) * 2 * a.nk * a.d : 0);
   L.total = off;
   return L;
 }
@@ -328,10 +328,18 @@ int sparsepr_selected_attn_backward(const sparsepr_selected* p, const sparsepr_v
   if ((rc = cuda_status(spr::launch_delta(a, st), "selected attention backward: row sums"))) return rc;
   if (!a.f32 && (rc = cuda_status(spr::launch_wide_blocks(a, a.k, st), "selected attention backward: ranges"))) return rc;
   if ((rc = cuda_status(spr::launch_lists(a, st), "selected attention backward: lists"))) return rc;
-  for (int r = 0; r < L.regions; r += L.chunk)
+  a.acc = a.slices > 1 ? at<float>(ws, L.acc) : nullptr;
+  for (int r = 0; r < L.regions; r += L.chunk) {
+    if (a.acc != nullptr && r % a.slices == 0 &&
+        (rc = cuda_status(cudaMemsetAsync(a.acc, 0, sizeof(float) * 2 * a.nk * a.d, st), "selected attention backward: sums")))
+      return rc;
     if ((rc = cuda_status(spr::launch_selected_backward(a, r, std::min(L.chunk, L.regions - r), st),
                           "selected attention backward")))
       return rc;
+    if (a.acc != nullptr && r % a.slices == a.slices - 1 &&
+        (rc = cuda_status(spr::launch_slice_sums(a, r / a.slices, st), "selected attention backward: sums")))
+      return rc;
+  }
   if (a.f32) return SPARSEPR_OK;
   return cuda_status(spr::launch_mend(a, true, st), "selected attention backward: values outside the parts' range");
 }

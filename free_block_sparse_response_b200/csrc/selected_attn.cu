@@ -387,6 +387,36 @@ __global__ void __launch_bounds__(256) delta_kernel(const SelArgs a) {
   }
 }
 
+// Four columns of a key's dK and dV: written, or added to the sums of the head's earlier slices.
+template <typename T, int D>
+__device__ __forceinline__ void store_gradients(const SelArgs& a, int b, int kh, int j, int col, float4 dk, float4 dv) {
+  if (a.acc == nullptr) {
+    store4<T>(row_ptr<T>(a.gk, b, kh, j) + col, dk);
+    store4<T>(row_ptr<T>(a.gv, b, kh, j) + col, dv);
+  } else {
+    float* v = a.acc + static_cast<size_t>(j) * D + col;
+    float* k = v + static_cast<size_t>(a.nk) * D;
+    float4 x = *reinterpret_cast<const float4*>(k), y = *reinterpret_cast<const float4*>(v);
+    axpy4(1.f, dk, x);
+    axpy4(1.f, dv, y);
+    *reinterpret_cast<float4*>(k) = x;
+    *reinterpret_cast<float4*>(v) = y;
+  }
+}
+
+// The sums over a head's slices, rounded once.  One thread for two columns of a key.
+template <typename T>
+__global__ void __launch_bounds__(256) slice_sums_kernel(const SelArgs a, int z) {
+  const long long i = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) * 2;
+  if (i >= static_cast<long long>(a.nk) * a.d) return;
+  const int j = static_cast<int>(i / a.d), c = static_cast<int>(i % a.d), b = z / a.Hk, kh = z % a.Hk;
+  const float2 dv = *reinterpret_cast<const float2*>(a.acc + i);
+  const float2 dk = *reinterpret_cast<const float2*>(a.acc + static_cast<size_t>(a.nk) * a.d + i);
+  T *v = row_ptr<T>(a.gv, b, kh, j) + c, *k = row_ptr<T>(a.gk, b, kh, j) + c;
+  v[0] = from_f32<T>(dv.x), v[1] = from_f32<T>(dv.y);
+  k[0] = from_f32<T>(dk.x), k[1] = from_f32<T>(dk.y);
+}
+
 constexpr int kBwdThreads = 256, kBwdRows = 32;
 
 template <int D, int B>
@@ -530,8 +560,7 @@ __global__ void __launch_bounds__(kBwdThreads) backward_kernel(const SelArgs a, 
         *reinterpret_cast<float4*>(seg + j * D + col) = gk[i][c];
         *reinterpret_cast<float4*>(seg + B * D + j * D + col) = gv[i][c];
       } else if (j0 + j < a.nk) {
-        store4<T>(row_ptr<T>(a.gk, b, kh, j0 + j) + col, gk[i][c]);
-        store4<T>(row_ptr<T>(a.gv, b, kh, j0 + j) + col, gv[i][c]);
+        store_gradients<T, D>(a, b, kh, j0 + j, col, gk[i][c], gv[i][c]);
       }
     }
 }
@@ -542,7 +571,7 @@ __global__ void __launch_bounds__(256) join_kv_kernel(const SelArgs a, int first
   const int g = blockIdx.x, region = first + blockIdx.y, z = region / a.slices;
   const int b = z / a.Hk, kh = z % a.Hk;
   const int4 bk = a.blk[static_cast<size_t>(region) * a.nb + g];
-  if (bk.x == 1) return;
+  if (bk.x == 1 || (bk.x == 0 && a.acc != nullptr)) return;
   const size_t tile = static_cast<size_t>(a.block) * D;
   const float* seg = a.seg + (static_cast<size_t>(blockIdx.y) * a.seg_cap + bk.y) * 2 * tile;
   for (int i = threadIdx.x * 4; i < a.block * D; i += 1024) {
@@ -553,8 +582,7 @@ __global__ void __launch_bounds__(256) join_kv_kernel(const SelArgs a, int first
       axpy4(1.f, *reinterpret_cast<const float4*>(seg + s * 2 * tile + i), x);
       axpy4(1.f, *reinterpret_cast<const float4*>(seg + s * 2 * tile + tile + i), y);
     }
-    store4<T>(row_ptr<T>(a.gk, b, kh, j) + i % D, x);
-    store4<T>(row_ptr<T>(a.gv, b, kh, j) + i % D, y);
+    store_gradients<T, D>(a, b, kh, j, i % D, x, y);
   }
 }
 
@@ -639,6 +667,12 @@ cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cud
   if (a.d == 128)
     return a.block == 128 ? backward<float, 128, 128>(a, first, count, st) : backward<float, 128, 64>(a, first, count, st);
   return a.block == 128 ? backward<float, 64, 128>(a, first, count, st) : backward<float, 64, 64>(a, first, count, st);
+}
+
+cudaError_t launch_slice_sums(const SelArgs& a, int z, cudaStream_t st) {
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a.nk) * a.d / 2 + 255) / 256);
+  a.f32 ? slice_sums_kernel<float><<<grid, 256, 0, st>>>(a, z) : slice_sums_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(a, z);
+  return counted(cudaGetLastError(), 1);
 }
 
 cudaError_t launch_mend(const SelArgs& a, bool grad, cudaStream_t st) {

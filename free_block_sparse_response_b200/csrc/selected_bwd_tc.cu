@@ -187,6 +187,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 32; ++c) seg[static_cast<size_t>(c0 + c) * D] = __uint_as_float(x[c]) * f;
           continue;
         }
+        if (a.acc != nullptr) {
+          float* acc = a.acc + (static_cast<size_t>(which) * a.nk + un.g * B) * D + d0 + lane;
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (c0 + c < keys) acc[static_cast<size_t>(c0 + c) * D] += __uint_as_float(x[c]) * f;
+          continue;
+        }
         // 32 keys x 32 dims turned in shared memory (rows of 80 bytes: no two keys
         // of a group in one bank), so that 4 lanes write 64 bytes of a key
         __syncwarp();
@@ -475,7 +482,7 @@ __global__ void __launch_bounds__(256) join_kv_tc_kernel(const SelArgs a, int fi
     if (g0 + warp < a.nb) {
       const int4 bk = a.blk[static_cast<size_t>(region) * a.nb + g0 + warp];  // tiles, -, first tile of its region
       if (bk.x == 0) {
-        c0 = 0;  // zeros
+        c0 = a.acc == nullptr ? 0 : -1;  // zeros
       } else {
         const long long t0 = static_cast<long long>(before) + bk.z;
         auto share = [&](long long t) {
@@ -523,6 +530,14 @@ __global__ void __launch_bounds__(256) join_kv_tc_kernel(const SelArgs a, int fi
       for (int k = 0; k < kBatch; ++k) {
         const int i = i0 + k * 1024, j = g * a.block + i / D;
         if (i >= a.block * D || j >= a.nk) continue;
+        if (a.acc != nullptr) {
+          float4* v4 = reinterpret_cast<float4*>(a.acc + static_cast<size_t>(j) * D + i % D);
+          float4* k4 = reinterpret_cast<float4*>(a.acc + (static_cast<size_t>(a.nk) + j) * D + i % D);
+          const float4 v0 = *v4, k0 = *k4;
+          *v4 = make_float4(v0.x + y[k].x, v0.y + y[k].y, v0.z + y[k].z, v0.w + y[k].w);
+          *k4 = make_float4(k0.x + x[k].x, k0.y + x[k].y, k0.z + x[k].z, k0.w + x[k].w);
+          continue;
+        }
         __nv_bfloat16* dk = static_cast<__nv_bfloat16*>(a.gk.p) + b * a.gk.sb + kh * a.gk.sh + j * a.gk.sn + i % D;
         __nv_bfloat16* dv = static_cast<__nv_bfloat16*>(a.gv.p) + b * a.gv.sb + kh * a.gv.sh + j * a.gv.sn + i % D;
         *reinterpret_cast<uint2*>(dk) = make_uint2(pack_bf16x2(x[k].x, x[k].y), pack_bf16x2(x[k].z, x[k].w));

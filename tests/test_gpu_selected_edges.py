@@ -370,3 +370,33 @@ def test_gradients_of_several_chunks_of_heads():
     grads, bounds = by_head(q, k, v, sel, dout, out, cfg, lens, torch.zeros_like(lens))
     for name, g, w, b in zip(("dq", "dk", "dv"), got, grads, bounds):
         close(g, w, b + 1e-30, name)
+
+
+@pytest.mark.parametrize("dtype,causal", [(BF, False), (BF, True), (F, False)])
+def test_gradients_of_a_head_cut_into_token_slices(dtype, causal):
+    """A head whose partial rows alone pass the chunk: its tokens in slices, a key's gradient over all of them;
+    rows and keys of a ragged length, blocks that some slices do not select, the same in every run."""
+    gen = gen_of(87)
+    n, keys, grp, top, d = 33000, 4096, 16, 16, 64
+    q, k, v = rnd(gen, 1, grp, n, d, dtype=dtype), rnd(gen, 1, 1, keys, d, dtype=dtype), rnd(gen, 1, 1, keys, d, dtype=dtype)
+    dout = rnd(gen, 1, grp, n, d, dtype=dtype)
+    lens = torch.tensor([keys - 100], dtype=torch.int32, device=DEV)
+    starts = torch.tensor([-n + keys if causal else 0], dtype=torch.int32, device=DEV)
+    cfg = spr.SelectConfig(block=64, top=top, causal=causal)
+    ws = spr.selected_workspace(q, k, cfg, backward=True)
+    assert ws.numel() < 2 << 30
+    sel = spr.select_blocks(q, spr.key_means(k, 64, kv_len=lens), keys, cfg, ws, kv_len=lens, q_start=starts)
+    sel[:, :, 20000:][sel[:, :, 20000:] < 8] = -1  # (a row's first entries: its selection ends there)
+    sel[:, :, :9000][sel[:, :, :9000] > 40] = -1
+    out, lse = spr.selected_attn(q, k, v, sel, cfg, ws, kv_len=lens, q_start=starts)
+    runs = [spr.selected_attn_backward(dout, q, k, v, out, lse, sel, cfg, ws, kv_len=lens, q_start=starts) for _ in range(2)]
+    spr.check(ws)
+    for a, b in zip(*runs):
+        assert torch.equal(a, b)
+    first = (sel < 0).int().argmax(-1, keepdim=True)
+    ends = torch.where((sel < 0).any(-1, keepdim=True), first, top)
+    live = torch.where(torch.arange(top, device=DEV) < ends, sel, -1)
+    grads, bounds = by_head(q, k, v, live, dout, out, cfg, lens, starts)
+    for name, g, w, b in zip(("dq", "dk", "dv"), runs[0], grads, bounds):
+        close(g, w, b + 1e-30, name)
+    assert (runs[0][1][:, :, keys - 100:] == 0).all() and (runs[0][2][:, :, keys - 100:] == 0).all()
