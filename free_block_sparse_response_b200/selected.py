@@ -19,6 +19,10 @@ or, call by call, with a workspace that the caller keeps:
     out, lse = spr.selected_attn(q, k, v, sel, cfg, ws, rest=rest)
     dq, dk, dv = spr.selected_attn_backward(dout, q, k, v, out, lse, sel, cfg, ws, rest=rest)
 
+Where a tensor needs a gradient, autograd records ``rotary``, ``selected_attn`` and
+``block_attention`` (so ``block_attention(q, k, v, cfg).backward(dout)`` works); the calls for
+gradients are for who keeps outputs and workspaces, and for steps captured into graphs.
+
 For a cache, ``kv_len`` [batch] holds each sequence's length and ``q_start`` [batch] the key
 position of its first query; after appending keys, ``key_means(..., kv_start=, max_new=,
 out=means)`` renews the touched blocks' means.
@@ -33,6 +37,7 @@ import threading
 from typing import NamedTuple, Optional, Sequence
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import sparsepr as _s
 
@@ -158,6 +163,31 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+def _written(*outs) -> None:
+    """Given outputs count as changed in place, as by torch's own calls: a graph that kept one says so."""
+    for t in outs:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
+def _may_record(**outs) -> None:
+    """Refusals of a call that autograd is to record: it makes its own outputs, and is not captured."""
+    for name, t in outs.items():
+        if t is not None:
+            raise ValueError(f"{name} cannot be given where autograd records the call (it can under torch.no_grad())")
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError("a call that autograd records cannot be captured into a graph: capture it under torch.no_grad(), "
+                         "with the calls for gradients")
+
+
+def _plain_rows(g: torch.Tensor) -> torch.Tensor:
+    """An incoming gradient as the calls take it: contiguous rows on 16-byte boundaries."""
+    per = 16 // g.element_size()
+    if g.stride(3) == 1 and g.data_ptr() % 16 == 0 and all(n == 1 or st % per == 0 for n, st in zip(g.shape[:3], g.stride())):
+        return g
+    return g.clone(memory_format=torch.contiguous_format)
+
+
 # ------------------------------------------------------------------------------ rotary
 
 class RotaryPlan(NamedTuple):
@@ -239,10 +269,16 @@ def rotary(plan: RotaryPlan, positions: torch.Tensor, q: torch.Tensor, k: Option
     positions: int32 [batch or 1, rows, axes] (axes may be left out where there is one), last
     dimension contiguous.  ``inverse`` rotates back: the gradient of the rotation (the factor
     is applied in both directions).  ``out``: the output tensor or pair, which may be the input
-    itself or a strided view such as the new rows of a key cache."""
+    itself or a strided view such as the new rows of a key cache.  Autograd records the call where
+    q or k needs a gradient."""
+    if (q.requires_grad or (k is not None and k.requires_grad)) and torch.is_grad_enabled():
+        _may_record(out=out)
+        return _Rotary.apply(plan, positions, bool(inverse), q, k)
     qo, ko = (None, None) if out is None else tuple(out) if k is not None else (out, None)
     key = ("rotary", plan[1:], bool(inverse), _signature(plan.freqs, positions, q, k, qo, ko))
     c = _prepared(key, _rotary_call, plan, positions, q, k, inverse, qo, ko)
+    if out is not None:
+        _written(qo, ko)
     qo = _rows_like(q) if qo is None else qo
     if k is not None:
         ko = _rows_like(k) if ko is None else ko
@@ -250,6 +286,24 @@ def rotary(plan: RotaryPlan, positions: torch.Tensor, q: torch.Tensor, k: Option
     c.q.data, c.qo.data = q.data_ptr(), qo.data_ptr()
     c.run(c.par_ref, plan.freqs.data_ptr(), positions.data_ptr(), *c.sizes, c.q_ref, c.qo_ref, c.h2, c.k_ref, c.ko_ref)
     return qo if k is None else (qo, ko)
+
+
+class _Rotary(torch.autograd.Function):
+    """The gradient of a rotation is the rotation back."""
+
+    @staticmethod
+    def forward(ctx, plan, positions, inverse, q, k):
+        ctx.save_for_backward(positions, plan.freqs)
+        ctx.plan, ctx.inverse, ctx.both = plan, inverse, k is not None
+        return rotary(plan, positions, q, k, inverse=inverse)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        positions, freqs = ctx.saved_tensors
+        gq, gk = (_plain_rows(g) for g in (grads if ctx.both else (grads[0], grads[0])))
+        got = rotary(ctx.plan._replace(freqs=freqs), positions, gq, gk if ctx.both else None, inverse=not ctx.inverse)
+        return (None, None, None) + (got if ctx.both else (got, None))
 
 
 def _rotary_call(plan, positions, q, k, inverse, qo, ko) -> _Call:
@@ -345,9 +399,12 @@ def key_means(k: torch.Tensor, block: int, kv_len: Optional[torch.Tensor] = None
               kv_start: Optional[torch.Tensor] = None, max_new: int = 0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Mean key of every block of ``block`` keys: [batch, heads, ceil(rows / block), d] fp32.
     With ``kv_start`` [batch] int32 only the blocks holding keys [kv_start, kv_len) are renewed
-    in ``out`` (at most ``max_new`` keys per sequence were appended)."""
+    in ``out`` (at most ``max_new`` keys per sequence were appended).  For selections: carries no
+    gradient."""
     c = _prepared(("means", block, _signature(k, kv_len, kv_start, out)), _means_call, k, block, kv_len, kv_start, out)
     means = torch.empty(c.shape, dtype=torch.float32, device=k.device) if out is None else out
+    if out is not None:
+        _written(out)
     c.k.data, c.p.kv_len = k.data_ptr(), _ptr(kv_len)
     c.run(c.p_ref, c.k_ref, _ptr(kv_start), max_new, means.data_ptr())
     return means
@@ -376,6 +433,8 @@ def select_blocks(q: torch.Tensor, means: torch.Tensor, keys: int, cfg: SelectCo
     c = _prepared(key, _select_call, q, means, keys, cfg, ws, kv_len, q_start, out)
     _need_aligned(ws)
     sel = torch.empty(c.shape, dtype=torch.int32, device=q.device) if out is None else out
+    if out is not None:
+        _written(out)
     c.q.data, c.p.kv_len, c.p.q_start = q.data_ptr(), _ptr(kv_len), _ptr(q_start)
     c.run(c.p_ref, c.q_ref, means.data_ptr(), sel.data_ptr(), ws.data_ptr())
     return sel
@@ -436,11 +495,20 @@ def selected_attn(q, k, v, sel: torch.Tensor, cfg: SelectConfig, ws: torch.Tenso
     """Softmax attention of every query over the keys of its selected blocks: (out, lse), out
     like q and lse [batch, heads, rows] fp32 (natural log; -inf and a zero row without keys).
     ``rest``: a contiguous bf16 tensor of q's shape that gets what the rounding of out left off,
-    for the backward call."""
+    for the backward call.
+
+    Autograd records the call where q, k or v needs a gradient (of out; lse carries none): it keeps
+    the inputs, out, lse and, in bf16, a rest of its own, and its backward pass takes a workspace
+    of its own, whose errors end up in ``ws``."""
+    if (q.requires_grad or k.requires_grad or v.requires_grad) and torch.is_grad_enabled():
+        _may_record(out=out, lse=lse, rest=rest)
+        return _SelectedAttn.apply(cfg, ws, ws[:4].view(torch.int32), q, k, v, sel, kv_len, q_start)
     key = ("attn", cfg, _signature(q, k, v, sel, ws, kv_len, q_start, out, lse, rest))
     c = _prepared(key, _attention_call, "sparsepr_selected_attn", False, cfg, ws, sel, kv_len, q_start, lse, rest, q, k, v,
                   (("out", out, q, True),))
     _need_aligned(ws)
+    if out is not None or lse is not None or rest is not None:
+        _written(out, lse, rest)
     out = _rows_like(q) if out is None else out
     lse = torch.empty(c.lse_shape, dtype=torch.float32, device=q.device) if lse is None else lse
     _fill(c, kv_len, q_start, rest, q, k, v, out)
@@ -464,6 +532,8 @@ def selected_attn_backward(dout, q, k, v, out, lse, sel: torch.Tensor, cfg: Sele
                   q, k, v, (("dout", dout, q, False), ("out", out, q, False), ("dq", dq, q, True), ("dk", dk, k, True),
                             ("dv", dv, k, True)))
     _need_aligned(ws)
+    if dq is not None or dk is not None or dv is not None:
+        _written(dq, dk, dv)
     dq = _rows_like(q) if dq is None else dq
     dk = _rows_like(k) if dk is None else dk
     dv = _rows_like(k) if dv is None else dv
@@ -473,11 +543,43 @@ def selected_attn_backward(dout, q, k, v, out, lse, sel: torch.Tensor, cfg: Sele
     return dq, dk, dv
 
 
+class _SelectedAttn(torch.autograd.Function):
+    """``selected_attn`` with ``selected_attn_backward``; ``status``: the status word of the caller's
+    workspace (a view of it), or None."""
+
+    @staticmethod
+    def forward(ctx, cfg, ws, status, q, k, v, sel, kv_len, q_start):
+        rest = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q.dtype == torch.bfloat16 else None
+        out, lse = selected_attn(q, k, v, sel, cfg, ws, kv_len=kv_len, q_start=q_start, rest=rest)
+        ctx.save_for_backward(q, k, v, sel, kv_len, q_start, out, lse, rest)
+        ctx.cfg, ctx.status = cfg, status
+        ctx.mark_non_differentiable(lse)
+        return out, lse
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dout, _):
+        q, k, v, sel, kv_len, q_start, out, lse, rest = ctx.saved_tensors
+        ws = selected_workspace(q, k, ctx.cfg, backward=True)
+        grads = selected_attn_backward(_plain_rows(dout), q, k, v, out, lse, sel, ctx.cfg, ws, kv_len=kv_len,
+                                       q_start=q_start, rest=rest)
+        if ctx.status is not None:
+            torch.maximum(ctx.status, ws[:4].view(torch.int32), out=ctx.status)
+        return (None, None, None) + grads + (None, None, None)
+
+
 def block_attention(q, k, v, cfg: SelectConfig, ws: Optional[torch.Tensor] = None,
                     kv_len: Optional[torch.Tensor] = None, q_start: Optional[torch.Tensor] = None,
                     out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """Mean keys, selection and attention in one call: out like q."""
-    ws = selected_workspace(q, k, cfg) if ws is None else ws
+    """Mean keys, selection and attention in one call: out like q.  Autograd records the call where
+    q, k or v needs a gradient; the selection is fixed in it."""
+    recorded = (q.requires_grad or k.requires_grad or v.requires_grad) and torch.is_grad_enabled()
+    if recorded:
+        _may_record(out=out)
+    own = ws is None
+    ws = selected_workspace(q, k, cfg) if own else ws
     means = key_means(k, cfg.block, kv_len=kv_len)
     sel = select_blocks(q, means, k.shape[2], cfg, ws, kv_len=kv_len, q_start=q_start)
+    if recorded:  # (a view of a workspace made here would keep it until the backward pass)
+        return _SelectedAttn.apply(cfg, ws, None if own else ws[:4].view(torch.int32), q, k, v, sel, kv_len, q_start)[0]
     return selected_attn(q, k, v, sel, cfg, ws, kv_len=kv_len, q_start=q_start, out=out)[0]

@@ -400,3 +400,146 @@ def test_gradients_of_a_head_cut_into_token_slices(dtype, causal):
     for name, g, w, b in zip(("dq", "dk", "dv"), runs[0], grads, bounds):
         close(g, w, b + 1e-30, name)
     assert (runs[0][1][:, :, keys - 100:] == 0).all() and (runs[0][2][:, :, keys - 100:] == 0).all()
+
+
+# ------------------------------------------------------------------- autograd
+
+def leaves(*ts):
+    return [t.detach().clone().requires_grad_() for t in ts]
+
+
+@pytest.mark.parametrize("dtype", [BF, F])
+def test_autograd_gives_the_gradients_of_the_calls(dtype):
+    """Rotation, selection and attention on tensors that need gradients: what the explicit calls give."""
+    q, k, v, lens, starts, cfg = problem((2, 4, 2, 300, 300, 128, 64, 3, True, 1, 1, (300, 77), dtype), 90)
+    k, v = k.nan_to_num(0), v.nan_to_num(0, 0, 0)
+    plan = spr.rotary_plan(128, DEV, rot_dim=64)
+    pos = torch.arange(300, dtype=torch.int32, device=DEV)[None]
+    dout = rnd(gen_of(91), *q.shape, dtype=dtype)
+    a, b, c = leaves(q, k, v)
+    out = spr.block_attention(*spr.rotary(plan, pos, a, b), c, cfg, kv_len=lens, q_start=starts)
+    got = torch.autograd.grad(out, (a, b, c), dout)
+    qr, kr = spr.rotary(plan, pos, q, k)
+    ws = spr.selected_workspace(q, k, cfg, backward=True)
+    sel = spr.select_blocks(qr, spr.key_means(kr, 64, kv_len=lens), 300, cfg, ws, kv_len=lens, q_start=starts)
+    rest = torch.empty_like(q) if dtype is BF else None
+    o, lse = spr.selected_attn(qr, kr, v, sel, cfg, ws, kv_len=lens, q_start=starts, rest=rest)
+    dq, dk, dv = spr.selected_attn_backward(dout, qr, kr, v, o, lse, sel, cfg, ws, kv_len=lens, q_start=starts, rest=rest)
+    want = spr.rotary(plan, pos, dq, dk, inverse=True) + (dv,)
+    assert torch.equal(out, o)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    # one tensor alone, and a gradient that is an expanded, a strided or an odd-offset tensor
+    x, = leaves(q)
+    assert torch.equal(torch.autograd.grad(spr.rotary(plan, pos, x, inverse=True), x, dout)[0], spr.rotary(plan, pos, dout))
+    for g in (torch.ones((), dtype=dtype, device=DEV).expand(q.shape), dout.transpose(1, 2).contiguous().transpose(1, 2),
+              torch.cat([dout.flatten(), dout.flatten()[:1]])[1:].view(q.shape)):
+        x, y, z = leaves(qr, kr, v)
+        out, lse = spr.selected_attn(x, y, z, sel, cfg, ws, kv_len=lens, q_start=starts)
+        assert not lse.requires_grad
+        got = torch.autograd.grad(out, (x, y, z), g)
+        want = spr.selected_attn_backward(g.contiguous().clone(), qr, kr, v, o, lse, sel, cfg, ws, kv_len=lens, q_start=starts,
+                                          rest=rest)
+        assert all(torch.equal(s, t) for s, t in zip(got, want))
+    spr.check(ws)
+
+
+def test_autograd_adds_over_repeated_inputs_and_branches():
+    """Expanded keys get the sum over their repeats; two uses of a tensor add up; a frozen one gets nothing."""
+    gen = gen_of(92)
+    q, k, v = rnd(gen, 2, 4, 150, 64, dtype=F), rnd(gen, 1, 1, 300, 64, dtype=F), rnd(gen, 1, 1, 300, 64, dtype=F)
+    cfg = spr.SelectConfig(block=64, top=3)
+    a, b, c = leaves(q, k, v)
+    out = spr.block_attention(a, b.expand(2, 2, 300, 64), c.expand(2, 2, 300, 64), cfg)
+    got = torch.autograd.grad(out.square().sum(), (b, c))
+    y, z = leaves(k.expand(2, 2, 300, 64), v.expand(2, 2, 300, 64))
+    want = torch.autograd.grad(spr.block_attention(q, y, z, cfg).square().sum(), (y, z))
+    for s, t in zip(got, want):  # four terms added in fp32, in another order
+        t = t.double()
+        close(s, t.sum((0, 1), keepdim=True), 4 * U[F] * t.abs().sum((0, 1), keepdim=True) + 1e-30, "expanded")
+    x, = leaves(q)
+    twice = spr.block_attention(x, b.detach().expand(2, 2, 300, 64), c.detach().expand(2, 2, 300, 64), cfg)
+    g1, = torch.autograd.grad(twice.sum() + (2 * x).sum(), x, retain_graph=True)
+    g2, = torch.autograd.grad(twice.sum(), x)
+    assert torch.equal(g1, g2 + 2)
+
+
+def test_calls_that_autograd_records_are_checked():
+    q, k, v, lens, starts, cfg = problem((1, 2, 2, 40, 200, 64, 64, 2, False, 0, 0, None, BF), 93)
+    plan = spr.rotary_plan(64, DEV)
+    pos = torch.arange(40, dtype=torch.int32, device=DEV)[None]
+    ws = spr.selected_workspace(q, k, cfg)
+    sel = spr.select_blocks(q, spr.key_means(k, 64), 200, cfg, ws)
+    a, = leaves(q)
+    buf, lse = torch.empty_like(q), torch.empty(1, 2, 40, device=DEV)
+    for call in (lambda: spr.selected_attn(a, k, v, sel, cfg, ws, out=buf), lambda: spr.selected_attn(a, k, v, sel, cfg, ws, lse=lse),
+                 lambda: spr.selected_attn(a, k, v, sel, cfg, ws, rest=buf), lambda: spr.block_attention(a, k, v, cfg, out=buf),
+                 lambda: spr.rotary(plan, pos, a, out=buf)):
+        with pytest.raises(ValueError, match="autograd"):
+            call()
+        with torch.no_grad():
+            call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="captured"):
+            spr.selected_attn(a, k, v, sel, cfg, ws)
+        with torch.no_grad():
+            out, _ = spr.selected_attn(a, k, v, sel, cfg, ws)
+    graph.replay()
+    assert torch.equal(out, spr.selected_attn(q, k, v, sel, cfg, ws)[0])
+    with torch.inference_mode():
+        assert torch.equal(spr.selected_attn(a, k, v, sel, cfg, ws, out=torch.empty_like(q))[0], out)
+    # no second derivative
+    got, = torch.autograd.grad(spr.selected_attn(a, k, v, sel, cfg, ws)[0].float().square().sum(), a, create_graph=True)
+    with pytest.raises(RuntimeError):
+        got.sum().backward()
+    spr.check(ws)
+
+
+def test_what_a_recorded_call_keeps_is_not_overwritten_unseen():
+    """A selection, a length or an output written again before the backward pass: an error, not other gradients."""
+    q, k, v, lens, starts, cfg = problem((1, 2, 2, 40, 200, 64, 64, 2, False, 0, 0, None, BF), 94)
+    ws = spr.selected_workspace(q, k, cfg)
+    means = spr.key_means(k, 64)
+    plan = spr.rotary_plan(64, DEV)
+    pos = torch.arange(40, dtype=torch.int32, device=DEV)[None]
+    for change in (lambda t: spr.select_blocks(q, means, 200, cfg, ws, out=t["sel"]), lambda t: t["lens"].sub_(1),
+                   lambda t: spr.rotary(plan, pos, q, out=t["q"])):
+        t = {"sel": spr.select_blocks(q, means, 200, cfg, ws), "lens": lens.clone(), "q": q.clone()}
+        c, = leaves(v)
+        out, _ = spr.selected_attn(t["q"], k, c, t["sel"], cfg, ws, kv_len=t["lens"])
+        change(t)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            out.sum().backward()
+
+
+def test_errors_of_a_recorded_backward_pass_reach_the_callers_workspace():
+    """Bad entries seen by the backward pass alone (the status of the forward call was reset)."""
+    q, k, v, lens, starts, cfg = problem((1, 2, 2, 40, 400, 64, 64, 3, False, 0, 0, None, BF), 95)
+    sel = torch.tensor([1, 3, 2], dtype=torch.int32, device=DEV).expand(1, 2, 40, 3).contiguous()
+    ws = spr.selected_workspace(q, k, cfg)
+    a, = leaves(q)
+    out, _ = spr.selected_attn(a, k, v, sel, cfg, ws)
+    with pytest.raises(spr.SparsePRError):
+        spr.check(ws)
+    spr.sparsepr.reset_workspace(ws)
+    out.sum().backward()
+    with pytest.raises(spr.SparsePRError) as e:
+        spr.check(ws)
+    assert e.value.code == spr.ERR_INVALID_ARG
+
+
+def test_a_recorded_pass_on_another_stream():
+    """Forward and backward on a stream that is not the default one, gradients read on the default one."""
+    q, k, v, lens, starts, cfg = problem((1, 4, 2, 700, 700, 128, 64, 4, True, 0, 1, None, BF), 96)
+    dout = rnd(gen_of(97), *q.shape)
+    a, b, c = leaves(q, k, v)
+    spr.block_attention(a, b, c, cfg).backward(dout)
+    want = [t.grad.clone() for t in (a, b, c)]
+    side = torch.cuda.Stream()
+    a, b, c = leaves(q, k, v)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        out = spr.block_attention(a, b, c, cfg)
+        out.backward(dout)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(t.grad, w) for t, w in zip((a, b, c), want))
