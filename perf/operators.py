@@ -232,7 +232,7 @@ def prepare(case, seed):
     if case["kind"] == "train":
         s["grad"] = torch.randn(b, hq, n, d, generator=gen, device=dev).to(dt)
     if case["kind"] == "decode":
-        s["means"] = _plain_means(s["k"], case["block"], lens)  # the cache's means, kept up to the token before
+        s["means"] = _plain_means(s["k"], case["block"], lens - 1)  # the cache's means, kept up to the token before
     if own:
         s["cfg"] = spr.SelectConfig(block=case["block"], top=case["top"], causal=case["causal"], n_first=case["first"],
                                     n_local=case["local"])
