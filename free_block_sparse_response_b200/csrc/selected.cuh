@@ -41,9 +41,10 @@ constexpr int kTcShares = 148;
 // One work item of the attention kernels: rows [r0, r0 + rows) of the entries of key block g,
 // whose first entry is `off` of its region's list; row r is query head r % group of entry r / group.
 // rows = 0: none.  live, qs: the length and the position of query 0, both from the block's first
-// key on.  total: the block's rows in this region.  wide: a.wide of the block.
+// key on.  total: the block's rows in this region.  k: a.range of the block.
 struct __align__(16) Unit {
-  int g, off, r0, rows, live, qs, b, kh, total, wide;
+  int g, off, r0, rows, live, qs, b, kh, total;
+  float k;
   int pad[2];
 };
 
@@ -78,12 +79,14 @@ struct SelArgs {
   // partial rows of one chunk of regions, [chunk regions][slice * top * group][d]: fp32, or fp16
   // with the columns of part_column() (selected_tc.cuh)
   float* part;
-  // statistics of each partial row.  fp32: its maximum (log2 units) and sum; fp16 dQ: -, scale
+  // statistics of each partial row.  fp32: its maximum (log2 units) and sum; fp16 forward: its
+  // log-sum-exp and the exponent that its values are to be multiplied by 2^ of; fp16 dQ: -, scale
   float2* ml;
-  // fp16 forward: log-sum-exp (log2 units), the exponent and the factor that its values are to be
-  // multiplied by (2^ of the one, times the other), -
-  float4* stat;
-  int* wide;             // [Bt * Hk][nb] whether a block's parts take store_wide (bf16)
+  // bf16, [Bt * Hk][nb]: not finite where a block is wide (its parts take store_wide), else, forward, the
+  // power of two that the parts of rows which see all of it are divided by; forward, [Bt * Hk][nb *
+  // block]: the power for rows that see the block up to this key
+  float* range;
+  signed char* key_range;
   float* delta;          // backward: sum of o * go per query row
   __nv_bfloat16* rest;   // [Bt, Hq, n, d] what the rounding of o left off, or null
   float* seg;            // backward: [chunk regions][seg_cap][2][block][d] sums of split blocks
@@ -104,8 +107,9 @@ __device__ __forceinline__ int q_start_of(const SelArgs& a, int b) {
 cudaError_t launch_key_means(const SelArgs& a, const int* kv_start, int max_new, float* means, cudaStream_t st);
 cudaError_t launch_select(const SelArgs& a, int* sel, cudaStream_t st);
 cudaError_t launch_lists(const SelArgs& a, cudaStream_t st);
-// a.wide from the blocks of v (whose sums the parts are), before the lists.
-cudaError_t launch_wide_blocks(const SelArgs& a, const View& v, cudaStream_t st);
+// a.range (forward: and a.key_range) from the blocks of V (backward: K), whose sums the parts are; before
+// the lists.
+cudaError_t launch_ranges(const SelArgs& a, bool backward, cudaStream_t st);
 // One chunk of `count` regions starting at region `first`.
 cudaError_t launch_selected_forward(const SelArgs& a, int first, int count, cudaStream_t st);
 cudaError_t launch_selected_backward(const SelArgs& a, int first, int count, cudaStream_t st);

@@ -109,7 +109,7 @@ constexpr size_t kPartialBytes = 1ull << 30;
 // status header).
 struct Plan {
   int regions, chunk;  // chunk: regions per launch
-  size_t slow, mean_parts, mean_norm2, wide, offs, list, inv, units, n_units, blk, part, ml, delta, seg, acc, total;
+  size_t slow, mean_parts, mean_norm2, range, key_range, offs, list, inv, units, n_units, blk, part, ml, delta, seg, acc, total;
 };
 
 Plan make_plan(SelArgs& a, bool backward) {
@@ -117,8 +117,7 @@ Plan make_plan(SelArgs& a, bool backward) {
   const long long subs = spr::ceil_div(a.n, spr::kSub);
   // the tensor-core kernels keep their partial rows in fp16
   const size_t val = a.f32 ? sizeof(float) : 2;
-  const size_t stats = a.f32 || backward ? sizeof(float2) : sizeof(float4);
-  const size_t row = val * a.d + stats;
+  const size_t row = val * a.d + sizeof(float2);
   const size_t sub_bytes = row * spr::kSub * a.top * a.group;
   // A region is cut where its partial rows pass the chunk.  A key block's gradient is then the sum of
   // its slices', which go one after the other and add to fp32 sums of the head (acc).
@@ -156,7 +155,8 @@ Plan make_plan(SelArgs& a, bool backward) {
   const size_t means = static_cast<size_t>(a.Bt) * a.Hk * a.nb;
   L.mean_parts = take(backward ? 0 : 2 * 2 * means * a.d);
   L.mean_norm2 = take(backward ? 0 : sizeof(float) * means);
-  L.wide = take(a.f32 ? 0 : sizeof(int) * means);
+  L.range = take(a.f32 ? 0 : sizeof(float) * means);
+  L.key_range = take(a.f32 || backward ? 0 : means * a.block);
   L.offs = take(sizeof(int) * R * a.nb * a.subs);
   L.list = take(sizeof(int) * R * entries);
   L.inv = take(sizeof(int) * static_cast<size_t>(a.Bt) * a.Hk * a.n * a.top);
@@ -164,7 +164,7 @@ Plan make_plan(SelArgs& a, bool backward) {
   L.n_units = take(sizeof(int) * R);
   L.blk = take(sizeof(int4) * R * a.nb);
   L.part = take(val * a.d * rows * L.chunk);
-  L.ml = take(backward && a.f32 ? 0 : stats * rows * L.chunk);
+  L.ml = take(backward && a.f32 ? 0 : sizeof(float2) * rows * L.chunk);
   L.delta = take(backward ? sizeof(float) * static_cast<size_t>(a.Bt) * a.Hq * a.n : 0);
   L.seg = take(sizeof(float) * 2 * a.block * a.d *
                (!backward ? 0 : a.f32 ? static_cast<size_t>(a.seg_cap) * L.chunk : 2 * size_t{spr::kTcShares}));
@@ -183,7 +183,8 @@ void bind(SelArgs& a, const Plan& L, void* ws) {
   a.slow = at<int>(ws, L.slow);
   a.mean_parts = at<char>(ws, L.mean_parts);
   a.mean_norm2 = at<float>(ws, L.mean_norm2);
-  a.wide = at<int>(ws, L.wide);
+  a.range = at<float>(ws, L.range);
+  a.key_range = at<signed char>(ws, L.key_range);
   a.offs = at<int>(ws, L.offs);
   a.list = at<int>(ws, L.list);
   a.inv = at<int>(ws, L.inv);
@@ -192,7 +193,6 @@ void bind(SelArgs& a, const Plan& L, void* ws) {
   a.blk = at<int4>(ws, L.blk);
   a.part = at<float>(ws, L.part);
   a.ml = at<float2>(ws, L.ml);
-  a.stat = at<float4>(ws, L.ml);
   a.delta = at<float>(ws, L.delta);
   a.seg = at<float>(ws, L.seg);
 }
@@ -296,7 +296,7 @@ int sparsepr_selected_attn(const sparsepr_selected* p, const sparsepr_view* Q, c
   bind(a, L, ws);
   a.q = view(Q), a.k = view(K), a.v = view(V), a.o = view(O), a.sel = sel, a.lse = lse;
   if (spr::use_decode(a)) return cuda_status(spr::launch_decode(a, st), "selected attention: few tokens");
-  if (!a.f32 && (rc = cuda_status(spr::launch_wide_blocks(a, a.v, st), "selected attention: ranges"))) return rc;
+  if (!a.f32 && (rc = cuda_status(spr::launch_ranges(a, false, st), "selected attention: ranges"))) return rc;
   if ((rc = cuda_status(spr::launch_lists(a, st), "selected attention: lists"))) return rc;
   for (int r = 0; r < L.regions; r += L.chunk)
     if ((rc = cuda_status(spr::launch_selected_forward(a, r, std::min(L.chunk, L.regions - r), st), "selected attention")))
@@ -326,7 +326,7 @@ int sparsepr_selected_attn_backward(const sparsepr_selected* p, const sparsepr_v
   a.gq = view(dQ), a.gk = view(dK), a.gv = view(dV);
   a.sel = sel, a.lse = const_cast<float*>(lse);
   if ((rc = cuda_status(spr::launch_delta(a, st), "selected attention backward: row sums"))) return rc;
-  if (!a.f32 && (rc = cuda_status(spr::launch_wide_blocks(a, a.k, st), "selected attention backward: ranges"))) return rc;
+  if (!a.f32 && (rc = cuda_status(spr::launch_ranges(a, true, st), "selected attention backward: ranges"))) return rc;
   if ((rc = cuda_status(spr::launch_lists(a, st), "selected attention backward: lists"))) return rc;
   a.acc = a.slices > 1 ? at<float>(ws, L.acc) : nullptr;
   for (int r = 0; r < L.regions; r += L.chunk) {

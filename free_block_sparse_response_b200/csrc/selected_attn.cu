@@ -134,8 +134,8 @@ __device__ __forceinline__ void mend_row(const SelArgs& a, int z, int t, int h, 
   }
 }
 
-// bf16: the rows that the joins listed, a CTA each: rows of blocks that are wide (wide_blocks_kernel) with a
-// value that fp16 cannot hold beside the row's largest, hidden NaNs and infinities among them.  (In the
+// bf16: the rows that the joins listed, a CTA each: rows of blocks that are wide (ranges_kernel) with a
+// value that fp16 cannot hold, hidden NaNs and infinities among them.  (In the
 // joins themselves, as in fp32, this would take twice their registers, and they live from the warps
 // under way.)
 constexpr int kMendWarps = 16;

@@ -225,8 +225,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lane0 = 32 * w4 + 16 * half;
         const uint32_t tRow = tDp + (static_cast<uint32_t>(lane0) << 16);
         float up[2];
-        if (un.wide) {
-          store_wide<D>(tRow, lane0 + q, un.rows, part + 32 * i, out0, up);
+        if (un.k != un.k) {
+          store_wide<D, false>(tRow, true, lane0 + q, un.rows, part + 32 * i, out0, up);
           if (half == 1) {
             tc::fence_before_sync();
             tc::mbar_arrive(bar(kDqFree));

@@ -209,13 +209,20 @@ __global__ void __launch_bounds__(512) scan_kernel(const SelArgs a) {
       }
     }
   }
-  for (int g = warp; g < a.nb; g += 16) {
-    const int4 k = s_blk[g];
-    const int rows = k.y * a.group, nu = ceil_div(rows, a.unit_rows);
-    for (int i = lane; i < nu; i += 32)
-      a.units[static_cast<size_t>(region) * a.unit_cap + k.w + i] =
-          Unit{g, k.x, i * a.unit_rows, min(a.unit_rows, rows - i * a.unit_rows), len - g * a.block, qs - g * a.block, b,
-               z % a.Hk, rows, a.f32 ? 0 : __ldg(a.wide + static_cast<size_t>(z) * a.nb + g), {}};
+  for (int g0 = warp; g0 < a.nb; g0 += 16 * 32) {
+    // (the ranges of the warp's next 32 blocks at once)
+    const int gl = g0 + 16 * lane;
+    const float ranges = a.f32 || gl >= a.nb ? 0.f : __ldg(a.range + static_cast<size_t>(z) * a.nb + gl);
+    for (int j = 0; j < 32 && g0 + 16 * j < a.nb; ++j) {
+      const int g = g0 + 16 * j;
+      const float range = __shfl_sync(0xffffffffu, ranges, j);
+      const int4 k = s_blk[g];
+      const int rows = k.y * a.group, nu = ceil_div(rows, a.unit_rows);
+      for (int i = lane; i < nu; i += 32)
+        a.units[static_cast<size_t>(region) * a.unit_cap + k.w + i] =
+            Unit{g, k.x, i * a.unit_rows, min(a.unit_rows, rows - i * a.unit_rows), len - g * a.block, qs - g * a.block, b,
+                 z % a.Hk, rows, range, {}};
+    }
   }
   if (threadIdx.x == 0) a.n_units[region] = unit0;
   if (threadIdx.x == 0 && region == 0) *a.slow = 0;

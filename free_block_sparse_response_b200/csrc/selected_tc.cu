@@ -4,20 +4,23 @@
 // query rows that selected it.  K and V of the block stay in shared memory; 128 rows at a time
 //   S = Q K^T (128 x B),  P = exp(S - row max),  O = P V (128 x D)
 // need no running maximum, since one tile holds all the keys of the row's part.  The part goes
-// out in fp16 with a power of two and its log-sum-exp; join_half_kernel adds a row's parts.  A
-// part's rounding, 2^-12, is 16 times finer than the result's bf16; fp32 parts would double the
-// traffic of the output and the join.  The power of two is the row's own (store_part), so that a row
-// is the same to the bit whatever the keys hold that it does not see.  Blocks of V that span too much for
-// fp16 (wide_blocks_kernel) are watched on their way out (store_wide), and what does not fit is
-// formed again from the inputs in fp32 (mend_kernel).
+// out in fp16, with its log-sum-exp; join_half_kernel adds a row's parts.  So that O needs no
+// scaling on its way out, P is formed as exp(S - row max) 2^-k: with |V| < 2^e over the keys that
+// the row sees in the block, k = e + log2 B - 15 keeps |O| <= 2^15, inside fp16, and leaves its 11 bits
+// to everything down to 2^-29 of that bound.  A part's rounding, 2^-12, is 16 times finer than the
+// result's bf16; fp32 parts would double the traffic of the output and the join.  Below 2^-29 a
+// part may lose 2^-40 of the bound (2^-33 of the largest |V|): blocks in which that could be much, or
+// that hold what is not finite, are wide (ranges_kernel).  Their parts are watched on the way out
+// (store_wide) and what does not fit is formed again from the inputs in fp32 (mend_kernel).  So nothing
+// that a row does not see reaches it: k is its own, and a hidden NaN makes one that is formed again.
 //
 // Work of a tile (B = D = 128): 8.4 MFLOP, 16K exponentials, 32 KB of Q gathered, 32 KB written.
-// A tile passes through five stages of ~1 us (gather, S, softmax, O, output), so one persistent
+// A tile passes through five stages of 1 to 2 us (gather, S, softmax, O, output), so one persistent
 // CTA per SM keeps five tiles in a ring of slots, each slot holding Q and then P of its tile, and
 // gives each stage warps of its own; tiles alternate between two streams (S and O in TMEM each):
 //   warps 0-7    softmax, one warpgroup a stream, one thread a row: maximum, then exponentials,
 //                reading S twice (a second read costs ~100 cycles, 128 held values spill);
-//   warps 8-11   output: O / l of each tile to memory;
+//   warps 8-11   output: O of each tile to memory;
 //   warps 12-15  gather Q rows through the block's list (16-byte asynchronous copies, 16 lanes a
 //                row, into the 128-byte swizzle), slots ahead of the products;
 //   warps 16-17  issue the products of one stream each: S of the stream's next tile as soon as
@@ -26,9 +29,11 @@
 //                (their P is 0, but 0 times what a cache holds there need not be).
 // All waits are bounded; on a timeout every role leaves, products and copies in flight drained.
 //
-// Bound by the stages' latencies and the tiles in flight (tensor pipe 31% active, HBM 53% of its
-// nominal rate).  16 heads x 32,760 tokens, 16 of 256 blocks, D 128: this kernel 850 us (0.55 TFLOP,
-// 650 TFLOP/s; 2.1 GB of parts out), join_half_kernel 475 us (2.3 GB, 4.8 TB/s), the lists 150 us.
+// Bound by the output warps, which drain every tile: 128 more instructions a tile there (a maximum and a
+// scale for each row) took the kernel from 820 to 850 us (tensor pipe 31% active, HBM 53% of its nominal
+// rate).  16 heads x 32,760 tokens, 16 of 256 blocks, D 128: this kernel 820 us, 1.85 us a tile (0.55
+// TFLOP, 670 TFLOP/s; 2.1 GB of parts out), join_half_kernel 487 us (2.3 GB, 4.7 TB/s), the lists 140
+// us, the ranges 31 us.
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cudaTypedefs.h>
@@ -49,7 +54,7 @@ constexpr float kInf = __builtin_huge_valf();
 constexpr int kThreads = 640, kLoaders = 128;
 constexpr int kRegSoftmax = 112, kRegOut = 136, kRegRest = 56;
 constexpr int kOutWarp = 8, kLoadWarp = 12, kMmaWarp = 16, kKvWarp = 18;
-constexpr float kRoom = 8.f;  // P is 2^-8 at most, so that O, 128 terms, stays below the largest |V|
+constexpr float kMostK = 60.f;  // P is not divided by more: its smallest weights would leave fp32
 
 template <int D, int B>
 struct Fwd {
@@ -146,6 +151,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         int nv = un.live;  // visible keys of this row in the block
         if (a.causal && row < un.rows)
           nv = min(nv, un.qs + __ldg(a.list + (first + ci) * cap + un.off + (un.r0 + row) / a.group) + 1);
+        const int whole = min(B, un.live);
+        float k = un.k;  // P is divided by 2^k; rows that see a part of the block go by that part
+        if (__any_sync(0xffffffffu, nv < whole) || !(k < kInf))
+          k = fminf(a.key_range[(static_cast<size_t>(un.b * a.Hk + un.kh) * a.nb + un.g) * B + max(min(nv, whole), 1) - 1], kMostK);
         if (!wait(kS + x, t >> 1)) return false;
         tc::fence_after_sync();
         const bool cut = __any_sync(0xffffffffu, nv < B);
@@ -158,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (cut) mask_from(s, nv - c0);
           max_into(mx, s);
         }
-        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2, shift = (m == -kInf ? 0.f : m) + kRoom;
+        const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale2, shift = (m == -kInf ? 0.f : m) + k;
         const uint64_t sc2 = f32x2(scale2, scale2), nm2 = f32x2(-shift, -shift);
         uint64_t sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
         const uint32_t sP = sSlot + (t % R) * F::kSlot;  // over Q, which S has read
@@ -188,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         f32x2_split(sum[1], l2, l3);
         const float l = (l0 + l1) + (l2 + l3);  // not above 0: no visible key (or a NaN, which stays one)
         if (row < un.rows)
-          *reinterpret_cast<float2*>(a.stat + (ci * cap + un.off) * a.group + un.r0 + row) =
+          a.ml[(ci * cap + un.off) * a.group + un.r0 + row] =
               l > 0.f || l != l ? make_float2(shift + __log2f(l), shift) : make_float2(-kInf, -kInf);
         return true;
     });
@@ -210,30 +219,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int half = 0; half < 2; ++half) {
           const int lane0 = 32 * w4 + 16 * half;
           const uint32_t tRow = tO + (static_cast<uint32_t>(lane0) << 16);
-          float up[2];
-          if (un.wide) {
-            store_wide<D>(tRow, lane0 + q, un.rows, part + 32 * i, out0, up);
-            if (half == 1) {
-              tc::fence_before_sync();
-              tc::mbar_arrive(bar(kOFree + x));
-            }
+          if (!(un.k < kInf)) {
+            float up[2];
+            store_wide<D, true>(tRow, un.k != un.k, lane0 + q, un.rows, part + 32 * i, out0, up);
           } else {
             uint32_t o[D / 2];
 #pragma unroll
             for (int c = 0; c < D; c += 64) tmem_ld_16x64(tRow + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c / 2]));
             tc::tmem_wait_ld();
-            if (half == 1) {
-              tc::fence_before_sync();
-              tc::mbar_arrive(bar(kOFree + x));
-            }
-            store_part<D>(o, lane0 + q, un.rows, part + 32 * i, out0, up);
-          }
-          if (i == 0) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              if (lane0 + q + 8 * k < un.rows) a.stat[out0 + lane0 + q + 8 * k].z = up[k];
+            store_part_as_is<D>(o, lane0 + q, un.rows, part + 32 * i, out0);
           }
         }
+        tc::fence_before_sync();
+        tc::mbar_arrive(bar(kOFree + x));
         return true;
     });
   } else if (warp < kMmaWarp) {
@@ -430,13 +428,7 @@ __global__ void __launch_bounds__(256, 6) join_half_kernel(const SelArgs a, int 
   float m = -kInf, l = 0.f, acc[8] = {};
   for (int j0 = 0; j0 < a.top; j0 += kPer) {
     const int e = live && j0 + ch < a.top ? __ldg(inv + j0 + ch) : -1;
-    float4 st = make_float4(-kInf, GRAD ? 0.f : -kInf, 0.f, 0.f);
-    if (e >= 0) {
-      if (GRAD)
-        st.y = __ldcs(a.ml + row0 + static_cast<size_t>(e) * a.group).y;
-      else
-        st = __ldcs(a.stat + row0 + static_cast<size_t>(e) * a.group);
-    }
+    const float2 st = e >= 0 ? __ldcs(a.ml + row0 + static_cast<size_t>(e) * a.group) : make_float2(-kInf, GRAD ? 0.f : -kInf);
     float f = st.y;
     if (!GRAD) {
       float mx = st.x;
@@ -446,7 +438,7 @@ __global__ void __launch_bounds__(256, 6) join_half_kernel(const SelArgs a, int 
       const float ms = mx == -kInf ? 0.f : mx, old = exp2f(m - ms), wt = exp2f(st.x - ms);
       m = mx;
       l = fmaf(l, old, wt);
-      f = exp2f(st.y - ms) * st.z;
+      f = exp2f(st.y - ms);
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] *= old;
     }
@@ -511,45 +503,113 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// Which blocks are wide: they hold a value that is not finite, or columns whose largest magnitudes'
-// exponents are more than 24 apart (columns of zeros aside).  What the parts of the others may lose, 2^-39
-// of a row's largest value, is at most 2^-14 of any column's largest.  One CTA a block, bound by
-// the read of the tensor.
-template <int D>
-__global__ void __launch_bounds__(256) wide_blocks_kernel(const SelArgs a, const View x) {
-  constexpr int L = D / 8, kRows = 256 / L;
+// A block's range, of its finite values.  Forward (V): k of the rows that see its keys up to each (SelArgs::
+// key_range), that of the whole block, and whether it is wide: it holds a value that is not finite, k
+// past what P takes (|V| about 2^-93 and 2^68), or rows or columns whose largest magnitudes' exponents are
+// more than 18 apart, so that the 2^-33 of the largest |V| that parts may lose are not below 2^-14 of a row's
+// or a column's largest (those of zeros aside).  Backward (K): dQ's parts have scales of their own and
+// lose 2^-39 of a row's largest; wide where columns are more than 24 apart or something is not
+// finite.  One CTA a block, bound by the read of the tensor.
+template <int D, bool BACKWARD>
+__global__ void __launch_bounds__(256) ranges_kernel(const SelArgs a, const View x) {
+  constexpr int L = D / 8, kRows = 256 / L, kPer = 128 / kRows;  // lanes a row, rows at a time, of a thread
   __shared__ uint4 s_mx[8][L];
+  __shared__ int s_row[128];
   const int g = blockIdx.x, kh = blockIdx.y, b = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = min(a.block, kv_len_of(a, b) - g * a.block), ch = threadIdx.x % L;
+  const int rows = min(a.block, kv_len_of(a, b) - g * a.block), ch = threadIdx.x % L, r0 = threadIdx.x / L;
+  const size_t at = (static_cast<size_t>(b) * a.Hk + kh) * a.nb + g;
   const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(x.p) + b * x.sb + kh * x.sh +
                            static_cast<long long>(g) * a.block * x.sn + ch * 8;
-  uint32_t mx[4] = {};  // by column
-  auto add = [&](const uint4& v) {
-    mx[0] = max_abs_bf16x2(mx[0], v.x), mx[1] = max_abs_bf16x2(mx[1], v.y);
-    mx[2] = max_abs_bf16x2(mx[2], v.z), mx[3] = max_abs_bf16x2(mx[3], v.w);
+  uint32_t mx[4];  // by column
+  auto finite_only = [](uint32_t w) {
+    return ((w & 0x7f80u) == 0x7f80u ? 0u : w & 0xffffu) | ((w & 0x7f800000u) == 0x7f800000u ? 0u : w & 0xffff0000u);
   };
-#pragma unroll 4
-  for (int r = threadIdx.x / L; r < rows; r += kRows) add(*reinterpret_cast<const uint4*>(p + r * x.sn));
+  int pass = 0;  // a second one without what is not finite, where there is such
+  for (;; ++pass) {
+    uint4 v[kPer];
 #pragma unroll
-  for (int o = L; o < 32; o <<= 1)
+    for (int i = 0; i < kPer; ++i)
+      v[i] = r0 + i * kRows < rows ? *reinterpret_cast<const uint4*>(p + (r0 + i * kRows) * x.sn) : make_uint4(0, 0, 0, 0);
+    uint32_t row[kPer];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) mx[w] = max_abs_bf16x2(mx[w], __shfl_xor_sync(0xffffffffu, mx[w], o));
-  if (lane < L) s_mx[warp][lane] = make_uint4(mx[0], mx[1], mx[2], mx[3]);
-  __syncthreads();
+    for (int w = 0; w < 4; ++w) mx[w] = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        if (pass > 0) u[w] = finite_only(u[w]);
+        mx[w] = max_abs_bf16x2(mx[w], u[w]);
+      }
+      row[i] = max_abs_bf16x2(max_abs_bf16x2(u[0], u[1]), max_abs_bf16x2(u[2], u[3]));
+    }
+    if (!BACKWARD) {
+#pragma unroll
+      for (int i = 0; i < kPer; i += 2) {  // two rows a word
+        uint32_t m = max_abs_bf16x2(__byte_perm(row[i], row[i + 1], 0x5410), __byte_perm(row[i], row[i + 1], 0x7632));
+#pragma unroll
+        for (int o = L / 2; o > 0; o >>= 1) m = max_abs_bf16x2(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (ch == 0) s_row[r0 + i * kRows] = m & 0x7fffu, s_row[r0 + (i + 1) * kRows] = m >> 16 & 0x7fffu;
+      }
+    }
+    bool finite = true;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+#pragma unroll
+      for (int o = L; o < 32; o <<= 1) mx[w] = max_abs_bf16x2(mx[w], __shfl_xor_sync(0xffffffffu, mx[w], o));
+      finite = finite && (mx[w] & 0x7f80u) != 0x7f80u && (mx[w] & 0x7f800000u) != 0x7f800000u;
+    }
+    if (lane < L) s_mx[warp][lane] = make_uint4(mx[0], mx[1], mx[2], mx[3]);
+    if (__syncthreads_and(finite) || pass > 0) break;
+  }
   if (warp > 0) return;
 #pragma unroll
-  for (int w = 1; w < 8; ++w) add(s_mx[w][ch]);
-  uint32_t top = 0, low = 0x7fffu;
+  for (int w = 1; w < 8; ++w) {
+    const uint4 v = s_mx[w][ch];
+    mx[0] = max_abs_bf16x2(mx[0], v.x), mx[1] = max_abs_bf16x2(mx[1], v.y);
+    mx[2] = max_abs_bf16x2(mx[2], v.z), mx[3] = max_abs_bf16x2(mx[3], v.w);
+  }
+  int top = 0, low = 0x7fff;  // magnitudes' bits: ordered as integers
 #pragma unroll
   for (int w = 0; w < 4; ++w)
 #pragma unroll
-    for (int k = 0; k < 32; k += 16) {
-      const uint32_t u = mx[w] >> k & 0x7fffu;
-      top = max(top, u);
-      if (u != 0) low = min(low, u);
+    for (int i = 0; i < 32; i += 16) {
+      const int m = static_cast<int>(mx[w] >> i & 0x7fffu);
+      top = max(top, m);
+      if (m != 0) low = min(low, m);
     }
-  top = __reduce_max_sync(0xffffffffu, top), low = __reduce_min_sync(0xffffffffu, low);
-  if (lane == 0) a.wide[(static_cast<size_t>(b) * a.Hk + kh) * a.nb + g] = top >= 0x7f80u || (top >> 7) > (low >> 7) + 24;
+  top = __reduce_max_sync(0xffffffffu, top);
+  float k = 0.f;
+  bool wide = pass > 0;
+  if (!BACKWARD) {
+    const int extra = (a.block == 128 ? 7 : 6) - 15;
+    // |V| < 2^((bits >> 7) - 126); zeros take any k
+    auto k_of = [&](int bits) { return bits == 0 ? 0 : max((bits >> 7) - 126 + extra, -100); };
+    const int per = a.block / 32;  // a lane's rows
+    int run = 0;                   // over the lanes before this one
+    for (int i = 0; i < per; ++i) {
+      const int r = lane * per + i, m = r < rows ? s_row[r] : 0;
+      run = max(run, m);
+      if (m != 0) low = min(low, m);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run = max(run, y);
+    }
+    run = __shfl_up_sync(0xffffffffu, run, 1);
+    if (lane == 0) run = 0;
+    for (int i = 0; i < per && lane * per + i < rows; ++i) {
+      run = max(run, s_row[lane * per + i]);
+      a.key_range[at * a.block + lane * per + i] = static_cast<signed char>(k_of(run));
+    }
+    k = static_cast<float>(k_of(top));
+    wide = wide || k > kMostK || (top != 0 && (top >> 7) - 126 + extra < -100);
+  }
+  low = __reduce_min_sync(0xffffffffu, low);
+  wide = wide || (top >> 7) > (low >> 7) + (BACKWARD ? 24 : 18);
+  // (infinite: P is divided by so much that a value of O may have become 0 by it)
+  if (lane == 0) a.range[at] = !wide ? k : k > 20.f ? kInf : __builtin_nanf("");
 }
 
 template <int D, int B>
@@ -572,9 +632,12 @@ cudaError_t forward(const SelArgs& a, int first, int count, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_wide_blocks(const SelArgs& a, const View& v, cudaStream_t st) {
+cudaError_t launch_ranges(const SelArgs& a, bool backward, cudaStream_t st) {
   const dim3 grid(a.nb, a.Hk, a.Bt);
-  a.d == 128 ? wide_blocks_kernel<128><<<grid, 256, 0, st>>>(a, v) : wide_blocks_kernel<64><<<grid, 256, 0, st>>>(a, v);
+  if (a.d == 128)
+    backward ? ranges_kernel<128, true><<<grid, 256, 0, st>>>(a, a.k) : ranges_kernel<128, false><<<grid, 256, 0, st>>>(a, a.v);
+  else
+    backward ? ranges_kernel<64, true><<<grid, 256, 0, st>>>(a, a.k) : ranges_kernel<64, false><<<grid, 256, 0, st>>>(a, a.v);
   return counted(cudaGetLastError(), 1);
 }
 

@@ -216,7 +216,7 @@ __device__ __forceinline__ bool each_tile(const SelArgs& a, int first, const int
     Unit un;
     un.g = get(rec.g), un.off = get(rec.off), un.r0 = get(rec.r0), un.rows = get(rec.rows), un.live = get(rec.live);
     un.qs = get(rec.qs), un.b = get(rec.b), un.kh = get(rec.kh), un.total = get(rec.total);
-    un.wide = get(rec.wide);
+    un.k = __int_as_float(get(__float_as_int(rec.k)));
     const bool closes = (ends >> src) & 1u;
     if (!f(un, get(rec_ci), t, u, opens, closes)) return false;
     opens = closes;
@@ -225,14 +225,12 @@ __device__ __forceinline__ bool each_tile(const SelArgs& a, int first, const int
   return true;
 }
 
-constexpr float kSmallestHalf = 0x1p-14f;  // the smallest normal fp16
-
 // Rows r and r + 8 of a tile, held by the quad's lanes as tmem_ld_16x64 leaves them (D / 2
 // registers), to the partial rows out0 + r of a chunk: fp16, the row's largest magnitude scaled to
 // [2^14, 2^15), so that 11 bits are left to everything down to 2^-29 of it and the rest is off by at
-// most 2^-39 of it; up[k] is the power of two that undoes it.  The scale is the row's own, so that what a row cannot see does not reach it.  The
-// two rows go side by side, since this is bound by its latencies.  `part` is the lane's 32 bytes
-// of row 0.  For blocks that are not wide (wide_blocks_kernel).
+// most 2^-39 of it; up[k] is the power of two that undoes it.  The two rows go side by side, since
+// this is bound by its latencies.  `part` is the lane's 32 bytes of row 0.  For blocks that are not
+// wide (ranges_kernel).
 template <int D>
 __device__ __forceinline__ void store_part(const uint32_t (&o)[D / 2], int r, int rows, uint8_t* part, long long out0,
                                            float (&up)[2]) {
@@ -269,30 +267,53 @@ __device__ __forceinline__ void store_part(const uint32_t (&o)[D / 2], int r, in
   }
 }
 
-// The same straight from TMEM for any values.  One that fp16 cannot hold beside the row's largest (smaller
-// than 2^-29 of it, infinite, or a NaN, as 0 times a hidden NaN is) goes out as a NaN, which the
-// row's sum keeps; mend_kernel then forms it again from the inputs.  Eight columns at a time, twice
-// (the largest first): ~10 us a tile, but small.  Wider or unrolled code here, though never run,
-// took the kernels from 850 to 880 us and more (16 heads x 32,760 tokens, 16 of 256 blocks).
+// The same without a scale: the values are inside fp16.
 template <int D>
-__device__ __forceinline__ void store_wide(uint32_t taddr, int r, int rows, uint8_t* part, long long out0, float (&up)[2]) {
-  float mx[2] = {}, g[2];
-  uint32_t o[4];
-#pragma unroll 1
-  for (int j = 0; j < D / 8; ++j) {
-    tmem_ld_16x8(taddr + 8 * j, o);
-    tc::tmem_wait_ld();
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const float x = fabsf(__uint_as_float(o[c]));
-      mx[c >> 1] = fmaxf(mx[c >> 1], x < __builtin_huge_valf() ? x : 0.f);
-    }
-  }
+__device__ __forceinline__ void store_part_as_is(const uint32_t (&o)[D / 2], int r, int rows, uint8_t* part,
+                                                 long long out0) {
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
-    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-    part_scale(mx[k], up[k], g[k]);
+    if (r + 8 * k >= rows) continue;
+#pragma unroll
+    for (int c = 0; c < D; c += 64) {
+      uint32_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const __half2 v = __floats2half2_rn(__uint_as_float(o[c / 2 + 4 * j + 2 * k]), __uint_as_float(o[c / 2 + 4 * j + 2 * k + 1]));
+        h[j] = *reinterpret_cast<const uint32_t*>(&v);
+      }
+      st_global_32(part + (out0 + r + 8 * k) * (2 * D) + c * 2, h);
+    }
+  }
+}
+
+// The parts of a wide block, straight from TMEM, without a scale (AS_IS) or with the rows' own.  A value that
+// fp16 cannot hold (below its normal range, and not a 0 where `zeros` are to be trusted, above it, or a
+// NaN, as 0 times a hidden NaN is) goes out as a NaN, which the row's sum keeps; mend_kernel then forms it again from the
+// inputs.  Eight columns at a time, twice with a scale: 5 and 10 us a tile, but small.  Wider or unrolled
+// code here, though never run, slowed the kernels by 3 to 30%.
+template <int D, bool AS_IS>
+__device__ __forceinline__ void store_wide(uint32_t taddr, bool zeros, int r, int rows, uint8_t* part, long long out0, float (&up)[2]) {
+  float g[2] = {1.f, 1.f};
+  uint32_t o[4];
+  if (!AS_IS) {
+    float mx[2] = {};
+#pragma unroll 1
+    for (int j = 0; j < D / 8; ++j) {
+      tmem_ld_16x8(taddr + 8 * j, o);
+      tc::tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float x = fabsf(__uint_as_float(o[c]));
+        mx[c >> 1] = fmaxf(mx[c >> 1], x < __builtin_huge_valf() ? x : 0.f);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+      mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+      part_scale(mx[k], up[k], g[k]);
+    }
   }
 #pragma unroll 1
   for (int j = 0; j < D / 8; ++j) {
@@ -304,8 +325,8 @@ __device__ __forceinline__ void store_wide(uint32_t taddr, int r, int rows, uint
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         const float x = __uint_as_float(o[2 * k + c]);
-        y[c] = x * g[k];
-        if (x != 0.f && !(fabsf(y[c]) >= 0x1p-14f && fabsf(y[c]) < 0x1p16f)) y[c] = __builtin_nanf("");
+        y[c] = AS_IS ? x : x * g[k];
+        if (!(fabsf(y[c]) >= 0x1p-14f && fabsf(y[c]) <= 0x1p15f) && !(zeros && x == 0.f)) y[c] = __builtin_nanf("");
       }
       if (r + 8 * k < rows)
         *reinterpret_cast<__half2*>(part + (out0 + r + 8 * k) * (2 * D) + (j >> 3) * 128 + (j & 7) * 4) =
