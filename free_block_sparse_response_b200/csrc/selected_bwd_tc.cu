@@ -459,10 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // dK and dV of the blocks that shares cut (their CTAs' sums, in order) and of blocks that no
-// query selected; `shares` CTAs ran the backward kernel.  A CTA looks at eight blocks of a
+// query selected (SLICES: sums added to a.acc); `shares` CTAs ran the backward kernel.  A CTA looks at eight blocks of a
 // region, a warp each (most were written already), then works on those left, four loads a
 // thread under way.
-template <int D>
+template <int D, bool SLICES>
 __global__ void __launch_bounds__(256) join_kv_tc_kernel(const SelArgs a, int first, int count, int shares) {
   __shared__ int s_c0[8], s_c1[8], s_slot[8];  // shares of the block (c0 > c1: none, -1: nothing to do), slot of c0
   const int ci = blockIdx.y, region = first + ci, z = region / a.slices, b = z / a.Hk, kh = z % a.Hk;
@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(256) join_kv_tc_kernel(const SelArgs a, int fi
     if (g0 + warp < a.nb) {
       const int4 bk = a.blk[static_cast<size_t>(region) * a.nb + g0 + warp];  // tiles, -, first tile of its region
       if (bk.x == 0) {
-        c0 = a.acc == nullptr ? 0 : -1;  // zeros
+        c0 = SLICES ? -1 : 0;  // zeros
       } else {
         const long long t0 = static_cast<long long>(before) + bk.z;
         auto share = [&](long long t) {
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(256) join_kv_tc_kernel(const SelArgs a, int fi
       for (int k = 0; k < kBatch; ++k) {
         const int i = i0 + k * 1024, j = g * a.block + i / D;
         if (i >= a.block * D || j >= a.nk) continue;
-        if (a.acc != nullptr) {
+        if (SLICES) {
           float4* v4 = reinterpret_cast<float4*>(a.acc + static_cast<size_t>(j) * D + i % D);
           float4* k4 = reinterpret_cast<float4*>(a.acc + (static_cast<size_t>(a.nk) + j) * D + i % D);
           const float4 v0 = *v4, k0 = *k4;
@@ -562,7 +562,9 @@ cudaError_t backward(const SelArgs& a, int first, int count, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   kern<<<kShares, kThreads, smem, st>>>(mk, mv, a, first, count);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
-  join_kv_tc_kernel<D><<<dim3(ceil_div(a.nb, 8), count), 256, 0, st>>>(a, first, count, kShares);
+  const dim3 grid(ceil_div(a.nb, 8), count);
+  a.acc == nullptr ? join_kv_tc_kernel<D, false><<<grid, 256, 0, st>>>(a, first, count, kShares)
+                   : join_kv_tc_kernel<D, true><<<grid, 256, 0, st>>>(a, first, count, kShares);
   if ((e = counted(cudaGetLastError(), 1)) != cudaSuccess) return e;
   return launch_join_half(a, first, count, true, st);
 }
