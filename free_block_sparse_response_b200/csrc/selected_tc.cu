@@ -54,7 +54,10 @@ constexpr float kInf = __builtin_huge_valf();
 constexpr int kThreads = 640, kLoaders = 128;
 constexpr int kRegSoftmax = 112, kRegOut = 136, kRegRest = 56;
 constexpr int kOutWarp = 8, kLoadWarp = 12, kMmaWarp = 16, kKvWarp = 18;
-constexpr float kMostK = 60.f;  // P is not divided by more: its smallest weights would leave fp32
+// P takes this much of a k, so that its smallest and largest weights stay inside fp32; the output the rest
+// (values above 2^68 or below 2^-93)
+constexpr float kLeastK = -100.f, kMostK = 60.f;
+__device__ __forceinline__ float p_share(float k) { return fminf(fmaxf(k, kLeastK), kMostK); }
 
 template <int D, int B>
 struct Fwd {
@@ -154,7 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int whole = min(B, un.live);
         float k = un.k;  // P is divided by 2^k; rows that see a part of the block go by that part
         if (__any_sync(0xffffffffu, nv < whole) || !(k < kInf))
-          k = fminf(a.key_range[(static_cast<size_t>(un.b * a.Hk + un.kh) * a.nb + un.g) * B + max(min(nv, whole), 1) - 1], kMostK);
+          k = a.key_range[(static_cast<size_t>(un.b * a.Hk + un.kh) * a.nb + un.g) * B + max(min(nv, whole), 1) - 1];
+        k = p_share(k);
         if (!wait(kS + x, t >> 1)) return false;
         tc::fence_after_sync();
         const bool cut = __any_sync(0xffffffffu, nv < B);
@@ -198,7 +202,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float l = (l0 + l1) + (l2 + l3);  // not above 0: no visible key (or a NaN, which stays one)
         if (row < un.rows)
           a.ml[(ci * cap + un.off) * a.group + un.r0 + row] =
-              l > 0.f || l != l ? make_float2(shift + __log2f(l), shift) : make_float2(-kInf, -kInf);
+              l > 0.f || l != l ? make_float2(shift + __log2f(l), shift + (un.k < kInf ? un.k - p_share(un.k) : 0.f))
+                                : make_float2(-kInf, -kInf);
         return true;
     });
   } else if (warp < kLoadWarp) {
@@ -227,6 +232,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < D; c += 64) tmem_ld_16x64(tRow + c, *reinterpret_cast<uint32_t(*)[32]>(&o[c / 2]));
             tc::tmem_wait_ld();
+            if (un.k != p_share(un.k)) {
+              const float f = exp2f(p_share(un.k) - un.k);
+#pragma unroll
+              for (int c = 0; c < D / 2; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * f);
+            }
             store_part_as_is<D>(o, lane0 + q, un.rows, part + 32 * i, out0);
           }
         }
@@ -504,10 +514,9 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
 }
 
 // A block's range, of its finite values.  Forward (V): k of the rows that see its keys up to each (SelArgs::
-// key_range), that of the whole block, and whether it is wide: it holds a value that is not finite, k
-// past what P takes (|V| about 2^-93 and 2^68), or rows or columns whose largest magnitudes' exponents are
-// more than 18 apart, so that the 2^-33 of the largest |V| that parts may lose are not below 2^-14 of a row's
-// or a column's largest (those of zeros aside).  Backward (K): dQ's parts have scales of their own and
+// key_range), that of the whole block, and whether it is wide: it holds a value that is not finite, or rows
+// or columns (those of zeros aside) whose largest magnitudes' exponents are more than 20 apart, so that the
+// 2^-33 of the largest |V| that parts may lose can be more than 2^-12 of a row's or a column's largest.  Backward (K): dQ's parts have scales of their own and
 // lose 2^-39 of a row's largest; wide where columns are more than 24 apart or something is not
 // finite.  One CTA a block, bound by the read of the tensor.
 template <int D, bool BACKWARD>
@@ -584,7 +593,7 @@ __global__ void __launch_bounds__(256) ranges_kernel(const SelArgs a, const View
   if (!BACKWARD) {
     const int extra = (a.block == 128 ? 7 : 6) - 15;
     // |V| < 2^((bits >> 7) - 126); zeros take any k
-    auto k_of = [&](int bits) { return bits == 0 ? 0 : max((bits >> 7) - 126 + extra, -100); };
+    auto k_of = [&](int bits) { return bits == 0 ? 0 : max((bits >> 7) - 126 + extra, -120); };
     const int per = a.block / 32;  // a lane's rows
     int run = 0;                   // over the lanes before this one
     for (int i = 0; i < per; ++i) {
@@ -604,10 +613,9 @@ __global__ void __launch_bounds__(256) ranges_kernel(const SelArgs a, const View
       a.key_range[at * a.block + lane * per + i] = static_cast<signed char>(k_of(run));
     }
     k = static_cast<float>(k_of(top));
-    wide = wide || k > kMostK || (top != 0 && (top >> 7) - 126 + extra < -100);
   }
   low = __reduce_min_sync(0xffffffffu, low);
-  wide = wide || (top >> 7) > (low >> 7) + (BACKWARD ? 24 : 18);
+  wide = wide || (top >> 7) > (low >> 7) + (BACKWARD ? 24 : 20);
   // (infinite: P is divided by so much that a value of O may have become 0 by it)
   if (lane == 0) a.range[at] = !wide ? k : k > 20.f ? kInf : __builtin_nanf("");
 }

@@ -177,6 +177,26 @@ def test_a_value_of_no_weight_leaves_the_others(size, n):
 
 
 @pytest.mark.parametrize("d,block", [(64, 64), (64, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("size", [1e-33, 1e-20, 1e16, 1e25])
+def test_causal_values_of_any_size(size, d, block):
+    """Rows that see a part of a block beside rows that see all of it, for values whose power of two the weights
+    take and for some past that; the first keys smaller than the others by up to 10^5."""
+    n = 300
+    q, k, v, lens, starts, cfg = problem((1, 4, 2, n, n, d, block, 3, True, 0, 1, None, BF), 98)
+    v = v.float() * size
+    v[:, :, :150] *= torch.logspace(-5, 0, 150, device=DEV)[:, None]
+    v = v.to(BF)
+    ws = spr.selected_workspace(q, k, cfg)
+    sel = spr.select_blocks(q, spr.key_means(k, block), n, cfg, ws)
+    out, lse = spr.selected_attn(q, k, v, sel, cfg, ws)
+    spr.check(ws)
+    want, wlse, p = R.attention(q, k, v, R.mask(sel, n, n, block, lens, starts, True), d ** -0.5)
+    wide = p @ v.double().abs().repeat_interleave(2, 1)
+    close(out, want, U[BF] * want.abs() + (U[BF] + E) * wide + 1e-38, "out")
+    close(lse, wlse, 1e-5 * (1 + wlse.abs()), "lse")
+
+
+@pytest.mark.parametrize("d,block", [(64, 64), (64, 128), (128, 64), (128, 128)])
 @pytest.mark.parametrize("size", [1e3, 1e8, 1e30])
 def test_one_large_key_column_leaves_the_gradients_of_others(size, d, block):
     """dq in the columns beside one of very large keys (where the queries hold zeros)."""
