@@ -21,7 +21,7 @@
 // Rows that leave more than 32 blocks open (equal keys, zero or non-finite queries) go to a
 // list that select_row_kernel works off, one CTA a row, all scores in 64 bits; it also takes
 // the calls of a few rows.  Bound by instructions (8 heads x 8,192 tokens: issue slots 61% busy,
-// tensor pipe 6%), step 2 the larger part: 271 us for 2 x 8 key heads x 16,383 tokens in groups of
+// tensor pipe 6%), step 2 the larger part: 276 us for 2 x 8 key heads x 16,383 tokens in groups of
 // 4, 128 blocks; the bytes would take 55.
 #include <cuda_runtime.h>
 

@@ -26,8 +26,8 @@
 //
 // P and dS are rounded to bf16 as operands: 2^-8 of each at most, with signs of their own, so that
 // dV and dK lose about as much again as their own rounding takes (2.3e-3 against 1.7e-3 in the norm).
-// Bound by the chain of the products and the softmax of one tile at a time (tensor pipe 26%
-// active): 16 heads x 32,760 tokens, 8 of 256 blocks, 1.29 ms, 530 TFLOP/s.
+// Bound by the chain of the products and the softmax of one tile at a time (tensor pipe 29%
+// active): 16 heads x 32,760 tokens, 8 of 256 blocks, 1.24 ms, 550 TFLOP/s.
 #include <cuda.h>
 #include <cuda_fp16.h>
 

@@ -3,8 +3,8 @@
 // Mathematics as in selected_attn.cu, without the detour over the blocks' lists: with a token
 // or a few per key head there is nothing to share a key tile with but the token's own group.
 // What bounds it: HBM, one read of the selected blocks' K and V; for a single sequence, latency.
-// 32 sequences x 8 key heads, 32 blocks of 64 keys: 268 MB in 52 us, 5.1 TB/s; one sequence, 16
-// blocks of 128: 9 us.
+// 32 sequences x 8 key heads, 32 blocks of 64 keys: 268 MB in 53 us, 5.1 TB/s; one sequence, 16
+// blocks of 128: 10 us.
 //
 // One cluster per (batch, key head, token, 16 query heads of the group); the keys of the
 // selected blocks are cut into pieces of 32, dealt to the cluster's warps.  A warp takes 16 keys
@@ -283,7 +283,9 @@ cudaError_t decode(const SelArgs& a, cudaStream_t st) {
 
 // Few tokens read the selected blocks once each and straight; the lists share a block's tile
 // between the tokens that selected it, at the price of five more launches and of tiles of 128 rows.
-// Direct up to 12 tokens, and while a block has at most three tokens on average (n top / nb).
+// Direct up to 12 tokens, and while a block has at most three tokens on average (n top / nb): where it won at
+// every head count tried.  The rule does not look at how many CTAs a call fills, so that it gives away
+// up to 1.6x where they are few (8 key heads, n = 16 .. 64 below); fp32 has no direct form.
 // Measured, direct and lists in us (replayed graphs; batch x key heads x group):
 //   1 x 8 x 4, d 128, 16 of 64 blocks of 128:  n = 1 9, 31;  8 15, 38;  16 24, 39;  32 39, 40
 //   8 x 8 x 1, d 128, 16 of 64 blocks of 128:  n = 1 18, 70;  8 84, 117;  12 119, 122;  16 154, 125

@@ -13,7 +13,7 @@
 // Bits make the order independent of the threads' timing: entries of a block ascend by token,
 // so every sum over a block's queries is formed in the same order in each run.  All three are
 // bound by latency, of memory and of the bits' atomics (the selection is 4 bytes per query and
-// slot, read four times): 16 heads x 32,760 tokens x 16 slots, 256 blocks, 43, 23 and 85 us.
+// slot, read four times): 16 heads x 32,760 tokens x 16 slots, 256 blocks, 42, 21 and 78 us.
 #include <cuda_runtime.h>
 
 #include "common.cuh"
