@@ -513,12 +513,14 @@ __device__ __forceinline__ uint32_t max_abs_bf16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
-// A block's range, of its finite values.  Forward (V): k of the rows that see its keys up to each (SelArgs::
-// key_range), that of the whole block, and whether it is wide: it holds a value that is not finite, or rows
-// or columns (those of zeros aside) whose largest magnitudes' exponents are more than 20 apart, so that the
-// 2^-33 of the largest |V| that parts may lose can be more than 2^-12 of a row's or a column's largest.  Backward (K): dQ's parts have scales of their own and
-// lose 2^-39 of a row's largest; wide where columns are more than 24 apart or something is not
-// finite.  One CTA a block, bound by the read of the tensor.
+// A block's range, of its finite values.  Forward (V): k of the rows that see its keys up to each
+// (SelArgs::key_range), that of the whole block, and whether it is wide: it holds a value that is not
+// finite, or rows or columns (those of zeros aside) whose largest magnitudes' exponents are more than 20
+// apart, so that the 2^-33 of the largest |V| that parts may lose can be more than 2^-12 of a row's or a
+// column's largest (8 apart where the output takes a share of the block's k, the same for rows with smaller
+// ones).  Backward (K): dQ's parts have scales of their own and lose 2^-39 of a row's largest; wide where
+// columns are more than 24 apart or something is not finite.  One CTA a block, bound by the read of
+// the tensor.
 template <int D, bool BACKWARD>
 __global__ void __launch_bounds__(256) ranges_kernel(const SelArgs a, const View x) {
   constexpr int L = D / 8, kRows = 256 / L, kPer = 128 / kRows;  // lanes a row, rows at a time, of a thread
@@ -615,7 +617,7 @@ __global__ void __launch_bounds__(256) ranges_kernel(const SelArgs a, const View
     k = static_cast<float>(k_of(top));
   }
   low = __reduce_min_sync(0xffffffffu, low);
-  wide = wide || (top >> 7) > (low >> 7) + (BACKWARD ? 24 : 20);
+  wide = wide || (top >> 7) > (low >> 7) + (BACKWARD ? 24 : k == p_share(k) ? 20 : 8);
   // (infinite: P is divided by so much that a value of O may have become 0 by it)
   if (lane == 0) a.range[at] = !wide ? k : k > 20.f ? kInf : __builtin_nanf("");
 }

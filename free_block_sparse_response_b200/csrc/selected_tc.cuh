@@ -287,13 +287,14 @@ __device__ __forceinline__ void store_part_as_is(const uint32_t (&o)[D / 2], int
   }
 }
 
-// The parts of a wide block, straight from TMEM, without a scale (AS_IS) or with the rows' own.  A value that
-// fp16 cannot hold (below its normal range, and not a 0 where `zeros` are to be trusted, above it, or a
-// NaN, as 0 times a hidden NaN is) goes out as a NaN, which the row's sum keeps; mend_kernel then forms it again from the
-// inputs.  Eight columns at a time, twice with a scale: 5 and 10 us a tile, but small.  Wider or unrolled
-// code here, though never run, slowed the kernels by 3 to 30%.
+// The parts of a wide block, straight from TMEM, without a scale (AS_IS) or with the rows' own.  A value
+// that fp16 cannot hold goes out as a NaN: one below its normal range (but a 0 where `zeros` are to be
+// trusted), above it, or a NaN, as 0 times a hidden NaN is.  The row's sum keeps it, and mend_kernel then forms
+// it again from the inputs.  Eight columns at a time, twice with a scale: 5 and 10 us a tile, but small.
+// Wider or unrolled code here, though never run, slowed the kernels by 3 to 30%.
 template <int D, bool AS_IS>
-__device__ __forceinline__ void store_wide(uint32_t taddr, bool zeros, int r, int rows, uint8_t* part, long long out0, float (&up)[2]) {
+__device__ __forceinline__ void store_wide(uint32_t taddr, bool zeros, int r, int rows, uint8_t* part, long long out0,
+                                           float (&up)[2]) {
   float g[2] = {1.f, 1.f};
   uint32_t o[4];
   if (!AS_IS) {

@@ -403,7 +403,8 @@ SPARSEPR_API int sparsepr_select_blocks(const sparsepr_selected* p, const sparse
  * O [Bt,Hq,Nq,d] in dtype, lse [Bt,Hq,Nq] fp32 natural log-sum-exp; a query without keys
  * gets a zero row and -inf.  sel rows ascend and end at their first negative entry; an entry
  * that does not ascend or is past the last block is skipped and records
- * SPARSEPR_ERR_INVALID_ARG in the status word. */
+ * SPARSEPR_ERR_INVALID_ARG in the status word.  Weighted sums of V run before the division by their
+ * weights: |V| times the number of selected keys must stay inside fp32. */
 SPARSEPR_API int sparsepr_selected_attn(const sparsepr_selected* p, const sparsepr_view* Q, const sparsepr_view* K,
                                         const sparsepr_view* V, const int32_t* sel, const sparsepr_view* O, float* lse,
                                         void* ws, sparsepr_stream_t stream);
